@@ -1,0 +1,122 @@
+// kv.h -- launch interface between the entry points (kv_entry.hip) and the
+// gfx950 kernels of the 4-bit key/value cache.  Internal to the library.
+#ifndef LW_KV_H
+#define LW_KV_H
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "lw.h"
+
+// A cache and a batch as the kernels see them: passed by value, so every
+// field is uniform.
+struct KvGeom {
+    uint8_t *pages;
+    const int32_t *start;        // [n_seqs + 1]
+    const int32_t *lens;         // [n_seqs]
+    const int32_t *table;        // [n_seqs][stride]
+    int64_t n_pages, stride;
+    int64_t page_bytes;          // kv_heads * block_bytes
+    int32_t block_bytes;         // one head's part of a page: page_tokens * (head_dim + 8)
+    int32_t n_seqs, n_tokens, kv_heads;
+    int32_t page_shift;          // log2(page_tokens)
+};
+
+// One packed tensor [n_tokens][heads][head_dim]; strides in elements.
+struct KvTensor {
+    void *data;
+    int64_t token, head;
+    int32_t wide;                // 1: every 8-element group is 16-byte aligned
+};
+
+struct KvAttend {
+    KvGeom g;
+    KvTensor q, out;
+    float *lse;                  // [n_tokens][q_heads], or null
+    float *part;                 // split partials (see kv_attend.hip), or null
+    int32_t group;               // query heads per kv head
+    int32_t causal, window;      // window 0: none
+    int32_t splits, chunk;       // token chunks per row tile, tokens per chunk
+    float scale;                 // > 0
+};
+
+// How a call is cut up: rows per tile, row tiles, splits and chunk.
+struct KvPlan {
+    int tile;
+    int64_t tiles;
+    int splits, chunk;
+    size_t work_bytes;
+};
+
+KvPlan lw_kv_plan(int head_dim, int kv_heads, int group, int64_t n_seqs, int64_t n_tokens, int64_t max_len,
+                  int window, int most);
+
+hipError_t lw_launch_kv_append(const KvGeom &g, int head_dim, const KvTensor &k, const KvTensor &v, int dtype,
+                               hipStream_t s);
+hipError_t lw_launch_kv_read(const KvGeom &g, int head_dim, const KvTensor &k, const KvTensor &v, int dtype,
+                             hipStream_t s);
+hipError_t lw_launch_kv_attend(const KvAttend &a, int head_dim, int dtype, const KvPlan &p, hipStream_t s);
+
+#ifdef __HIPCC__
+// ------------------------------------------------------------ device helpers
+
+// The cached token of a packed row: its sequence, position and page.
+struct KvPlace {
+    int32_t seq, pos;            // seq < 0: the row belongs to no sequence
+    int64_t page;                // < 0: the token is absent
+};
+
+// Number of entries of bound(s), s = 0..n-1, that are <= x, for a bound that
+// does not decrease: the wavefront's 64 lanes look at 64 entries at a time
+// (one load latency where a binary search has one for each halving).
+template <class F>
+__device__ __forceinline__ int kv_count_le(int n, int x, F bound)
+{
+    const int lane = threadIdx.x & 63;
+    int found = 0;
+    for (int s = 0; s < n; s += 64) {
+        const bool le = s + lane < n && bound(s + lane) <= x;
+        const int c = __popcll(__ballot(le));
+        found += c;
+        if (c < 64) break;
+    }
+    return found;
+}
+
+// First and one-past-last packed row of a sequence, kept inside the tensor
+// whatever the caller's array holds.
+__device__ __forceinline__ int2 kv_rows(const KvGeom &g, int seq)
+{
+    const int a = min(max(g.start[seq], 0), g.n_tokens);
+    const int b = min(max(g.start[seq + 1], a), g.n_tokens);
+    return make_int2(a, b);
+}
+
+__device__ __forceinline__ int64_t kv_page(const KvGeom &g, int seq, int pos)
+{
+    const int64_t i = pos >> g.page_shift;
+    if (pos < 0 || i >= g.stride) return -1;
+    const int64_t p = g.table[(int64_t)seq * g.stride + i];
+    return p < g.n_pages ? p : -1;           // a negative entry stays negative
+}
+
+// Word index, inside a head's block, of word w of token t's keys and values.
+// Keys: tiles of 16 tokens, each a [unit][token] array of units of W words,
+// so that the 64 lanes that hold a matrix instruction's 16 tokens x 4 parts
+// read consecutive units.  Values: [token / 4][word][token % 4], so that one
+// 16-byte load gives a lane four tokens of the same eight dimensions.
+template <int D>
+__device__ __forceinline__ int kv_kword(int t, int w)
+{
+    constexpr int W = D >= 128 ? 4 : D / 32, U = D / 8 / W;
+    return (((t >> 4) * U + w / W) * 16 + (t & 15)) * W + w % W;
+}
+
+template <int D>
+__device__ __forceinline__ int kv_vword(int t, int w)
+{
+    return ((t >> 2) * (D / 8) + w) * 4 + (t & 3);
+}
+#endif
+
+#endif

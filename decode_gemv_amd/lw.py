@@ -24,6 +24,7 @@ LW_PIPE_FUSED, LW_PIPE_FULL_DECODE, LW_PIPE_EXPONENT, LW_PIPE_PALETTE, LW_PIPE_D
 LW_FORM_PALETTE, LW_FORM_EXPONENT = 0, 1
 LW_CODE_HUFFMAN, LW_CODE_COMPACT, LW_CODE_LENS = 0, 1, 2
 LW_RECON_VARIANTS = 5
+LW_F16, LW_BF16, LW_F32 = range(3)
 (LW_REG_TABLE, LW_REG_GPUTAB, LW_REG_TILE_OFF, LW_REG_WORDS, LW_REG_DM, LW_REG_PALETTE, LW_REG_SM,
  LW_REG_VB_BITS, LW_REG_VB_START, LW_REG_VERBATIM, LW_REG_SPLIT, LW_REG_WORK, LW_REG_COUNT) = range(13)
 
@@ -47,6 +48,20 @@ class lw_bundle_info(C.Structure):
 
 class lw_build_opts(C.Structure):
     _fields_ = [("code", C.c_int32), ("parts", C.c_int32), ("lens", C.c_void_p)]
+
+
+class lw_kv_cache(C.Structure):
+    _fields_ = [("pages", C.c_void_p), ("n_pages", C.c_int64), ("kv_heads", C.c_int32), ("head_dim", C.c_int32),
+                ("page_tokens", C.c_int32)]
+
+
+class lw_kv_batch(C.Structure):
+    _fields_ = [("n_seqs", C.c_int64), ("start", C.c_void_p), ("lens", C.c_void_p), ("table", C.c_void_p),
+                ("table_stride", C.c_int64), ("max_len", C.c_int64)]
+
+
+class lw_kv_tensor(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
 
 
 def _load():
@@ -94,6 +109,11 @@ def _load():
         "lw_pipeline_get": (st, [P, i32, C.POINTER(C.c_int)]),
         "lw_gemm": (st, [P, P, P, i32, P, C.c_size_t, P]),
         "lw_autotune": (st, [P, P, i32, P, C.c_size_t, P, P, i32, P, P]),
+        "lw_kv_page_bytes": (C.c_size_t, [i32, i32, i32]),
+        "lw_kv_append": (st, [P, P, i64, P, P, i32, P]),
+        "lw_kv_read": (st, [P, P, i64, P, P, i32, P]),
+        "lw_kv_attend": (st, [P, P, i64, P, P, i32, i32, C.c_float, i32, i32, P, P, C.c_size_t, P]),
+        "lw_kv_attend_scratch_bytes": (C.c_size_t, [P, P, i64, i32]),
         "lw_status_str": (C.c_char_p, [st]),
         "lw_last_error": (C.c_char_p, []),
     }
@@ -460,6 +480,109 @@ def lw_swiglu(gate, up, h, stream=None) -> None:
     if up.numel() != n or h.numel() != n:
         raise LwError(LW_E_ARG, "gate, up and h must have the same number of elements")
     _check(_L.lw_swiglu(_dptr(gate, "gate"), _dptr(up, "up"), _dptr(h, "h"), n, _stream(stream)))
+
+
+# ---------------------------------------------------------------- key/value cache
+
+def lw_kv_page_bytes(kv_heads: int, head_dim: int, page_tokens: int) -> int:
+    """Bytes of one page of a 4-bit key/value cache (0: not supported)."""
+    return int(_L.lw_kv_page_bytes(kv_heads, head_dim, page_tokens))
+
+
+class KvCache:
+    """A 4-bit key/value cache: `pages` is a device uint8 tensor of whole pages."""
+
+    def __init__(self, pages, kv_heads: int, head_dim: int, page_tokens: int):
+        size = lw_kv_page_bytes(kv_heads, head_dim, page_tokens)
+        if not size:
+            raise LwError(LW_E_UNSUPPORTED, "kv_heads must be in 1..1024, head_dim 64, 128 or 256 and page_tokens 32, 64, "
+                                            "128 or 256")
+        p = _dptr(pages, "pages")
+        n = pages.numel() * pages.element_size()
+        if n % size:
+            raise LwError(LW_E_ARG, f"pages must hold whole pages of {size} bytes")
+        self.pages, self.n_pages = pages, n // size
+        self.kv_heads, self.head_dim, self.page_tokens = kv_heads, head_dim, page_tokens
+        self.desc = lw_kv_cache(p, n // size, kv_heads, head_dim, page_tokens)
+        self.ref = C.byref(self.desc)
+
+
+class KvBatch:
+    """The sequences of a call: device int32 tensors start [n + 1], lens [n] and table [n][pages].  The tensors
+    may be changed in place between calls; max_len is the longest sequence to plan for (0: what the table holds)."""
+
+    def __init__(self, start, lens, table, max_len: int = 0):
+        import torch
+        ps, pl, pt = _dptr(start, "start"), _dptr(lens, "lens"), _dptr(table, "table")
+        if any(t.dtype != torch.int32 for t in (start, lens, table)):
+            raise LwError(LW_E_ARG, "start, lens and table must be int32")
+        n = lens.numel()
+        if start.numel() != n + 1 or table.dim() != 2 or table.shape[0] != n:
+            raise LwError(LW_E_ARG, "start must hold one entry more than lens, table one row for each")
+        self.start, self.lens, self.table = start, lens, table
+        self.desc = lw_kv_batch(n, ps, pl, pt, table.shape[1], max_len)
+        self.ref = C.byref(self.desc)
+
+
+_KV_TYPES = {}
+
+
+def _kv_tensor(t, what: str, heads: int, cache: KvCache):
+    """(descriptor, dtype) of a packed device tensor [n][heads][head_dim] with any row and head strides."""
+    import torch
+    if not _KV_TYPES:
+        _KV_TYPES.update({torch.float16: LW_F16, torch.bfloat16: LW_BF16, torch.float32: LW_F32})
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3:
+        raise LwError(LW_E_ARG, f"{what} must be a device tensor [tokens][heads][head_dim]")
+    if t.shape[1] != heads or t.shape[2] != cache.head_dim:
+        raise LwError(LW_E_ARG, f"{what} must be [tokens][{heads}][{cache.head_dim}]")
+    s0, s1, s2 = t.stride()
+    if s2 != 1:
+        raise LwError(LW_E_ARG, f"{what} must have its head vectors contiguous")
+    kind = _KV_TYPES.get(t.dtype)
+    if kind is None:
+        raise LwError(LW_E_ARG, f"{what} must be fp16, bf16 or fp32")
+    return lw_kv_tensor(t.data_ptr(), s0, s1), kind
+
+
+def _kv_pair(cache, a, b, names, heads):
+    ta, ka = _kv_tensor(a, names[0], heads, cache)
+    tb, kb = _kv_tensor(b, names[1], heads, cache)
+    if ka != kb or a.shape[0] != b.shape[0]:
+        raise LwError(LW_E_ARG, f"{names[0]} and {names[1]} must have the same rows and type")
+    return C.byref(ta), C.byref(tb), ka, a.shape[0]
+
+
+def lw_kv_append(cache: KvCache, batch: KvBatch, k, v, stream=None) -> None:
+    """Quantise the new tokens' keys and values [n][kv_heads][head_dim] into the cache."""
+    tk, tv, kind, n = _kv_pair(cache, k, v, ("k", "v"), cache.kv_heads)
+    _check(_L.lw_kv_append(cache.ref, batch.ref, n, tk, tv, kind, _stream(stream)))
+
+
+def lw_kv_read(cache: KvCache, batch: KvBatch, k, v, stream=None) -> None:
+    """Dequantise the batch's tokens into k and v [n][kv_heads][head_dim]."""
+    tk, tv, kind, n = _kv_pair(cache, k, v, ("k", "v"), cache.kv_heads)
+    _check(_L.lw_kv_read(cache.ref, batch.ref, n, tk, tv, kind, _stream(stream)))
+
+
+def lw_kv_attend_scratch_bytes(cache: KvCache, batch: KvBatch, n_tokens: int, q_heads: int) -> int:
+    return int(_L.lw_kv_attend_scratch_bytes(cache.ref, batch.ref, n_tokens, q_heads))
+
+
+def lw_kv_attend(cache: KvCache, batch: KvBatch, q, out, scale: float | None = None, causal: bool = True,
+                 window: int = 0, lse=None, work=None, stream=None) -> None:
+    """out = attention of q [n][q_heads][head_dim] over the cache; scale None: head_dim ** -0.5."""
+    heads = q.shape[1] if getattr(q, "ndim", 0) == 3 else 0
+    tq, to, kind, n = _kv_pair(cache, q, out, ("q", "out"), heads)
+    pl = None
+    if lse is not None:
+        pl = _dptr(lse, "lse")
+        if lse.numel() != n * heads or lse.element_size() != 4:
+            raise LwError(LW_E_ARG, "lse must be fp32 [tokens][q_heads]")
+    wp, wn = _wbuf(work) if work is not None and work.numel() else (None, 0)
+    _check(_L.lw_kv_attend(cache.ref, batch.ref, n, tq, to, kind, heads,
+                           cache.head_dim ** -0.5 if scale is None else scale, int(causal), int(window), pl, wp, wn,
+                           _stream(stream)))
 
 
 # ---------------------------------------------------------------- conveniences

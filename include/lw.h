@@ -399,6 +399,111 @@ lw_status lw_rans_decode(int kind, int64_t rows, int64_t cols, int halves, const
  * Errors: LW_E_ARG (n < 0, or a null pointer with n > 0), LW_E_DEVICE. */
 lw_status lw_swiglu(const float *gate, const float *up, uint16_t *h, int64_t n, void *stream);
 
+/* ---------------------------------------------------------------- key/value cache */
+/* A paged key/value cache held in 4 bits, and the attention that reads it:
+ * past some context length the bytes of the cache overtake those of the
+ * weights ("Software-Defined Bandwidth Expansion", the context wall
+ * C* = P b / (8 kappa f)), and the cache is then what coding has to shrink.
+ *
+ * One key or value head vector x[0..D) is held as 4-bit codes q and an fp16
+ * pair (d, m), worth d q - m (the dequantisation rule of the weights):
+ *   m = fp16(-min x), d = fp16((max x - min x) / 15), kept within +-65504,
+ *   q = clamp(rint((x + m) (1/d)), 0, 15), 0 where d = 0, in fp32
+ * and a vector with a NaN or an infinity has d = m = NaN (it reads back as
+ * NaN): D/2 + 4 bytes a vector, 4.25 bits an element at D = 128.
+ *
+ * A page holds page_tokens tokens of every kv head, P below; page p starts at
+ * p * lw_kv_page_bytes, and head h's part, P*(D + 8) bytes, at h*P*(D + 8) in
+ * it: P*D/2 bytes of key codes, P*D/2 of value codes, P words d | m << 16 of
+ * the keys and P of the values.  A 32-bit word holds the codes of eight
+ * dimensions, the lowest in the low nibble; word w of token t is at word
+ *   keys  : ((t/16 * U + w/W) * 16 + t%16) * W + w%W, W = min(4, D/32), U = D/8/W
+ *   values: (t/4 * (D/8) + w) * 4 + t%4
+ * The memory needs no initialisation: what holds no token is not looked at. */
+typedef enum { LW_F16 = 0, LW_BF16 = 1, LW_F32 = 2 } lw_dtype;
+
+typedef struct {
+    void *pages;               /* device, 16-byte aligned, n_pages * lw_kv_page_bytes bytes */
+    int64_t n_pages;
+    int32_t kv_heads;          /* 1..1024 */
+    int32_t head_dim;          /* D: 64, 128 or 256 */
+    int32_t page_tokens;       /* P: 32, 64, 128 or 256 */
+} lw_kv_cache;
+
+/* The sequences of a call.  Their new tokens are packed back to back: rows
+ * start[s] .. start[s+1] - 1 of the tensors are sequence s's, and they are
+ * the last of its lens[s] tokens (row i of n at position lens[s] - n + i).
+ * table[s*table_stride + j] is the page of positions j*P .. j*P + P - 1.
+ * start must not decrease.  The arrays are read on the device, so a captured
+ * call follows their contents.  A token whose position is negative or past
+ * the table, or whose page number is outside 0..n_pages - 1 (such as -1, a
+ * page given up), is absent: not written, read back as zeros, seen by no row.
+ * Rows before start[0] and from start[n_seqs] on belong to no sequence and
+ * are left as they are. */
+typedef struct {
+    int64_t n_seqs;            /* 0 does nothing */
+    const int32_t *start;      /* device [n_seqs + 1] */
+    const int32_t *lens;       /* device [n_seqs], new tokens included */
+    const int32_t *table;      /* device [n_seqs][table_stride] */
+    int64_t table_stride;      /* entries per sequence */
+    int64_t max_len;           /* the largest lens[s] to plan for (0: table_stride * P); a longer sequence
+                                  is still served in full, only cut up less finely */
+} lw_kv_batch;
+
+/* A packed tensor [n_tokens][heads][D]: element (i, h, e) at
+ * i*token_stride + h*head_stride + e of data, strides in elements and not
+ * negative (a slice of a fused projection output will do).  Any alignment of
+ * the element type; 16-byte aligned head vectors take wide accesses. */
+typedef struct {
+    void *data;
+    int64_t token_stride, head_stride;
+} lw_kv_tensor;
+
+/* Bytes of one page, or 0 where the cache kind is not supported. */
+size_t lw_kv_page_bytes(int kv_heads, int head_dim, int page_tokens);
+
+/* Quantise the new tokens' keys and values (n_tokens rows of k and v,
+ * dtype LW_F16, LW_BF16 or LW_F32) into the cache.  No two rows may name the
+ * same place of a page (sequences that share a page do so in tokens that are
+ * not new).  Errors: LW_E_ARG, LW_E_UNSUPPORTED (head_dim, page_tokens),
+ * LW_E_DEVICE. */
+lw_status lw_kv_append(const lw_kv_cache *cache, const lw_kv_batch *batch, int64_t n_tokens, const lw_kv_tensor *k,
+                       const lw_kv_tensor *v, int dtype, void *stream);
+
+/* Dequantise the same tokens from the cache into k and v (with a batch whose
+ * rows cover whole sequences: the sequences).  d q - m is rounded once to
+ * dtype.  Errors: as lw_kv_append. */
+lw_status lw_kv_read(const lw_kv_cache *cache, const lw_kv_batch *batch, int64_t n_tokens, const lw_kv_tensor *k,
+                     const lw_kv_tensor *v, int dtype, void *stream);
+
+/* Attention of the new tokens over the cache (whose entries for them
+ * lw_kv_append has made): for query head h of a row, over the tokens j it
+ * sees and kv head h / (q_heads / kv_heads),
+ *   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q.k_j)
+ * A row at position p sees the tokens that are present with j <= p (causal)
+ * or all of the sequence's (causal 0), and with window w > 0 only j > p - w.
+ * A row that sees none gives zeros.
+ *   q, out  : [n_tokens][q_heads][D], dtype LW_F16 or LW_BF16 both
+ *   lse     : fp32 [n_tokens][q_heads] receiving log sum_j p_j (-infinity
+ *             where no token is seen), or NULL
+ *   scale   : > 0 and finite
+ *   work    : device, 16-byte aligned, lw_kv_attend_scratch_bytes bytes
+ *             (NULL/0 where that is 0), contents not kept between calls; a
+ *             smaller one lowers the number of chunks that a sequence is cut
+ *             into, and LW_E_ARG is given only for a misaligned one
+ * Scores, sums and the output's accumulation are fp32, p times a value's d
+ * is rounded to fp16; sums run in a fixed order: results are deterministic.
+ * Errors: LW_E_ARG, LW_E_UNSUPPORTED (head_dim, page_tokens, dtype),
+ * LW_E_DEVICE. */
+lw_status lw_kv_attend(const lw_kv_cache *cache, const lw_kv_batch *batch, int64_t n_tokens, const lw_kv_tensor *q,
+                       const lw_kv_tensor *out, int dtype, int q_heads, float scale, int causal, int window,
+                       float *lse, void *work, size_t work_bytes, void *stream);
+
+/* Bytes of work with which lw_kv_attend cuts long sequences as finely as it
+ * would like to, for batches of up to that many sequences, rows and max_len
+ * (0 where one chunk a sequence does, or for arguments that it refuses). */
+size_t lw_kv_attend_scratch_bytes(const lw_kv_cache *cache, const lw_kv_batch *batch, int64_t n_tokens, int q_heads);
+
 /* ---------------------------------------------------------------- pipelines */
 /* "Unweight", sections "Four approaches to using compressed weights" and
  * "Why no single pipeline wins": full decode rebuilds every bf16 weight in
