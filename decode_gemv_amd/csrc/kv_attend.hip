@@ -38,6 +38,7 @@
 // multiplies the centred code, so the output's error from it is a random
 // 2^-12 of the centred part; scores, maxima, sums and outputs are fp32.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv.h"
 
@@ -51,10 +52,9 @@ typedef float f16v __attribute__((ext_vector_type(16)));
 constexpr int NW = 4;                  // wavefronts of a workgroup
 constexpr int STEP = 32;               // tokens of a wavefront's step
 constexpr float NONE = -1e30f;         // log2 of "nothing seen yet"
-constexpr float SLACK = 6.0f;          // log2 of how far p may exceed the reference before rescaling
 
 // Wavefronts a SIMD is to hold (the registers that leaves).
-template <int D, int TILE> constexpr int WAVES = D * TILE <= 2048 ? 2 : 1;
+template <int D, int TILE> constexpr int WAVES = D * TILE <= 2048 && TILE == 16 ? 3 : D * TILE <= 4096 ? 2 : 1;
 
 template <int TILE> struct Mma;
 template <> struct Mma<16> {           // 16 x 16 x 32: lane = row/column l % 16, 8 of the 32 at 8 * (l / 16)
@@ -160,34 +160,56 @@ __device__ __forceinline__ Span chunk_of(const KvAttend &a, const RowTile &t, in
     return s;
 }
 
-// What is loaded of 32 tokens: key words, value words, and the pairs of the
-// tokens whose scores the lane will hold (groups of four).
+// What a lane holds of 32 tokens: key words and value words, and the pairs of
+// the tokens whose scores it will have (groups of four).
 template <int D, int TILE>
-struct Tokens {
-    static constexpr int KW = D * STEP / 8 / 64;             // key words a lane holds
-    static constexpr int REPS = D / 8 > TILE ? D / 8 / TILE : 1;
-    static constexpr int TG = STEP / 4 / Mma<TILE>::GROUPS;  // token groups of a lane
-    uint32_t k[KW];
-    uint4 v[TG][REPS];
-    uint4 dk[TG], dv[TG];
+struct Shape {
+    static constexpr int G = Mma<TILE>::GROUPS;
+    static constexpr int SUB = STEP / TILE;                  // token tiles of a step (2 or 1)
+    static constexpr int TG = STEP / 4 / G;                  // token groups of a lane
+    static constexpr int DW = D / 8;                         // words of a token
+    static constexpr int PER = DW / G;                       // of them, those of a lane's part
+    static constexpr int REPS = DW > TILE ? DW / TILE : 1;   // value words of a lane in each token group
+    static constexpr int PARTS = DW < TILE ? TILE / DW : 1;  // lanes that share a value word
+    static constexpr int NT = 8 / PARTS;                     // output tiles of a value word
+    // 16 rows keep their query operands in registers.  32 rows keep them in
+    // LDS, one copy for the workgroup: D/4 registers fewer, which is a second
+    // wavefront per SIMD, for D/16 reads a step
+    static constexpr bool QREG = TILE == 16;
+    // Passes over the head's dimensions in which the wavefronts' results meet
+    static constexpr int PASSES = NW * TILE * D > 16384 ? 2 : 1;
+    static constexpr int PD = D / PASSES, ROWF = PD + 4;     // dimensions of a pass; a row in LDS, spread over the banks
+};
+
+// A lane's tokens of a step: scores, and probabilities in pairs.
+template <int D, int TILE> using Scores = float[Shape<D, TILE>::TG][4];
+template <int D, int TILE> using Probs = h2[Shape<D, TILE>::TG][2];
+
+template <int D, int TILE>
+struct Keys {
+    uint32_t w[Shape<D, TILE>::SUB][Shape<D, TILE>::PER];
+    uint4 dm[Shape<D, TILE>::TG];
 };
 
 template <int D, int TILE>
-__device__ __forceinline__ void load_tokens(Tokens<D, TILE> &o, const uint8_t *block, int P, int t0, int lane)
+struct Values {
+    uint4 w[Shape<D, TILE>::TG][Shape<D, TILE>::REPS];
+    uint4 dm[Shape<D, TILE>::TG];
+};
+
+template <int D, int TILE>
+__device__ __forceinline__ void load_keys(Keys<D, TILE> &o, const uint8_t *block, int P, int t0, int lane)
 {
-    using K = Tokens<D, TILE>;
-    constexpr int G = Mma<TILE>::GROUPS, W = D >= 128 ? 4 : 2, DW = D / 8;
-    constexpr int SUB = STEP / TILE;                         // token tiles per step (2 or 1)
-    constexpr int PER = DW / G;                              // words of a token that a lane holds
+    using H = Shape<D, TILE>;
+    constexpr int W = D >= 128 ? 4 : 2;
     const int m = lane % TILE, g = lane / TILE;
     const uint32_t *w = reinterpret_cast<const uint32_t *>(block);
-    const uint32_t *dm = w + P * (D / 4);
 #pragma unroll
-    for (int u = 0; u < SUB; u++)
+    for (int u = 0; u < H::SUB; u++)
 #pragma unroll
-        for (int j = 0; j < PER; j += W) {
-            const uint32_t *p = w + kv_kword<D>(t0 + u * TILE + m, g * PER + j);
-            uint32_t *q = &o.k[u * PER + j];
+        for (int j = 0; j < H::PER; j += W) {
+            const uint32_t *p = w + kv_kword<D>(t0 + u * TILE + m, g * H::PER + j);
+            uint32_t *q = &o.w[u][j];
             if constexpr (W == 4) {
                 const uint4 x = *reinterpret_cast<const uint4 *>(p);
                 q[0] = x.x, q[1] = x.y, q[2] = x.z, q[3] = x.w;
@@ -197,109 +219,132 @@ __device__ __forceinline__ void load_tokens(Tokens<D, TILE> &o, const uint8_t *b
             }
         }
 #pragma unroll
-    for (int i = 0; i < K::TG; i++) {
-        const int t = t0 + 4 * (i * G + g);
-        o.dk[i] = *reinterpret_cast<const uint4 *>(dm + t);
-        o.dv[i] = *reinterpret_cast<const uint4 *>(dm + P + t);
+    for (int i = 0; i < H::TG; i++)
+        o.dm[i] = *reinterpret_cast<const uint4 *>(w + P * (D / 4) + t0 + 4 * (i * H::G + g));
+}
+
+template <int D, int TILE>
+__device__ __forceinline__ void load_values(Values<D, TILE> &o, const uint8_t *block, int P, int t0, int lane)
+{
+    using H = Shape<D, TILE>;
+    const int m = lane % TILE, g = lane / TILE;
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(block) + P * H::DW;
 #pragma unroll
-        for (int r = 0; r < K::REPS; r++)
-            o.v[i][r] = *reinterpret_cast<const uint4 *>(w + P * DW + kv_vword<D>(t, (m + r * TILE) % DW));
+    for (int i = 0; i < H::TG; i++) {
+        const int t = t0 + 4 * (i * H::G + g);
+#pragma unroll
+        for (int r = 0; r < H::REPS; r++)
+            o.w[i][r] = *reinterpret_cast<const uint4 *>(w + kv_vword<D>(t, (m + r * TILE) % H::DW));
+        o.dm[i] = *reinterpret_cast<const uint4 *>(w + P * H::DW + P + t);
     }
 }
 
-// One wavefront's running state for its row tile.  Values are relative to
-// 2^mo of their row; mo = mrow - kd, mrow the row's reference score (log2)
-// and kd a power that puts p dv high in fp16's range.
+// One wavefront's running state for its row tile.  Sums are relative to 2^mo
+// of their row, where mo lies so far below the row's largest score that
+// p dv is high in fp16's range.
 template <int D, int TILE>
 struct State {
     static constexpr int TILES = D / TILE;                   // output tiles along the head
-    static constexpr int QW = D / 8 / Mma<TILE>::GROUPS;     // query operands of a lane
-    h8 q[QW];
+    h8 q[Shape<D, TILE>::QREG ? Shape<D, TILE>::PER : 1];    // query operands, where registers hold them
     typename Mma<TILE>::Acc o[TILES];
     float qs, qsum;              // score = qs * (acc dk + (8 dk - mk) qsum), log2 units
-    float mrow, mo, thr;         // reference, offset, and the raw score that calls for a new reference
+    float mo, mrow;              // the offset, and the row's largest score when it was set
+    float thr;                   // the raw score that calls for a new offset,
+    uint32_t dlim;               // and the dv (fp16 bits) that does
     float l, z;                  // sum p, sum p (8 dv - mv)
-    float dlim;                  // largest dv that kd allows for
-    int kd;
 };
 
-// The 32 tokens t0..t0+31; masked: some of them may be hidden from some rows.
+// Raw scores of 32 tokens.
 template <int D, int TILE>
-__device__ __forceinline__ void step(State<D, TILE> &st, Tokens<D, TILE> &tk, int t0, Span seen, bool masked, int lane)
+__device__ __forceinline__ void scores(Scores<D, TILE> &s, const State<D, TILE> &st,
+                                       const h8 *q, const Keys<D, TILE> &k)
 {
     using M = Mma<TILE>;
-    using K = Tokens<D, TILE>;
-    using S = State<D, TILE>;
-    constexpr int G = M::GROUPS, SUB = STEP / TILE, DW = D / 8;
-    const int m = lane % TILE, g = lane / TILE;
-
-    float s[K::TG][4];
+    using H = Shape<D, TILE>;
 #pragma unroll
-    for (int u = 0; u < SUB; u++) {
+    for (int u = 0; u < H::SUB; u++) {
         typename M::Acc acc;
 #pragma unroll
         for (int i = 0; i < M::ACC; i++) acc[i] = 0.0f;
 #pragma unroll
-        for (int j = 0; j < S::QW; j++) acc = M::go(spread8(tk.k[u * S::QW + j]), st.q[j], acc);
+        for (int j = 0; j < H::PER; j++) acc = M::go(spread8(k.w[u][j]), H::QREG ? st.q[j] : q[j * 64], acc);
 #pragma unroll
-        for (int i = 0; i < M::ACC; i++) s[u * (M::ACC / 4) + i / 4][i % 4] = acc[i];
-    }
-#pragma unroll
-    for (int i = 0; i < K::TG; i++) {
-        const uint32_t *dk = reinterpret_cast<const uint32_t *>(&tk.dk[i]);
-#pragma unroll
-        for (int b = 0; b < 4; b++) s[i][b] = fmaf(s[i][b], half_lo(dk[b]), fmaf(half_lo(dk[b]), 8.0f, -half_hi(dk[b])) * st.qsum);
-    }
-    if (masked) {
-#pragma unroll
-        for (int i = 0; i < K::TG; i++) {
-            uint32_t *dv = reinterpret_cast<uint32_t *>(&tk.dv[i]);
-#pragma unroll
-            for (int b = 0; b < 4; b++) {
-                const int t = t0 + 4 * (i * G + g) + b;
-                const bool hide = (unsigned)(t - seen.lo) >= (unsigned)(seen.hi - seen.lo);
-                s[i][b] = hide ? -__builtin_inff() : s[i][b];
-                dv[b] = hide ? 0u : dv[b];                   // what lies there may be NaN
-            }
+        for (int i = 0; i < M::ACC; i++) {
+            const int n = u * (M::ACC / 4) + i / 4;
+            const uint32_t dm = reinterpret_cast<const uint32_t *>(&k.dm[n])[i % 4];
+            s[n][i % 4] = fmaf(acc[i], half_lo(dm), fmaf(half_lo(dm), 8.0f, -half_hi(dm)) * st.qsum);
         }
     }
-    float top = -__builtin_inff(), dtop = 0.0f;
+}
+
+// Hides the tokens of t0..t0+31 that the lane's row does not see.
+template <int D, int TILE>
+__device__ __forceinline__ void hide(Scores<D, TILE> &s, Values<D, TILE> &v, int t0, Span seen, int lane)
+{
+    using H = Shape<D, TILE>;
+    const int g = lane / TILE;
 #pragma unroll
-    for (int i = 0; i < K::TG; i++) {
-        const uint32_t *dv = reinterpret_cast<const uint32_t *>(&tk.dv[i]);
+    for (int i = 0; i < H::TG; i++) {
+        uint32_t *dv = reinterpret_cast<uint32_t *>(&v.dm[i]);
+#pragma unroll
+        for (int b = 0; b < 4; b++) {
+            const int t = t0 + 4 * (i * H::G + g) + b;
+            const bool out = (unsigned)(t - seen.lo) >= (unsigned)(seen.hi - seen.lo);
+            s[i][b] = out ? -__builtin_inff() : s[i][b];
+            dv[b] = out ? 0u : dv[b];                        // what lies there may be NaN
+        }
+    }
+}
+
+// Sees to it that the tokens' p dv fit fp16: where a score or a pair has
+// outgrown the offset (rarely, after the first steps), sets a new one, for
+// which p dv is below 2^7 for all seen so far, and brings the sums to it.
+// Scores may then exceed the reference 2^7 times before the next.
+template <int D, int TILE>
+__device__ __forceinline__ void fit(State<D, TILE> &st, const Scores<D, TILE> &s, const Values<D, TILE> &v)
+{
+    using H = Shape<D, TILE>;
+    float top = -__builtin_inff();
+    uint16_t d = 0;
+#pragma unroll
+    for (int i = 0; i < H::TG; i++) {
+        const uint32_t *dv = reinterpret_cast<const uint32_t *>(&v.dm[i]);
 #pragma unroll
         for (int b = 0; b < 4; b++) {
             top = fmaxf(top, s[i][b]);
-            dtop = fmaxf(dtop, half_lo(dv[b]));
+            d = __builtin_elementwise_max(d, (uint16_t)dv[b]);     // d >= 0: its bits are in order
         }
     }
-    if (__any(top > st.thr || dtop > st.dlim)) {             // rare: a new reference
+    uint32_t dtop = min((uint32_t)d, 0x7BFFu);                     // (a NaN asks for nothing)
+    if (!__any(top > st.thr || dtop > st.dlim)) return;
 #pragma unroll
-        for (int o = TILE; o < 64; o *= 2) top = fmaxf(top, __shfl_xor(top, o));
+    for (int o = TILE; o < 64; o *= 2) top = fmaxf(top, __shfl_xor(top, o));
 #pragma unroll
-        for (int o = 1; o < 64; o *= 2) dtop = fmaxf(dtop, __shfl_xor(dtop, o));
-        const float old = st.mo;
-        if (dtop > st.dlim) {
-            const int e = (int)((__builtin_bit_cast(uint32_t, dtop) >> 23) & 255u) - 127;   // dtop > 0 here
-            st.kd = 6 - e;
-            st.dlim = ldexpf(1.0f, e + 1);
-        }
-        st.mrow = fmaxf(st.mrow, top * st.qs);
-        st.mo = st.mrow - (float)st.kd;
-        st.thr = (st.mrow + SLACK) / st.qs;
-        const float f = __builtin_amdgcn_exp2f(old - st.mo);
-        st.l *= f;
-        st.z *= f;
+    for (int o = 1; o < 64; o *= 2) dtop = max(dtop, (uint32_t)__shfl_xor((int)dtop, o));
+    st.dlim = max(st.dlim, dtop | 0x03FFu);                        // up to the next power of two
+    const float old = st.mo;
+    st.mrow = fmaxf(st.mrow, top * st.qs);
+    st.mo = st.mrow - (float)(6 + 15 - (int)(st.dlim >> 10));
+    st.thr = (st.mrow + 7.0f) / st.qs;
+    const float f = __builtin_amdgcn_exp2f(old - st.mo);
+    st.l *= f;
+    st.z *= f;
 #pragma unroll
-        for (int i = 0; i < S::TILES; i++)
+    for (int i = 0; i < State<D, TILE>::TILES; i++)
 #pragma unroll
-            for (int j = 0; j < M::ACC; j++) st.o[i][j] *= f;
-    }
-    // probabilities, and the operand p dv of the second product
-    h2 pd[K::TG][2];
+        for (int j = 0; j < Mma<TILE>::ACC; j++) st.o[i][j] *= f;
+}
+
+// From scores to probabilities p dv, as matrix operand; the sums of p.
+// FINE: what the rounding to fp16 leaves, as a second operand.
+template <int D, int TILE, bool FINE>
+__device__ __forceinline__ void probabilities(Probs<D, TILE> &hi, Probs<D, TILE> &lo, State<D, TILE> &st,
+                                              const Scores<D, TILE> &s, const Values<D, TILE> &v)
+{
+    using H = Shape<D, TILE>;
 #pragma unroll
-    for (int i = 0; i < K::TG; i++) {
-        const uint32_t *dv = reinterpret_cast<const uint32_t *>(&tk.dv[i]);
+    for (int i = 0; i < H::TG; i++) {
+        const uint32_t *dv = reinterpret_cast<const uint32_t *>(&v.dm[i]);
         float e[4];
 #pragma unroll
         for (int b = 0; b < 4; b++) {
@@ -308,37 +353,48 @@ __device__ __forceinline__ void step(State<D, TILE> &st, Tokens<D, TILE> &tk, in
             st.z = fmaf(p, fmaf(half_lo(dv[b]), 8.0f, -half_hi(dv[b])), st.z);
             e[b] = p * half_lo(dv[b]);
         }
-        pd[i][0] = h2{(_Float16)e[0], (_Float16)e[1]};
-        pd[i][1] = h2{(_Float16)e[2], (_Float16)e[3]};
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+            hi[i][c] = h2{(_Float16)e[2 * c], (_Float16)e[2 * c + 1]};
+            if (FINE) lo[i][c] = h2{(_Float16)(e[2 * c] - (float)hi[i][c][0]), (_Float16)(e[2 * c + 1] - (float)hi[i][c][1])};
+        }
     }
-    // O^T += V^T P^T, two token groups of a lane a time: the codes of a pair
-    // of tokens meet in one word, then one AND makes the pair an operand
-    constexpr int PARTS = DW < TILE ? TILE / DW : 1;         // lanes that share a word of eight dimensions
-    constexpr int NT = 8 / PARTS;                            // output tiles of a word
-    const int part = m / DW;
+}
+
+// O^T += V^T P^T, eight tokens of a lane a time: the codes of two tokens meet
+// in one word, from which pairs of codes are taken as operands.
+template <int D, int TILE, bool FINE>
+__device__ __forceinline__ void gather(State<D, TILE> &st, const Probs<D, TILE> &hi,
+                                       const Probs<D, TILE> &lo, const Values<D, TILE> &v, int lane)
+{
+    using M = Mma<TILE>;
+    using H = Shape<D, TILE>;
+    const int part = lane % TILE / H::DW;
 #pragma unroll
-    for (int i = 0; i < K::TG; i += 2) {
-        const uint4 pw = make_uint4(__builtin_bit_cast(uint32_t, pd[i][0]), __builtin_bit_cast(uint32_t, pd[i][1]),
-                                    __builtin_bit_cast(uint32_t, pd[i + 1][0]), __builtin_bit_cast(uint32_t, pd[i + 1][1]));
-        const h8 p = __builtin_bit_cast(h8, pw);
+    for (int i = 0; i < H::TG; i += 2) {
+        auto operand = [&](const Probs<D, TILE> &x) {
+            return h8{x[i][0][0], x[i][0][1], x[i][1][0], x[i][1][1],
+                      x[i + 1][0][0], x[i + 1][0][1], x[i + 1][1][0], x[i + 1][1][1]};
+        };
+        const h8 p = operand(hi);
 #pragma unroll
-        for (int r = 0; r < K::REPS; r++) {
-            uint32_t w[2][4];                                // [halves of a word][pairs]
+        for (int r = 0; r < H::REPS; r++) {
+            uint32_t w[2][4];                                // [halves of a word][pairs of tokens]
 #pragma unroll
             for (int c = 0; c < 4; c++) {
-                const uint32_t *x = reinterpret_cast<const uint32_t *>(&tk.v[i + c / 2][r]);
+                const uint32_t *x = reinterpret_cast<const uint32_t *>(&v.w[i + c / 2][r]);
                 const uint32_t a = x[2 * (c % 2)], b = x[2 * (c % 2) + 1];
-                if constexpr (PARTS == 1) {
+                if constexpr (H::PARTS == 1) {
                     w[0][c] = __builtin_amdgcn_perm(b, a, 0x05040100u);
                     w[1][c] = __builtin_amdgcn_perm(b, a, 0x07060302u);
-                } else if constexpr (PARTS == 2) {
+                } else if constexpr (H::PARTS == 2) {
                     w[0][c] = __builtin_amdgcn_perm(b, a, part ? 0x07060302u : 0x05040100u);
                 } else {
                     w[0][c] = __builtin_amdgcn_perm(b, a, 0x0C040C00u + 0x00010001u * (uint32_t)part);
                 }
             }
 #pragma unroll
-            for (int n = 0; n < NT; n++) {
+            for (int n = 0; n < H::NT; n++) {
                 h8 x;
 #pragma unroll
                 for (int c = 0; c < 4; c++) {
@@ -347,42 +403,43 @@ __device__ __forceinline__ void step(State<D, TILE> &st, Tokens<D, TILE> &tk, in
                     x[2 * c] = z[0];
                     x[2 * c + 1] = z[1];
                 }
-                st.o[r * NT + n] = M::go(x, p, st.o[r * NT + n]);
+                st.o[r * H::NT + n] = M::go(x, p, st.o[r * H::NT + n]);
+                if (FINE) st.o[r * H::NT + n] = M::go(x, operand(lo), st.o[r * H::NT + n]);
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
 }
 
-// The row's query as matrix operand, and the factors of its scores.
+// The row's query as matrix operand (in st or, for the workgroup, in sq) and
+// the factors of its scores.
 template <int D, int TILE, class T>
-__device__ __forceinline__ void load_query(State<D, TILE> &st, const KvAttend &a, const RowTile &t, int head, int lane)
+__device__ __forceinline__ void load_query(State<D, TILE> &st, h8 *sq, const KvAttend &a, const RowTile &t, int head,
+                                           int wave, int lane)
 {
-    using S = State<D, TILE>;
+    using H = Shape<D, TILE>;
     const int m = lane % TILE, g = lane / TILE;
     const int r = t.r0 + min(m, t.rows - 1), tok = r / a.group, h = head * a.group + r % a.group;
     const T *p = static_cast<const T *>(a.q.data) + (int64_t)(t.row0 + tok) * a.q.token + (int64_t)h * a.q.head +
-                 g * (S::QW * 8);
-    float x[S::QW][8];
+                 g * (H::PER * 8);
+    T x[H::PER][8];
 #pragma unroll
-    for (int j = 0; j < S::QW; j++) {
-        T e[8];
+    for (int j = 0; j < H::PER; j++) {
         if (a.q.wide) {
-            *reinterpret_cast<uint4 *>(e) = *reinterpret_cast<const uint4 *>(p + 8 * j);
+            *reinterpret_cast<uint4 *>(x[j]) = *reinterpret_cast<const uint4 *>(p + 8 * j);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; i++) e[i] = p[8 * j + i];
+            for (int i = 0; i < 8; i++) x[j][i] = p[8 * j + i];
         }
-#pragma unroll
-        for (int i = 0; i < 8; i++) x[j][i] = to_f(e[i]);
     }
     float top = 0.0f;
     double sum = 0.0;            // its error would be common to all tokens of the row, times m
 #pragma unroll
-    for (int j = 0; j < S::QW; j++)
+    for (int j = 0; j < H::PER; j++)
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-            top = fmaxf(top, fabsf(x[j][i]));
-            sum += x[j][i];
+            top = fmaxf(top, fabsf((float)x[j][i]));
+            sum += (float)x[j][i];
         }
 #pragma unroll
     for (int o = TILE; o < 64; o *= 2) {
@@ -395,16 +452,17 @@ __device__ __forceinline__ void load_query(State<D, TILE> &st, const KvAttend &a
     st.qs = a.scale * 1.44269504088896341f * ldexpf(1.0f, e - 14);
     st.qsum = ldexpf((float)sum, 14 - e);
 #pragma unroll
-    for (int j = 0; j < S::QW; j++) {
+    for (int j = 0; j < H::PER; j++) {
         constexpr int order[8] = {0, 4, 1, 5, 2, 6, 3, 7};
+        h8 y;
 #pragma unroll
-        for (int i = 0; i < 8; i++)
-            st.q[j][i] = (_Float16)ldexpf(x[j][order[i]], 14 - e - (order[i] % 2 ? 4 : 0));
+        for (int i = 0; i < 8; i++) y[i] = (_Float16)ldexpf((float)x[j][order[i]], 14 - e - (order[i] % 2 ? 4 : 0));
+        if constexpr (H::QREG)
+            st.q[j] = y;
+        else if (wave == j % NW)
+            sq[j * 64 + lane] = y;
     }
 }
-
-// Floats of a row in LDS: the row starts spread over the banks.
-template <int D> constexpr int ROWF = D + 4;
 
 // Partial results of the call's row tile (x, head) and chunk z: [TILE] rows of
 // D values, then [TILE] of (mo, l).
@@ -443,23 +501,27 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, TILE>)) void k_kv_attend(KvAtten
 {
     using M = Mma<TILE>;
     using S = State<D, TILE>;
-    using K = Tokens<D, TILE>;
-    __shared__ float so[NW * TILE * ROWF<D>];
+    using H = Shape<D, TILE>;
+    constexpr bool FINE = std::is_same<T, _Float16>::value;
+    __shared__ __align__(16) float so[NW * TILE * H::ROWF];
     __shared__ float sl[NW][TILE], sm[NW][TILE];
+    h8 *sq = reinterpret_cast<h8 *>(so);                     // the loop's; so is the end's
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int m = lane % TILE, g = lane / TILE, head = blockIdx.y;
     const int x = gridDim.x - 1 - blockIdx.x;                // later rows see more tokens: they go first
     const RowTile t = row_tile<TILE>(a, x);
     if (t.rows == 0) return;
-    const Span mine = chunk_of(a, t, blockIdx.z);
+    Span mine = chunk_of(a, t, blockIdx.z);
+    if (a.g.n_pages == 0) mine.hi = mine.lo;                 // nothing to load from
     if (blockIdx.z > 0 && mine.lo >= mine.hi) return;        // (chunk 0 always leaves a result)
 
     State<D, TILE> st;
-    load_query<D, TILE, T>(st, a, t, head, lane);
+    load_query<D, TILE, T>(st, sq, a, t, head, wave, lane);
+    if (!H::QREG) __syncthreads();
     st.mrow = st.mo = NONE;
     st.thr = NONE / fmaxf(st.qs, 1.0f);
-    st.l = st.z = st.dlim = 0.0f;
-    st.kd = 0;
+    st.dlim = 0;
+    st.l = st.z = 0.0f;
 #pragma unroll
     for (int i = 0; i < S::TILES; i++)
 #pragma unroll
@@ -474,17 +536,39 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, TILE>)) void k_kv_attend(KvAtten
     };
     auto block_of = [&](int64_t page) { return a.g.pages + page * a.g.page_bytes + (int64_t)head * a.g.block_bytes; };
     constexpr int HOP = NW * STEP;
+    // Absent pages and steps past the end load page 0, unused: no branches
+    // around the loads.  A step's keys are loaded once the scores have used
+    // up the last step's, its values after the second product, so both are
+    // under way for most of a step and need no second set of registers.
     int t0 = mine.lo + wave * STEP;
-    int64_t page = page_at(t0);
+    int64_t page = page_at(t0), after = page_at(t0 + HOP);
+    Keys<D, TILE> k;
+    Values<D, TILE> v;
+    if (t0 < mine.hi) {
+        load_keys<D, TILE>(k, block_of(max(page, (int64_t)0)), P, t0 & (P - 1), lane);
+        load_values<D, TILE>(v, block_of(max(page, (int64_t)0)), P, t0 & (P - 1), lane);
+    }
     while (t0 < mine.hi) {
-        const int64_t after = page_at(t0 + HOP);
-        if (page >= 0) {
-            K cur;
-            load_tokens<D, TILE>(cur, block_of(page), P, t0 & (P - 1), lane);
-            step<D, TILE>(st, cur, t0, seen, t0 < all_lo || t0 + STEP > all_hi || t.rows < TILE, lane);
-        }
+        const int64_t third = page_at(t0 + 2 * HOP);
+        const uint8_t *ahead = block_of(max(after, (int64_t)0));
+        const int tn = (t0 + HOP) & (P - 1);
+        Scores<D, TILE> s;
+        Probs<D, TILE> hi, lo;
+        scores<D, TILE>(s, st, sq + lane, k);
+        __builtin_amdgcn_sched_barrier(0);
+        load_keys<D, TILE>(k, ahead, P, tn, lane);
+        if (page < 0)
+            hide<D, TILE>(s, v, t0, Span{0, 0}, lane);
+        else if (t0 < all_lo || t0 + STEP > all_hi || t.rows < TILE)
+            hide<D, TILE>(s, v, t0, seen, lane);
+        fit<D, TILE>(st, s, v);
+        probabilities<D, TILE, FINE>(hi, lo, st, s, v);
+        gather<D, TILE, FINE>(st, hi, lo, v, lane);
+        __builtin_amdgcn_sched_barrier(0);
+        load_values<D, TILE>(v, ahead, P, tn, lane);
         t0 += HOP;
         page = after;
+        after = third;
     }
 
     // the lanes that share a row, then the wavefronts
@@ -501,79 +585,91 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, TILE>)) void k_kv_attend(KvAtten
     float mo = sm[0][m];
 #pragma unroll
     for (int w = 1; w < NW; w++) mo = fmaxf(mo, sm[w][m]);
-    {
-        const float f = __builtin_amdgcn_exp2f(st.mo - mo);
-        const float fixed = st.z * f;
-        constexpr int DW = D / 8, PARTS = DW < TILE ? TILE / DW : 1, NT = 8 / PARTS;
+    float *part = a.splits > 1 ? part_of<D, TILE>(a, x, head, blockIdx.z) : nullptr;
+    const float f = __builtin_amdgcn_exp2f(st.mo - mo), fixed = st.z * f;
+#pragma unroll
+    for (int pass = 0; pass < H::PASSES; pass++) {
+        if (pass) __syncthreads();
 #pragma unroll
         for (int i = 0; i < S::TILES; i++)
 #pragma unroll
             for (int j = 0; j < M::ACC; j++) {
-                const int r = i / NT, n = i % NT;
+                const int r = i / H::NT, n = i % H::NT;
                 const int row = TILE == 16 ? 4 * g + j : 8 * (j / 4) + 4 * g + j % 4;     // along the head
-                const int d = 8 * (row % DW + r * TILE) + (row / DW) * NT + n;
-                const float unit = n % 2 ? 0x1p-4f : 1.0f;
-                so[(wave * TILE + m) * ROWF<D> + d] = fmaf(st.o[i][j], unit * f, fixed);
+                const int d = 8 * (row % H::DW + r * TILE) + (row / H::DW) * H::NT + n;
+                // (a pass is the first or second half of j, or of r)
+                if (H::PASSES > 1 && (H::REPS > 1 ? r : j / (M::ACC / 2)) != pass) continue;
+                so[(wave * TILE + m) * H::ROWF + d % H::PD] = fmaf(st.o[i][j], n % 2 ? 0x1p-4f * f : f, fixed);
             }
-    }
-    __syncthreads();
-    float *part = a.splits > 1 ? part_of<D, TILE>(a, x, head, blockIdx.z) : nullptr;
-    for (int i = threadIdx.x; i < t.rows * (D / 8); i += NW * 64) {
-        const int r = i / (D / 8), d0 = i % (D / 8) * 8;
-        float y[8], top = sm[0][r], l = 0.0f;
+        __syncthreads();
+        for (int i = threadIdx.x; i < t.rows * (H::PD / 8); i += NW * 64) {
+            const int r = i / (H::PD / 8), d0 = i % (H::PD / 8) * 8;
+            float y[8], top = sm[0][r], l = 0.0f;
 #pragma unroll
-        for (int w = 1; w < NW; w++) top = fmaxf(top, sm[w][r]);
+            for (int w = 1; w < NW; w++) top = fmaxf(top, sm[w][r]);
 #pragma unroll
-        for (int w = 0; w < NW; w++) l += sl[w][r] * __builtin_amdgcn_exp2f(sm[w][r] - top);
+            for (int w = 0; w < NW; w++) l += sl[w][r] * __builtin_amdgcn_exp2f(sm[w][r] - top);
 #pragma unroll
-        for (int j = 0; j < 8; j++) y[j] = 0.0f;
+            for (int j = 0; j < 8; j++) y[j] = 0.0f;
 #pragma unroll
-        for (int w = 0; w < NW; w++)
+            for (int w = 0; w < NW; w++)
 #pragma unroll
-            for (int j = 0; j < 8; j++) y[j] += so[(w * TILE + r) * ROWF<D> + d0 + j];
-        if (part) {
+                for (int j = 0; j < 8; j++) y[j] += so[(w * TILE + r) * H::ROWF + d0 + j];
+            const int d = pass * H::PD + d0;
+            if (part) {
 #pragma unroll
-            for (int j = 0; j < 8; j += 4)
-                *reinterpret_cast<float4 *>(part + r * D + d0 + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
-            if (d0 == 0) *reinterpret_cast<float2 *>(part + TILE * D + 2 * r) = make_float2(top, l);
-        } else {
-            write_row<D, T>(a, t, head, r, d0, y, l, top);
+                for (int j = 0; j < 8; j += 4)
+                    *reinterpret_cast<float4 *>(part + r * D + d + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+                if (d == 0) *reinterpret_cast<float2 *>(part + TILE * D + 2 * r) = make_float2(top, l);
+            } else {
+                write_row<D, T>(a, t, head, r, d, y, l, top);
+            }
         }
     }
 }
 
-// Join the chunks of a row tile: eight dimensions of a row per thread.
+// Joins the chunks of one row: D/8 threads take eight dimensions each, in
+// 2048/D slices that take the chunks in turn and meet in LDS.
 template <int D, int TILE, class T>
 __global__ __launch_bounds__(256) void k_kv_join(KvAttend a)
 {
+    constexpr int C = D / 8, SLICES = 256 / C;
+    __shared__ __align__(16) float sy[SLICES][D];
+    __shared__ float2 sml[SLICES];
     const int64_t x = blockIdx.x;
-    const int head = blockIdx.y;
+    const int head = blockIdx.y, r = blockIdx.z;
     const RowTile t = row_tile<TILE>(a, (int)x);
-    if (t.rows == 0) return;
-    const int used = min((t.hi - t.lo + a.chunk - 1) / a.chunk, a.splits);
-    for (int i = blockIdx.z * 256 + threadIdx.x; i < t.rows * (D / 8); i += gridDim.z * 256) {
-        const int r = i / (D / 8), d0 = i % (D / 8) * 8;
-        float y[8], top = NONE, l = 0.0f;
+    if (r >= t.rows) return;
+    const int used = max(min((t.hi - t.lo + a.chunk - 1) / a.chunk, a.splits), 1);
+    const int slice = threadIdx.x / C, d0 = threadIdx.x % C * 8;
+    float y[8], top = NONE, l = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; j++) y[j] = 0.0f;
-        for (int z = 0; z < max(used, 1); z++) {
-            const float *p = part_of<D, TILE>(a, x, head, z);
-            const float2 ml = *reinterpret_cast<const float2 *>(p + TILE * D + 2 * r);
-            const float now = fmaxf(top, ml.x);
-            const float fo = __builtin_amdgcn_exp2f(top - now), fn = __builtin_amdgcn_exp2f(ml.x - now);
-            top = now;
-            l = l * fo + ml.y * fn;
+    for (int j = 0; j < 8; j++) y[j] = 0.0f;
+    auto add = [&](float mo, float n, const float *v) {
+        const float now = fmaxf(top, mo);
+        const float fo = __builtin_amdgcn_exp2f(top - now), fn = __builtin_amdgcn_exp2f(mo - now);
+        top = now;
+        l = l * fo + n * fn;
 #pragma unroll
-            for (int j = 0; j < 8; j += 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(p + r * D + d0 + j);
-                y[j] = y[j] * fo + v.x * fn;
-                y[j + 1] = y[j + 1] * fo + v.y * fn;
-                y[j + 2] = y[j + 2] * fo + v.z * fn;
-                y[j + 3] = y[j + 3] * fo + v.w * fn;
-            }
-        }
-        write_row<D, T>(a, t, head, r, d0, y, l, top);
+        for (int j = 0; j < 8; j++) y[j] = y[j] * fo + v[j] * fn;
+    };
+    for (int z = slice; z < used; z += SLICES) {
+        const float *p = part_of<D, TILE>(a, x, head, z);
+        const float2 ml = *reinterpret_cast<const float2 *>(p + TILE * D + 2 * r);
+        float v[8];
+        *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(p + r * D + d0);
+        *reinterpret_cast<float4 *>(v + 4) = *reinterpret_cast<const float4 *>(p + r * D + d0 + 4);
+        add(ml.x, ml.y, v);
     }
+    if (slice) {
+        *reinterpret_cast<float4 *>(&sy[slice][d0]) = make_float4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<float4 *>(&sy[slice][d0 + 4]) = make_float4(y[4], y[5], y[6], y[7]);
+        if (d0 == 0) sml[slice] = make_float2(top, l);
+    }
+    __syncthreads();
+    if (slice) return;
+    for (int z = 1; z < min(SLICES, used); z++) add(sml[z].x, sml[z].y, &sy[z][d0]);
+    write_row<D, T>(a, t, head, r, d0, y, l, top);
 }
 
 template <int D, int TILE, class T>
@@ -582,7 +678,7 @@ hipError_t launch(const KvAttend &a, const KvPlan &p, hipStream_t s)
     hipLaunchKernelGGL((k_kv_attend<D, TILE, T>), dim3((unsigned)p.tiles, a.g.kv_heads, p.splits), dim3(NW * 64), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
-    hipLaunchKernelGGL((k_kv_join<D, TILE, T>), dim3((unsigned)p.tiles, a.g.kv_heads, 1), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_kv_join<D, TILE, T>), dim3((unsigned)p.tiles, a.g.kv_heads, TILE), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
