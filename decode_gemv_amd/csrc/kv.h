@@ -15,8 +15,9 @@ struct KvGeom {
     const int32_t *start;        // [n_seqs + 1]
     const int32_t *lens;         // [n_seqs]
     const int32_t *table;        // [n_seqs][stride]
-    int64_t n_pages, stride;
+    int64_t stride;
     int64_t page_bytes;          // kv_heads * block_bytes
+    uint32_t n_pages;            // (a table's entry reaches 2^31 - 1)
     int32_t block_bytes;         // one head's part of a page: page_tokens * (head_dim + 8)
     int32_t n_seqs, n_tokens, kv_heads;
     int32_t page_shift;          // log2(page_tokens)
@@ -96,8 +97,8 @@ __device__ __forceinline__ int64_t kv_page(const KvGeom &g, int seq, int pos)
 {
     const int64_t i = pos >> g.page_shift;
     if (pos < 0 || i >= g.stride) return -1;
-    const int64_t p = g.table[(int64_t)seq * g.stride + i];
-    return p < g.n_pages ? p : -1;           // a negative entry stays negative
+    const int32_t p = g.table[(int64_t)seq * g.stride + i];
+    return (uint32_t)p < g.n_pages ? p : -1;
 }
 
 // Word index, inside a head's block, of word w of token t's keys and values.

@@ -79,21 +79,37 @@ __device__ __forceinline__ float half_hi(uint32_t w) { return (float)__builtin_b
 
 __device__ __forceinline__ h2 halves(uint32_t w) { return __builtin_bit_cast(h2, w); }
 
-// Two codes, one in each half at bits 0..3 (shifted: 4..7), as fp16 c - 8
+// Constants that the compiler is to keep in registers: an AND and an OR with
+// two of them are one instruction, with two literals they are two.
+struct Masks {
+    uint32_t low, high, exp;     // codes at bits 0..3 and 4..7 of each half, fp16's exponent of 1024
+};
+
+__device__ __forceinline__ Masks masks()
+{
+    Masks k;
+    asm("s_mov_b32 %0, 0x000f000f" : "=s"(k.low));
+    asm("s_mov_b32 %0, 0x00f000f0" : "=s"(k.high));
+    asm("v_mov_b32 %0, 0x64006400" : "=v"(k.exp));
+    return k;
+}
+
+// Two codes, one in each half at bits 0..3 (SHIFTED: 4..7), as fp16 c - 8
 // (16 (c - 8)): under the exponent of 1024 they are 1024 + c, and one packed
 // subtraction is exact.
 template <bool SHIFTED>
-__device__ __forceinline__ h2 centred(uint32_t w)
+__device__ __forceinline__ h2 centred(uint32_t w, Masks k)
 {
-    return SHIFTED ? halves((w & 0x00F000F0u) | 0x64006400u) - h2{(_Float16)1152.0f, (_Float16)1152.0f}
-                   : halves((w & 0x000F000Fu) | 0x64006400u) - h2{(_Float16)1032.0f, (_Float16)1032.0f};
+    return SHIFTED ? halves((w & k.high) | k.exp) - h2{(_Float16)1152.0f, (_Float16)1152.0f}
+                   : halves((w & k.low) | k.exp) - h2{(_Float16)1032.0f, (_Float16)1032.0f};
 }
 
 // Eight codes of a word in the order 0 4 1 5 2 6 3 7, those of odd dimensions
 // times 16.
-__device__ __forceinline__ h8 spread8(uint32_t w)
+__device__ __forceinline__ h8 spread8(uint32_t w, Masks k)
 {
-    const h2 a = centred<false>(w), b = centred<true>(w), c = centred<false>(w >> 8), d = centred<true>(w >> 8);
+    const h2 a = centred<false>(w, k), b = centred<true>(w, k);
+    const h2 c = centred<false>(w >> 8, k), d = centred<true>(w >> 8, k);
     return h8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
@@ -197,18 +213,21 @@ struct Values {
     uint4 dm[Shape<D, TILE>::TG];
 };
 
+// The loads of a step.  t0 is a multiple of 32, so a step's part of each
+// array starts at a uniform address, and a lane's place in it is the same for
+// all steps.
 template <int D, int TILE>
 __device__ __forceinline__ void load_keys(Keys<D, TILE> &o, const uint8_t *block, int P, int t0, int lane)
 {
     using H = Shape<D, TILE>;
     constexpr int W = D >= 128 ? 4 : 2;
     const int m = lane % TILE, g = lane / TILE;
-    const uint32_t *w = reinterpret_cast<const uint32_t *>(block);
+    const uint8_t *w = block + t0 * (D / 2), *dm = block + P * D + t0 * 4;
 #pragma unroll
     for (int u = 0; u < H::SUB; u++)
 #pragma unroll
         for (int j = 0; j < H::PER; j += W) {
-            const uint32_t *p = w + kv_kword<D>(t0 + u * TILE + m, g * H::PER + j);
+            const uint8_t *p = w + (unsigned)(kv_kword<D>(m, g * H::PER) * 4 + kv_kword<D>(u * TILE, j) * 4);
             uint32_t *q = &o.w[u][j];
             if constexpr (W == 4) {
                 const uint4 x = *reinterpret_cast<const uint4 *>(p);
@@ -219,8 +238,7 @@ __device__ __forceinline__ void load_keys(Keys<D, TILE> &o, const uint8_t *block
             }
         }
 #pragma unroll
-    for (int i = 0; i < H::TG; i++)
-        o.dm[i] = *reinterpret_cast<const uint4 *>(w + P * (D / 4) + t0 + 4 * (i * H::G + g));
+    for (int i = 0; i < H::TG; i++) o.dm[i] = *reinterpret_cast<const uint4 *>(dm + (unsigned)(16 * g + 16 * i * H::G));
 }
 
 template <int D, int TILE>
@@ -228,14 +246,14 @@ __device__ __forceinline__ void load_values(Values<D, TILE> &o, const uint8_t *b
 {
     using H = Shape<D, TILE>;
     const int m = lane % TILE, g = lane / TILE;
-    const uint32_t *w = reinterpret_cast<const uint32_t *>(block) + P * H::DW;
+    const uint8_t *w = block + P * (D / 2) + t0 * (D / 2), *dm = block + P * D + P * 4 + t0 * 4;
 #pragma unroll
     for (int i = 0; i < H::TG; i++) {
-        const int t = t0 + 4 * (i * H::G + g);
 #pragma unroll
         for (int r = 0; r < H::REPS; r++)
-            o.w[i][r] = *reinterpret_cast<const uint4 *>(w + kv_vword<D>(t, (m + r * TILE) % H::DW));
-        o.dm[i] = *reinterpret_cast<const uint4 *>(w + P * H::DW + P + t);
+            o.w[i][r] = *reinterpret_cast<const uint4 *>(w + (unsigned)((g * H::DW + m % H::DW) * 16 +
+                                                                        (i * H::G * H::DW + r * TILE) * 16));
+        o.dm[i] = *reinterpret_cast<const uint4 *>(dm + (unsigned)(16 * g + 16 * i * H::G));
     }
 }
 
@@ -257,7 +275,7 @@ struct State {
 // Raw scores of 32 tokens.
 template <int D, int TILE>
 __device__ __forceinline__ void scores(Scores<D, TILE> &s, const State<D, TILE> &st,
-                                       const h8 *q, const Keys<D, TILE> &k)
+                                       const h8 *q, const Keys<D, TILE> &k, Masks mk)
 {
     using M = Mma<TILE>;
     using H = Shape<D, TILE>;
@@ -267,7 +285,7 @@ __device__ __forceinline__ void scores(Scores<D, TILE> &s, const State<D, TILE> 
 #pragma unroll
         for (int i = 0; i < M::ACC; i++) acc[i] = 0.0f;
 #pragma unroll
-        for (int j = 0; j < H::PER; j++) acc = M::go(spread8(k.w[u][j]), H::QREG ? st.q[j] : q[j * 64], acc);
+        for (int j = 0; j < H::PER; j++) acc = M::go(spread8(k.w[u][j], mk), H::QREG ? st.q[j] : q[j * 64], acc);
 #pragma unroll
         for (int i = 0; i < M::ACC; i++) {
             const int n = u * (M::ACC / 4) + i / 4;
@@ -351,7 +369,7 @@ __device__ __forceinline__ void probabilities(Probs<D, TILE> &hi, Probs<D, TILE>
             const float p = __builtin_amdgcn_exp2f(fmaf(s[i][b], st.qs, -st.mo));
             st.l += p;
             st.z = fmaf(p, fmaf(half_lo(dv[b]), 8.0f, -half_hi(dv[b])), st.z);
-            e[b] = p * half_lo(dv[b]);
+            e[b] = fmaf(p, half_lo(dv[b]), 0.0f);            // (takes dv as it is)
         }
 #pragma unroll
         for (int c = 0; c < 2; c++) {
@@ -365,7 +383,7 @@ __device__ __forceinline__ void probabilities(Probs<D, TILE> &hi, Probs<D, TILE>
 // in one word, from which pairs of codes are taken as operands.
 template <int D, int TILE, bool FINE>
 __device__ __forceinline__ void gather(State<D, TILE> &st, const Probs<D, TILE> &hi,
-                                       const Probs<D, TILE> &lo, const Values<D, TILE> &v, int lane)
+                                       const Probs<D, TILE> &lo, const Values<D, TILE> &v, Masks mk, int lane)
 {
     using M = Mma<TILE>;
     using H = Shape<D, TILE>;
@@ -399,7 +417,7 @@ __device__ __forceinline__ void gather(State<D, TILE> &st, const Probs<D, TILE> 
 #pragma unroll
                 for (int c = 0; c < 4; c++) {
                     const uint32_t y = n % 4 >= 2 ? w[n / 4][c] >> 8 : w[n / 4][c];
-                    const h2 z = n % 2 ? centred<true>(y) : centred<false>(y);
+                    const h2 z = n % 2 ? centred<true>(y, mk) : centred<false>(y, mk);
                     x[2 * c] = z[0];
                     x[2 * c + 1] = z[1];
                 }
@@ -531,44 +549,54 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, TILE>)) void k_kv_attend(KvAtten
     const Span head_row = span_of<TILE>(a, t, 0), last_row = span_of<TILE>(a, t, t.rows - 1);
     const int all_lo = last_row.lo, all_hi = head_row.hi;     // tokens every row sees
     const int P = 1 << a.g.page_shift;
-    auto page_at = [&](int t0) -> int64_t {
-        return t0 < mine.hi ? kv_page(a.g, t.seq, t0) : -1;
+    // (the table's entry of a step past the end is the last one's again)
+    const int32_t *pages = a.g.table + (int64_t)t.seq * a.g.stride;
+    auto entry_at = [&](int t0) { return pages[min(t0, mine.hi - 1) >> a.g.page_shift]; };
+    auto present = [&](int32_t entry) { return (uint32_t)entry < a.g.n_pages; };
+    auto block_of = [&](int32_t entry) {
+        return a.g.pages + (uint64_t)(present(entry) ? (uint32_t)entry : 0u) * (uint64_t)a.g.page_bytes +
+               (uint32_t)head * (uint32_t)a.g.block_bytes;
     };
-    auto block_of = [&](int64_t page) { return a.g.pages + page * a.g.page_bytes + (int64_t)head * a.g.block_bytes; };
     constexpr int HOP = NW * STEP;
+    const Masks mk = masks();
     // Absent pages and steps past the end load page 0, unused: no branches
     // around the loads.  A step's keys are loaded once the scores have used
     // up the last step's, its values after the second product, so both are
     // under way for most of a step and need no second set of registers.
-    int t0 = mine.lo + wave * STEP;
-    int64_t page = page_at(t0), after = page_at(t0 + HOP);
-    Keys<D, TILE> k;
-    Values<D, TILE> v;
-    if (t0 < mine.hi) {
-        load_keys<D, TILE>(k, block_of(max(page, (int64_t)0)), P, t0 & (P - 1), lane);
-        load_values<D, TILE>(v, block_of(max(page, (int64_t)0)), P, t0 & (P - 1), lane);
-    }
-    while (t0 < mine.hi) {
-        const int64_t third = page_at(t0 + 2 * HOP);
-        const uint8_t *ahead = block_of(max(after, (int64_t)0));
-        const int tn = (t0 + HOP) & (P - 1);
-        Scores<D, TILE> s;
-        Probs<D, TILE> hi, lo;
-        scores<D, TILE>(s, st, sq + lane, k);
-        __builtin_amdgcn_sched_barrier(0);
-        load_keys<D, TILE>(k, ahead, P, tn, lane);
-        if (page < 0)
-            hide<D, TILE>(s, v, t0, Span{0, 0}, lane);
-        else if (t0 < all_lo || t0 + STEP > all_hi || t.rows < TILE)
-            hide<D, TILE>(s, v, t0, seen, lane);
-        fit<D, TILE>(st, s, v);
-        probabilities<D, TILE, FINE>(hi, lo, st, s, v);
-        gather<D, TILE, FINE>(st, hi, lo, v, lane);
-        __builtin_amdgcn_sched_barrier(0);
-        load_values<D, TILE>(v, ahead, P, tn, lane);
-        t0 += HOP;
-        page = after;
-        after = third;
+    if (mine.lo + wave * STEP < mine.hi) {
+        int t0 = mine.lo + wave * STEP;
+        int32_t page = __builtin_amdgcn_readfirstlane(entry_at(t0)), after = entry_at(t0 + HOP);
+        Keys<D, TILE> k;
+        Values<D, TILE> v;
+        load_keys<D, TILE>(k, block_of(page), P, t0 & (P - 1), lane);
+        load_values<D, TILE>(v, block_of(page), P, t0 & (P - 1), lane);
+        do {
+            const int32_t ahead = __builtin_amdgcn_readfirstlane(after);
+            after = entry_at(t0 + 2 * HOP);
+            const uint8_t *block = block_of(ahead);
+            const int tn = (t0 + HOP) & (P - 1);
+            Scores<D, TILE> s;
+            Probs<D, TILE> hi, lo;
+            scores<D, TILE>(s, st, sq + lane, k, mk);
+            // the scores are done here, not where they are used, so that the
+            // keys' registers are free
+#pragma unroll
+            for (int i = 0; i < H::TG; i++)
+#pragma unroll
+                for (int b = 0; b < 4; b++) asm volatile("" : "+v"(s[i][b]));
+            load_keys<D, TILE>(k, block, P, tn, lane);
+            if (!present(page))
+                hide<D, TILE>(s, v, t0, Span{0, 0}, lane);
+            else if (t0 < all_lo || t0 + STEP > all_hi || t.rows < TILE)
+                hide<D, TILE>(s, v, t0, seen, lane);
+            fit<D, TILE>(st, s, v);
+            probabilities<D, TILE, FINE>(hi, lo, st, s, v);
+            gather<D, TILE, FINE>(st, hi, lo, v, mk, lane);
+            load_values<D, TILE>(v, block, P, tn, lane);
+            asm volatile("" ::: "memory");                   // (or they are moved to the next step's start)
+            t0 += HOP;
+            page = ahead;
+        } while (t0 < mine.hi);
     }
 
     // the lanes that share a row, then the wavefronts

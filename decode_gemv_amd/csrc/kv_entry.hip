@@ -2,6 +2,7 @@
 // checks and launches.  Everything the kernels assume of the host's numbers
 // is checked here; what lies in device memory (start, lens, table) the
 // kernels check themselves.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <string>
@@ -43,7 +44,7 @@ lw_status geom(const lw_kv_cache *c, const lw_kv_batch *b, int64_t n_tokens, KvG
     g.start = b->start;
     g.lens = b->lens;
     g.table = b->table;
-    g.n_pages = c->n_pages;
+    g.n_pages = (uint32_t)std::min<int64_t>(c->n_pages, (int64_t)1 << 31);
     g.stride = b->table_stride;
     g.block_bytes = c->page_tokens * (c->head_dim + 8);
     g.page_bytes = (int64_t)g.block_bytes * c->kv_heads;
