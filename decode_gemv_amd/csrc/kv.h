@@ -36,6 +36,7 @@ struct KvAttend {
     float *lse;                  // [n_tokens][q_heads], or null
     float *part;                 // split partials (see kv_attend.hip), or null
     int32_t group;               // query heads per kv head
+    uint32_t group_inv;          // ceil(2^21 / group): (x * group_inv) >> 21 = x / group for x < 2048
     int32_t causal, window;      // window 0: none
     int32_t splits, chunk;       // token chunks per row tile, tokens per chunk
     float scale;                 // > 0
@@ -61,36 +62,36 @@ hipError_t lw_launch_kv_attend(const KvAttend &a, int head_dim, int dtype, const
 #ifdef __HIPCC__
 // ------------------------------------------------------------ device helpers
 
-// The cached token of a packed row: its sequence, position and page.
-struct KvPlace {
-    int32_t seq, pos;            // seq < 0: the row belongs to no sequence
-    int64_t page;                // < 0: the token is absent
+// A sequence of the batch, kept inside the tensors whatever the caller's
+// arrays hold: its packed rows row0 .. row0 + n_new - 1, and its length.
+struct KvSeq {
+    int32_t seq;                 // -1: none
+    int32_t row0, n_new, len;
 };
 
-// Number of entries of bound(s), s = 0..n-1, that are <= x, for a bound that
-// does not decrease: the wavefront's 64 lanes look at 64 entries at a time
-// (one load latency where a binary search has one for each halving).
+// The sequence that x belongs to, for a bound(start[s + 1], s) that does not
+// decrease with s: the first sequence whose bound is above x.  The
+// wavefront's 64 lanes look at 64 sequences at a time, and what there is to
+// know of the one found is then in a lane already (one load latency where a
+// binary search, and the loads after it, have one for each step).
 template <class F>
-__device__ __forceinline__ int kv_count_le(int n, int x, F bound)
+__device__ __forceinline__ KvSeq kv_find(const KvGeom &g, int x, F bound)
 {
     const int lane = threadIdx.x & 63;
-    int found = 0;
-    for (int s = 0; s < n; s += 64) {
-        const bool le = s + lane < n && bound(s + lane) <= x;
-        const int c = __popcll(__ballot(le));
-        found += c;
-        if (c < 64) break;
+    KvSeq r = {-1, 0, 0, 0};
+    for (int s = 0; s < g.n_seqs; s += 64) {
+        const int mine = min(s + lane, g.n_seqs - 1);
+        const int a = g.start[mine], b = g.start[mine + 1], len = g.lens[mine];
+        const int c = __popcll(__ballot(s + lane < g.n_seqs && bound(b, mine) <= x));
+        if (c == 64) continue;
+        if (s + c >= g.n_seqs) break;
+        r.seq = s + c;
+        r.row0 = min(max(__builtin_amdgcn_readlane(a, c), 0), g.n_tokens);
+        r.n_new = min(max(__builtin_amdgcn_readlane(b, c), r.row0), g.n_tokens) - r.row0;
+        r.len = max(__builtin_amdgcn_readlane(len, c), 0);
+        break;
     }
-    return found;
-}
-
-// First and one-past-last packed row of a sequence, kept inside the tensor
-// whatever the caller's array holds.
-__device__ __forceinline__ int2 kv_rows(const KvGeom &g, int seq)
-{
-    const int a = min(max(g.start[seq], 0), g.n_tokens);
-    const int b = min(max(g.start[seq + 1], a), g.n_tokens);
-    return make_int2(a, b);
+    return r;
 }
 
 __device__ __forceinline__ int64_t kv_page(const KvGeom &g, int seq, int pos)

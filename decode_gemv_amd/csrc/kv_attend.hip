@@ -25,7 +25,7 @@
 // maximum, the sums and the rescaling are per lane, and the loop has no
 // exchange between lanes, no shared memory and no barrier.
 //
-// A workgroup has one tile of 16 or 32 query rows of a sequence (row = token
+// A workgroup has one tile of 8, 16 or 32 query rows of a sequence (row = token
 // * group + head, all on one kv head) and a chunk of the sequence's tokens;
 // its wavefronts take 32-token tiles in turn and meet in LDS at the end.
 // Where row tiles are few, a sequence is cut into several chunks and
@@ -53,13 +53,13 @@ constexpr int NW = 4;                  // wavefronts of a workgroup
 constexpr int STEP = 32;               // tokens of a wavefront's step
 constexpr float NONE = -1e30f;         // log2 of "nothing seen yet"
 
-// Wavefronts a SIMD is to hold (the registers that leaves).
-template <int D, int TILE> constexpr int WAVES = D * TILE <= 2048 && TILE == 16 ? 3 : D * TILE <= 4096 ? 2 : 1;
-
-template <int TILE> struct Mma;
-template <> struct Mma<16> {           // 16 x 16 x 32: lane = row/column l % 16, 8 of the 32 at 8 * (l / 16)
+// A row tile has 8, 16 or 32 rows.  16 and 32 are the columns of a matrix
+// instruction; 8 rows take both halves of the 16, with the same queries, and
+// each half keeps its own half of the tokens: the work on scores and
+// probabilities, which goes by columns, is then done once and not twice.
+template <int ROWS> struct Mma {       // 16 x 16 x 32: lane = row/column l % 16, 8 of the 32 at 8 * (l / 16)
     using Acc = f4;
-    static constexpr int ACC = 4, GROUPS = 4;
+    static constexpr int WIDE = 16, ACC = 4;
     static __device__ __forceinline__ Acc go(h8 a, h8 b, Acc c)
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -67,12 +67,15 @@ template <> struct Mma<16> {           // 16 x 16 x 32: lane = row/column l % 16
 };
 template <> struct Mma<32> {           // 32 x 32 x 16: lane = row/column l % 32, 8 of the 16 at 8 * (l / 32)
     using Acc = f16v;
-    static constexpr int ACC = 16, GROUPS = 2;
+    static constexpr int WIDE = 32, ACC = 16;
     static __device__ __forceinline__ Acc go(h8 a, h8 b, Acc c)
     {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
     }
 };
+
+// Wavefronts a SIMD is to hold (the registers that leaves).
+template <int D, int ROWS> constexpr int WAVES = D <= 128 && ROWS <= 16 ? 3 : D * ROWS <= 4096 ? 2 : 1;
 
 __device__ __forceinline__ float half_lo(uint32_t w) { return (float)__builtin_bit_cast(h2, w)[0]; }
 __device__ __forceinline__ float half_hi(uint32_t w) { return (float)__builtin_bit_cast(h2, w)[1]; }
@@ -122,15 +125,22 @@ struct Span {
 
 // Everything the parts of a call agree on about a row tile.
 struct RowTile {
-    int seq, r0, rows;           // first row (token * group + head) and rows in use (0: nothing to do)
-    int row0, n_new, len;        // first packed row of the sequence, its new tokens, its length
+    int seq, rows;               // rows in use (0: nothing to do)
+    int row0, n_new, len;        // the sequence's first packed row, new tokens and length
+    int tok0, rem0;              // new token and head of the tile's first row
     int lo, hi;                  // tokens any of the rows may see: [lo, hi), lo a multiple of STEP
 };
 
-template <int TILE>
+// New token (x) and head of the kv head's group (y) of row r of the tile.
+__device__ __forceinline__ int2 token_of(const KvAttend &a, const RowTile &t, int r)
+{
+    const unsigned i = t.rem0 + r, q = (i * a.group_inv) >> 21;
+    return make_int2(t.tok0 + (int)q, (int)(i - q * a.group));
+}
+
 __device__ __forceinline__ Span span_of(const KvAttend &a, const RowTile &t, int r)
 {
-    const int i = (t.r0 + r) / a.group, pos = t.len - t.n_new + i;
+    const int pos = t.len - t.n_new + token_of(a, t, r).x;
     Span s = {0, a.causal ? pos + 1 : t.len};
     if (a.window && pos >= a.window) s.lo = pos - a.window + 1;
     if (r >= t.rows || s.hi < s.lo) s.hi = s.lo;
@@ -138,34 +148,42 @@ __device__ __forceinline__ Span span_of(const KvAttend &a, const RowTile &t, int
 }
 
 // Row tile x of the call.  Sequence s owns the tiles from
-// floor(start[s] * group / TILE) + s on, as many as its rows need at most, so
+// floor(start[s] * group / ROWS) + s on, as many as its rows need at most, so
 // its tiles are found without a prefix sum (and one may find nothing to do).
-template <int TILE>
+template <int ROWS>
 __device__ __forceinline__ RowTile row_tile(const KvAttend &a, int x)
 {
     const KvGeom &g = a.g;
     RowTile t = {};
-    auto first = [&](int row, int s) {
-        const int64_t rr = (int64_t)min(max(row, 0), g.n_tokens) * a.group;
-        return (int)(rr / TILE) + s;
-    };
-    const int seq = kv_count_le(g.n_seqs, x, [&](int s) { return first(g.start[s + 1], s + 1); });
-    t.seq = __builtin_amdgcn_readfirstlane(seq);
-    if (t.seq >= g.n_seqs) return t;
-    const int2 rows = kv_rows(g, t.seq);
-    t.row0 = rows.x;
-    t.n_new = rows.y - rows.x;
-    t.len = max(g.lens[t.seq], 0);
-    const int local = x - first(rows.x, t.seq);
-    const int64_t r0 = (int64_t)local * TILE, all = (int64_t)t.n_new * a.group;
+    auto first = [&](int row, int s) { return min(max(row, 0), g.n_tokens) * a.group / ROWS + s; };   // < 2^31
+    const KvSeq q = kv_find(g, x, [&](int next, int s) { return first(next, s + 1); });
+    t.seq = q.seq;
+    if (q.seq < 0) return t;
+    t.row0 = q.row0;
+    t.n_new = q.n_new;
+    t.len = q.len;
+    const int local = x - first(q.row0, q.seq), r0 = local * ROWS, all = q.n_new * a.group;
     if (local < 0 || r0 >= all) return t;
-    t.r0 = (int)r0;
-    t.rows = (int)min((int64_t)TILE, all - r0);
-    const Span b = span_of<TILE>(a, t, 0), e = span_of<TILE>(a, t, t.rows - 1);
+    t.rows = min(ROWS, all - r0);
+    t.tok0 = r0 / a.group;
+    t.rem0 = r0 - t.tok0 * a.group;
+    const Span b = span_of(a, t, 0), e = span_of(a, t, t.rows - 1);
     t.lo = b.lo & ~(STEP - 1);
     const int64_t cap = min(g.stride << g.page_shift, (int64_t)0x7FFF0000);     // the table names no more
     t.hi = max((int)min((int64_t)e.hi, cap), t.lo);
     return t;
+}
+
+// The row tile that workgroups of number z take: the last first, as later rows
+// see more tokens, and those of one parity before the others.  Row tiles with
+// nothing to do come at regular distances (every second where sequences fill
+// one tile each), and workgroups go round the eight XCDs: in plain order all
+// the work could fall to every second XCD (48 us where this takes 32, one
+// sequence of 131071 tokens).
+__device__ __forceinline__ int tile_at(int tiles, int z)
+{
+    const int first = (tiles + 1) / 2;
+    return z < first ? 2 * (first - 1 - z) : 2 * (tiles - first - 1 - (z - first)) + 1;
 }
 
 // Chunk z of a row tile's tokens; the last takes what is left.
@@ -178,56 +196,67 @@ __device__ __forceinline__ Span chunk_of(const KvAttend &a, const RowTile &t, in
 
 // What a lane holds of 32 tokens: key words and value words, and the pairs of
 // the tokens whose scores it will have (groups of four).
-template <int D, int TILE>
+template <int D, int ROWS>
 struct Shape {
-    static constexpr int G = Mma<TILE>::GROUPS;
-    static constexpr int SUB = STEP / TILE;                  // token tiles of a step (2 or 1)
-    static constexpr int TG = STEP / 4 / G;                  // token groups of a lane
+    static constexpr int WIDE = Mma<ROWS>::WIDE;
+    static constexpr int COPIES = WIDE / ROWS;               // columns of a row
+    static constexpr int G = 64 / WIDE;                      // lanes that share a column
+    static constexpr int SUB = STEP / WIDE;                  // token tiles of a step (2 or 1)
+    static constexpr int VG = STEP / 4 / G;                  // token groups of a lane's value words
+    static constexpr int TG = VG / COPIES;                   // and of its scores
     static constexpr int DW = D / 8;                         // words of a token
     static constexpr int PER = DW / G;                       // of them, those of a lane's part
-    static constexpr int REPS = DW > TILE ? DW / TILE : 1;   // value words of a lane in each token group
-    static constexpr int PARTS = DW < TILE ? TILE / DW : 1;  // lanes that share a value word
+    static constexpr int REPS = DW > WIDE ? DW / WIDE : 1;   // value words of a lane in each token group
+    static constexpr int PARTS = DW < WIDE ? WIDE / DW : 1;  // lanes that share a value word
     static constexpr int NT = 8 / PARTS;                     // output tiles of a value word
-    // 16 rows keep their query operands in registers.  32 rows keep them in
+    // Up to 16 rows keep their query operands in registers.  32 rows keep them in
     // LDS, one copy for the workgroup: D/4 registers fewer, which is a second
     // wavefront per SIMD, for D/16 reads a step
-    static constexpr bool QREG = TILE == 16;
+    static constexpr bool QREG = ROWS <= 16;
     // Passes over the head's dimensions in which the wavefronts' results meet
-    static constexpr int PASSES = NW * TILE * D > 16384 ? 2 : 1;
+    static constexpr int PASSES = NW * WIDE * D > 16384 ? 2 : 1;
     static constexpr int PD = D / PASSES, ROWF = PD + 4;     // dimensions of a pass; a row in LDS, spread over the banks
 };
 
 // A lane's tokens of a step: scores, and probabilities in pairs.
-template <int D, int TILE> using Scores = float[Shape<D, TILE>::TG][4];
-template <int D, int TILE> using Probs = h2[Shape<D, TILE>::TG][2];
+template <int D, int ROWS> using Scores = float[Shape<D, ROWS>::TG][4];
+template <int D, int ROWS> using Probs = h2[Shape<D, ROWS>::TG][2];
 
-template <int D, int TILE>
+template <int D, int ROWS>
 struct Keys {
-    uint32_t w[Shape<D, TILE>::SUB][Shape<D, TILE>::PER];
-    uint4 dm[Shape<D, TILE>::TG];
+    uint32_t w[Shape<D, ROWS>::SUB][Shape<D, ROWS>::PER];
+    uint4 dm[Shape<D, ROWS>::TG];
 };
 
-template <int D, int TILE>
+template <int D, int ROWS>
 struct Values {
-    uint4 w[Shape<D, TILE>::TG][Shape<D, TILE>::REPS];
-    uint4 dm[Shape<D, TILE>::TG];
+    uint4 w[Shape<D, ROWS>::VG][Shape<D, ROWS>::REPS];
+    uint4 dm[Shape<D, ROWS>::TG];
 };
+
+// First token of group i of a lane's scores.
+template <int D, int ROWS>
+__device__ __forceinline__ int group_token(int i, int lane)
+{
+    using H = Shape<D, ROWS>;
+    return 4 * ((H::COPIES > 1 ? lane % H::WIDE / ROWS : i) * H::G + lane / H::WIDE);
+}
 
 // The loads of a step.  t0 is a multiple of 32, so a step's part of each
 // array starts at a uniform address, and a lane's place in it is the same for
 // all steps.
-template <int D, int TILE>
-__device__ __forceinline__ void load_keys(Keys<D, TILE> &o, const uint8_t *block, int P, int t0, int lane)
+template <int D, int ROWS>
+__device__ __forceinline__ void load_keys(Keys<D, ROWS> &o, const uint8_t *block, int P, int t0, int lane)
 {
-    using H = Shape<D, TILE>;
+    using H = Shape<D, ROWS>;
     constexpr int W = D >= 128 ? 4 : 2;
-    const int m = lane % TILE, g = lane / TILE;
+    const int m = lane % H::WIDE, g = lane / H::WIDE;
     const uint8_t *w = block + t0 * (D / 2), *dm = block + P * D + t0 * 4;
 #pragma unroll
     for (int u = 0; u < H::SUB; u++)
 #pragma unroll
         for (int j = 0; j < H::PER; j += W) {
-            const uint8_t *p = w + (unsigned)(kv_kword<D>(m, g * H::PER) * 4 + kv_kword<D>(u * TILE, j) * 4);
+            const uint8_t *p = w + (unsigned)(kv_kword<D>(m, g * H::PER) * 4 + kv_kword<D>(u * H::WIDE, j) * 4);
             uint32_t *q = &o.w[u][j];
             if constexpr (W == 4) {
                 const uint4 x = *reinterpret_cast<const uint4 *>(p);
@@ -238,33 +267,35 @@ __device__ __forceinline__ void load_keys(Keys<D, TILE> &o, const uint8_t *block
             }
         }
 #pragma unroll
-    for (int i = 0; i < H::TG; i++) o.dm[i] = *reinterpret_cast<const uint4 *>(dm + (unsigned)(16 * g + 16 * i * H::G));
+    for (int i = 0; i < H::TG; i++)
+        o.dm[i] = *reinterpret_cast<const uint4 *>(dm + (unsigned)(4 * group_token<D, ROWS>(0, lane) + 16 * i * H::G));
 }
 
-template <int D, int TILE>
-__device__ __forceinline__ void load_values(Values<D, TILE> &o, const uint8_t *block, int P, int t0, int lane)
+template <int D, int ROWS>
+__device__ __forceinline__ void load_values(Values<D, ROWS> &o, const uint8_t *block, int P, int t0, int lane)
 {
-    using H = Shape<D, TILE>;
-    const int m = lane % TILE, g = lane / TILE;
+    using H = Shape<D, ROWS>;
+    const int m = lane % H::WIDE, g = lane / H::WIDE;
     const uint8_t *w = block + P * (D / 2) + t0 * (D / 2), *dm = block + P * D + P * 4 + t0 * 4;
 #pragma unroll
-    for (int i = 0; i < H::TG; i++) {
+    for (int i = 0; i < H::VG; i++)
 #pragma unroll
         for (int r = 0; r < H::REPS; r++)
             o.w[i][r] = *reinterpret_cast<const uint4 *>(w + (unsigned)((g * H::DW + m % H::DW) * 16 +
-                                                                        (i * H::G * H::DW + r * TILE) * 16));
-        o.dm[i] = *reinterpret_cast<const uint4 *>(dm + (unsigned)(16 * g + 16 * i * H::G));
-    }
+                                                                        (i * H::G * H::DW + r * H::WIDE) * 16));
+#pragma unroll
+    for (int i = 0; i < H::TG; i++)
+        o.dm[i] = *reinterpret_cast<const uint4 *>(dm + (unsigned)(4 * group_token<D, ROWS>(0, lane) + 16 * i * H::G));
 }
 
 // One wavefront's running state for its row tile.  Sums are relative to 2^mo
 // of their row, where mo lies so far below the row's largest score that
 // p dv is high in fp16's range.
-template <int D, int TILE>
+template <int D, int ROWS>
 struct State {
-    static constexpr int TILES = D / TILE;                   // output tiles along the head
-    h8 q[Shape<D, TILE>::QREG ? Shape<D, TILE>::PER : 1];    // query operands, where registers hold them
-    typename Mma<TILE>::Acc o[TILES];
+    static constexpr int TILES = D / Mma<ROWS>::WIDE;        // output tiles along the head
+    h8 q[Shape<D, ROWS>::QREG ? Shape<D, ROWS>::PER : 1];    // query operands, where registers hold them
+    typename Mma<ROWS>::Acc o[TILES];
     float qs, qsum;              // score = qs * (acc dk + (8 dk - mk) qsum), log2 units
     float mo, mrow;              // the offset, and the row's largest score when it was set
     float thr;                   // the raw score that calls for a new offset,
@@ -273,40 +304,43 @@ struct State {
 };
 
 // Raw scores of 32 tokens.
-template <int D, int TILE>
-__device__ __forceinline__ void scores(Scores<D, TILE> &s, const State<D, TILE> &st,
-                                       const h8 *q, const Keys<D, TILE> &k, Masks mk)
+template <int D, int ROWS>
+__device__ __forceinline__ void scores(Scores<D, ROWS> &s, const State<D, ROWS> &st, const h8 *q,
+                                       const Keys<D, ROWS> &k, Masks mk, int lane)
 {
-    using M = Mma<TILE>;
-    using H = Shape<D, TILE>;
+    using M = Mma<ROWS>;
+    using H = Shape<D, ROWS>;
+    typename M::Acc acc[H::SUB];
 #pragma unroll
     for (int u = 0; u < H::SUB; u++) {
-        typename M::Acc acc;
 #pragma unroll
-        for (int i = 0; i < M::ACC; i++) acc[i] = 0.0f;
+        for (int i = 0; i < M::ACC; i++) acc[u][i] = 0.0f;
 #pragma unroll
-        for (int j = 0; j < H::PER; j++) acc = M::go(spread8(k.w[u][j], mk), H::QREG ? st.q[j] : q[j * 64], acc);
-#pragma unroll
-        for (int i = 0; i < M::ACC; i++) {
-            const int n = u * (M::ACC / 4) + i / 4;
-            const uint32_t dm = reinterpret_cast<const uint32_t *>(&k.dm[n])[i % 4];
-            s[n][i % 4] = fmaf(acc[i], half_lo(dm), fmaf(half_lo(dm), 8.0f, -half_hi(dm)) * st.qsum);
-        }
+        for (int j = 0; j < H::PER; j++) acc[u] = M::go(spread8(k.w[u][j], mk), H::QREG ? st.q[j] : q[j * 64], acc[u]);
     }
+    const bool second = lane % H::WIDE / ROWS != 0;
+#pragma unroll
+    for (int n = 0; n < H::TG; n++)
+#pragma unroll
+        for (int b = 0; b < 4; b++) {
+            float x = acc[n * 4 / M::ACC][n * 4 % M::ACC + b];
+            if constexpr (H::COPIES == 2) x = second ? acc[H::SUB - 1][b] : x;
+            const uint32_t dm = reinterpret_cast<const uint32_t *>(&k.dm[n])[b];
+            s[n][b] = fmaf(x, half_lo(dm), fmaf(half_lo(dm), 8.0f, -half_hi(dm)) * st.qsum);
+        }
 }
 
 // Hides the tokens of t0..t0+31 that the lane's row does not see.
-template <int D, int TILE>
-__device__ __forceinline__ void hide(Scores<D, TILE> &s, Values<D, TILE> &v, int t0, Span seen, int lane)
+template <int D, int ROWS>
+__device__ __forceinline__ void hide(Scores<D, ROWS> &s, Values<D, ROWS> &v, int t0, Span seen, int lane)
 {
-    using H = Shape<D, TILE>;
-    const int g = lane / TILE;
+    using H = Shape<D, ROWS>;
 #pragma unroll
     for (int i = 0; i < H::TG; i++) {
         uint32_t *dv = reinterpret_cast<uint32_t *>(&v.dm[i]);
 #pragma unroll
         for (int b = 0; b < 4; b++) {
-            const int t = t0 + 4 * (i * H::G + g) + b;
+            const int t = t0 + group_token<D, ROWS>(i, lane) + b;
             const bool out = (unsigned)(t - seen.lo) >= (unsigned)(seen.hi - seen.lo);
             s[i][b] = out ? -__builtin_inff() : s[i][b];
             dv[b] = out ? 0u : dv[b];                        // what lies there may be NaN
@@ -318,10 +352,10 @@ __device__ __forceinline__ void hide(Scores<D, TILE> &s, Values<D, TILE> &v, int
 // outgrown the offset (rarely, after the first steps), sets a new one, for
 // which p dv is below 2^7 for all seen so far, and brings the sums to it.
 // Scores may then exceed the reference 2^7 times before the next.
-template <int D, int TILE>
-__device__ __forceinline__ void fit(State<D, TILE> &st, const Scores<D, TILE> &s, const Values<D, TILE> &v)
+template <int D, int ROWS>
+__device__ __forceinline__ void fit(State<D, ROWS> &st, const Scores<D, ROWS> &s, const Values<D, ROWS> &v)
 {
-    using H = Shape<D, TILE>;
+    using H = Shape<D, ROWS>;
     float top = -__builtin_inff();
     uint16_t d = 0;
 #pragma unroll
@@ -336,7 +370,7 @@ __device__ __forceinline__ void fit(State<D, TILE> &st, const Scores<D, TILE> &s
     uint32_t dtop = min((uint32_t)d, 0x7BFFu);                     // (a NaN asks for nothing)
     if (!__any(top > st.thr || dtop > st.dlim)) return;
 #pragma unroll
-    for (int o = TILE; o < 64; o *= 2) top = fmaxf(top, __shfl_xor(top, o));
+    for (int o = Mma<ROWS>::WIDE; o < 64; o *= 2) top = fmaxf(top, __shfl_xor(top, o));
 #pragma unroll
     for (int o = 1; o < 64; o *= 2) dtop = max(dtop, (uint32_t)__shfl_xor((int)dtop, o));
     st.dlim = max(st.dlim, dtop | 0x03FFu);                        // up to the next power of two
@@ -348,18 +382,18 @@ __device__ __forceinline__ void fit(State<D, TILE> &st, const Scores<D, TILE> &s
     st.l *= f;
     st.z *= f;
 #pragma unroll
-    for (int i = 0; i < State<D, TILE>::TILES; i++)
+    for (int i = 0; i < State<D, ROWS>::TILES; i++)
 #pragma unroll
-        for (int j = 0; j < Mma<TILE>::ACC; j++) st.o[i][j] *= f;
+        for (int j = 0; j < Mma<ROWS>::ACC; j++) st.o[i][j] *= f;
 }
 
 // From scores to probabilities p dv, as matrix operand; the sums of p.
 // FINE: what the rounding to fp16 leaves, as a second operand.
-template <int D, int TILE, bool FINE>
-__device__ __forceinline__ void probabilities(Probs<D, TILE> &hi, Probs<D, TILE> &lo, State<D, TILE> &st,
-                                              const Scores<D, TILE> &s, const Values<D, TILE> &v)
+template <int D, int ROWS, bool FINE>
+__device__ __forceinline__ void probabilities(Probs<D, ROWS> &hi, Probs<D, ROWS> &lo, State<D, ROWS> &st,
+                                              const Scores<D, ROWS> &s, const Values<D, ROWS> &v)
 {
-    using H = Shape<D, TILE>;
+    using H = Shape<D, ROWS>;
 #pragma unroll
     for (int i = 0; i < H::TG; i++) {
         const uint32_t *dv = reinterpret_cast<const uint32_t *>(&v.dm[i]);
@@ -381,20 +415,28 @@ __device__ __forceinline__ void probabilities(Probs<D, TILE> &hi, Probs<D, TILE>
 
 // O^T += V^T P^T, eight tokens of a lane a time: the codes of two tokens meet
 // in one word, from which pairs of codes are taken as operands.
-template <int D, int TILE, bool FINE>
-__device__ __forceinline__ void gather(State<D, TILE> &st, const Probs<D, TILE> &hi,
-                                       const Probs<D, TILE> &lo, const Values<D, TILE> &v, Masks mk, int lane)
+template <int D, int ROWS, bool FINE>
+__device__ __forceinline__ void gather(State<D, ROWS> &st, const Probs<D, ROWS> &hi,
+                                       const Probs<D, ROWS> &lo, const Values<D, ROWS> &v, Masks mk, int lane)
 {
-    using M = Mma<TILE>;
-    using H = Shape<D, TILE>;
-    const int part = lane % TILE / H::DW;
+    using M = Mma<ROWS>;
+    using H = Shape<D, ROWS>;
+    const int m = lane % H::WIDE, part = m / H::DW;
+    const uint32_t keep[2] = {m < ROWS ? ~0u : 0u, m < ROWS ? 0u : ~0u};      // COPIES 2: the half of the tokens that is the column's
 #pragma unroll
-    for (int i = 0; i < H::TG; i += 2) {
-        auto operand = [&](const Probs<D, TILE> &x) {
-            return h8{x[i][0][0], x[i][0][1], x[i][1][0], x[i][1][1],
-                      x[i + 1][0][0], x[i + 1][0][1], x[i + 1][1][0], x[i + 1][1][1]};
+    for (int i = 0; i < H::VG; i += 2) {
+        auto operand = [&](const Probs<D, ROWS> &x) {
+            uint4 w;
+            if constexpr (H::COPIES == 2) {
+                const uint32_t a = __builtin_bit_cast(uint32_t, x[0][0]), b = __builtin_bit_cast(uint32_t, x[0][1]);
+                w = make_uint4(a & keep[0], b & keep[0], a & keep[1], b & keep[1]);
+            } else {
+                w = make_uint4(__builtin_bit_cast(uint32_t, x[i][0]), __builtin_bit_cast(uint32_t, x[i][1]),
+                               __builtin_bit_cast(uint32_t, x[i + 1][0]), __builtin_bit_cast(uint32_t, x[i + 1][1]));
+            }
+            return __builtin_bit_cast(h8, w);
         };
-        const h8 p = operand(hi);
+        const h8 p = operand(hi), rest = FINE ? operand(lo) : p;
 #pragma unroll
         for (int r = 0; r < H::REPS; r++) {
             uint32_t w[2][4];                                // [halves of a word][pairs of tokens]
@@ -422,59 +464,70 @@ __device__ __forceinline__ void gather(State<D, TILE> &st, const Probs<D, TILE> 
                     x[2 * c + 1] = z[1];
                 }
                 st.o[r * H::NT + n] = M::go(x, p, st.o[r * H::NT + n]);
-                if (FINE) st.o[r * H::NT + n] = M::go(x, operand(lo), st.o[r * H::NT + n]);
+                if (FINE) st.o[r * H::NT + n] = M::go(x, rest, st.o[r * H::NT + n]);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
     }
 }
 
-// The row's query as matrix operand (in st or, for the workgroup, in sq) and
-// the factors of its scores.
-template <int D, int TILE, class T>
-__device__ __forceinline__ void load_query(State<D, TILE> &st, h8 *sq, const KvAttend &a, const RowTile &t, int head,
-                                           int wave, int lane)
+// A lane's part of its row's query.
+template <int D, int ROWS, class T>
+struct Query {
+    T x[Shape<D, ROWS>::PER][8];
+};
+
+template <int D, int ROWS, class T>
+__device__ __forceinline__ void load_query(Query<D, ROWS, T> &o, const KvAttend &a, const RowTile &t, int head, int lane)
 {
-    using H = Shape<D, TILE>;
-    const int m = lane % TILE, g = lane / TILE;
-    const int r = t.r0 + min(m, t.rows - 1), tok = r / a.group, h = head * a.group + r % a.group;
-    const T *p = static_cast<const T *>(a.q.data) + (int64_t)(t.row0 + tok) * a.q.token + (int64_t)h * a.q.head +
-                 g * (H::PER * 8);
-    T x[H::PER][8];
+    using H = Shape<D, ROWS>;
+    const int m = lane % H::WIDE, g = lane / H::WIDE;
+    const int2 at = token_of(a, t, min(m % ROWS, t.rows - 1));
+    const T *p = static_cast<const T *>(a.q.data) + (int64_t)(t.row0 + at.x) * a.q.token +
+                 (int64_t)(head * a.group + at.y) * a.q.head + g * (H::PER * 8);
 #pragma unroll
     for (int j = 0; j < H::PER; j++) {
         if (a.q.wide) {
-            *reinterpret_cast<uint4 *>(x[j]) = *reinterpret_cast<const uint4 *>(p + 8 * j);
+            *reinterpret_cast<uint4 *>(o.x[j]) = *reinterpret_cast<const uint4 *>(p + 8 * j);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; i++) x[j][i] = p[8 * j + i];
+            for (int i = 0; i < 8; i++) o.x[j][i] = p[8 * j + i];
         }
     }
-    float top = 0.0f;
-    double sum = 0.0;            // its error would be common to all tokens of the row, times m
+}
+
+// The row's query as matrix operand (in st or, for the workgroup, in sq) and
+// the factors of its scores.
+template <int D, int ROWS, class T>
+__device__ __forceinline__ void set_query(State<D, ROWS> &st, h8 *sq, const Query<D, ROWS, T> &q, float scale, int wave,
+                                          int lane)
+{
+    using H = Shape<D, ROWS>;
+    float top = 0.0f, sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < H::PER; j++)
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-            top = fmaxf(top, fabsf((float)x[j][i]));
-            sum += (float)x[j][i];
+            top = fmaxf(top, fabsf((float)q.x[j][i]));
+            sum += (float)q.x[j][i];
         }
 #pragma unroll
-    for (int o = TILE; o < 64; o *= 2) {
+    for (int o = H::WIDE; o < 64; o *= 2) {
         top = fmaxf(top, __shfl_xor(top, o));
         sum += __shfl_xor(sum, o);
     }
     // the largest element goes to [2^14, 2^15); an infinity stays one and
     // makes the row NaN, as its scores are
     const int e = top > 0.0f ? (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127 : 0;
-    st.qs = a.scale * 1.44269504088896341f * ldexpf(1.0f, e - 14);
-    st.qsum = ldexpf((float)sum, 14 - e);
+    st.qs = scale * 1.44269504088896341f * ldexpf(1.0f, e - 14);
+    st.qsum = ldexpf(sum, 14 - e);
 #pragma unroll
     for (int j = 0; j < H::PER; j++) {
         constexpr int order[8] = {0, 4, 1, 5, 2, 6, 3, 7};
         h8 y;
 #pragma unroll
-        for (int i = 0; i < 8; i++) y[i] = (_Float16)ldexpf((float)x[j][order[i]], 14 - e - (order[i] % 2 ? 4 : 0));
+        for (int i = 0; i < 8; i++)
+            y[i] = (_Float16)ldexpf((float)q.x[j][order[i]], 14 - e - (order[i] % 2 ? 4 : 0));
         if constexpr (H::QREG)
             st.q[j] = y;
         else if (wave == j % NW)
@@ -482,20 +535,21 @@ __device__ __forceinline__ void load_query(State<D, TILE> &st, h8 *sq, const KvA
     }
 }
 
-// Partial results of the call's row tile (x, head) and chunk z: [TILE] rows of
-// D values, then [TILE] of (mo, l).
-template <int D, int TILE>
+// Partial results of the call's row tile (x, head) and chunk z: [ROWS] rows of
+// D values, then [ROWS] of (mo, l).
+template <int D, int ROWS>
 __device__ __forceinline__ float *part_of(const KvAttend &a, int64_t x, int head, int z)
 {
-    return a.part + (((x * a.g.kv_heads + head) * a.splits) + z) * (TILE * (D + 2));
+    return a.part + (((x * a.g.kv_heads + head) * a.splits) + z) * (ROWS * (D + 2));
 }
 
 template <int D, class T>
 __device__ __forceinline__ void write_row(const KvAttend &a, const RowTile &t, int head, int r, int d0, const float *y,
                                           float l, float mo)
 {
-    const int row = t.r0 + r, tok = t.row0 + row / a.group, h = head * a.group + row % a.group;
-    T *p = static_cast<T *>(a.out.data) + (int64_t)tok * a.out.token + (int64_t)h * a.out.head + d0;
+    const int2 at = token_of(a, t, r);
+    const int64_t tok = t.row0 + at.x, h = (int64_t)head * a.group + at.y;
+    T *p = static_cast<T *>(a.out.data) + tok * a.out.token + h * a.out.head + d0;
     T e[8];
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
@@ -509,44 +563,32 @@ __device__ __forceinline__ void write_row(const KvAttend &a, const RowTile &t, i
     if (a.lse && d0 == 0) {
         int e = 0;                                           // l's power of two joins mo exactly
         const float f = frexpf(l, &e);
-        a.lse[(int64_t)tok * ((int64_t)a.g.kv_heads * a.group) + h] =
+        a.lse[tok * ((int64_t)a.g.kv_heads * a.group) + h] =
             l == 0.0f ? -__builtin_inff() : (__builtin_amdgcn_logf(f) + ((float)e + mo)) * 0.693147180559945309f;
     }
 }
 
-template <int D, int TILE, class T>
-__global__ __launch_bounds__(NW * 64, (WAVES<D, TILE>)) void k_kv_attend(KvAttend a)
+template <int D, int ROWS, class T>
+__global__ __launch_bounds__(NW * 64, (WAVES<D, ROWS>)) void k_kv_attend(KvAttend a)
 {
-    using M = Mma<TILE>;
-    using S = State<D, TILE>;
-    using H = Shape<D, TILE>;
+    using M = Mma<ROWS>;
+    using S = State<D, ROWS>;
+    using H = Shape<D, ROWS>;
     constexpr bool FINE = std::is_same<T, _Float16>::value;
-    __shared__ __align__(16) float so[NW * TILE * H::ROWF];
-    __shared__ float sl[NW][TILE], sm[NW][TILE];
+    __shared__ __align__(16) float so[NW * H::WIDE * H::ROWF];
+    __shared__ float sl[NW * H::WIDE], sm[NW * H::WIDE];     // by wavefront and column
     h8 *sq = reinterpret_cast<h8 *>(so);                     // the loop's; so is the end's
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int m = lane % TILE, g = lane / TILE, head = blockIdx.y;
-    const int x = gridDim.x - 1 - blockIdx.x;                // later rows see more tokens: they go first
-    const RowTile t = row_tile<TILE>(a, x);
+    const int m = lane % H::WIDE, g = lane / H::WIDE, head = blockIdx.y;
+    const int split = blockIdx.x, x = tile_at(gridDim.z, blockIdx.z);
+    const RowTile t = row_tile<ROWS>(a, x);
     if (t.rows == 0) return;
-    Span mine = chunk_of(a, t, blockIdx.z);
+    Span mine = chunk_of(a, t, split);
     if (a.g.n_pages == 0) mine.hi = mine.lo;                 // nothing to load from
-    if (blockIdx.z > 0 && mine.lo >= mine.hi) return;        // (chunk 0 always leaves a result)
+    if (split > 0 && mine.lo >= mine.hi) return;             // (chunk 0 always leaves a result)
 
-    State<D, TILE> st;
-    load_query<D, TILE, T>(st, sq, a, t, head, wave, lane);
-    if (!H::QREG) __syncthreads();
-    st.mrow = st.mo = NONE;
-    st.thr = NONE / fmaxf(st.qs, 1.0f);
-    st.dlim = 0;
-    st.l = st.z = 0.0f;
-#pragma unroll
-    for (int i = 0; i < S::TILES; i++)
-#pragma unroll
-        for (int j = 0; j < M::ACC; j++) st.o[i][j] = 0.0f;
-
-    const Span seen = span_of<TILE>(a, t, m);
-    const Span head_row = span_of<TILE>(a, t, 0), last_row = span_of<TILE>(a, t, t.rows - 1);
+    const Span seen = span_of(a, t, m % ROWS);
+    const Span head_row = span_of(a, t, 0), last_row = span_of(a, t, t.rows - 1);
     const int all_lo = last_row.lo, all_hi = head_row.hi;     // tokens every row sees
     const int P = 1 << a.g.page_shift;
     // (the table's entry of a step past the end is the last one's again)
@@ -563,36 +605,65 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, TILE>)) void k_kv_attend(KvAtten
     // around the loads.  A step's keys are loaded once the scores have used
     // up the last step's, its values after the second product, so both are
     // under way for most of a step and need no second set of registers.
-    if (mine.lo + wave * STEP < mine.hi) {
-        int t0 = mine.lo + wave * STEP;
-        int32_t page = __builtin_amdgcn_readfirstlane(entry_at(t0)), after = entry_at(t0 + HOP);
-        Keys<D, TILE> k;
-        Values<D, TILE> v;
-        load_keys<D, TILE>(k, block_of(page), P, t0 & (P - 1), lane);
-        load_values<D, TILE>(v, block_of(page), P, t0 & (P - 1), lane);
+    State<D, ROWS> st;
+    Keys<D, ROWS> k;
+    Values<D, ROWS> v;
+    int t0 = mine.lo + wave * STEP;
+    const bool any = t0 < mine.hi;
+    int32_t page = -1, after = -1;
+    {
+        Query<D, ROWS, T> q;
+        load_query<D, ROWS, T>(q, a, t, head, lane);
+        if (any) {
+            // (the loads' order is the loop's, or its waits would fit neither)
+            page = __builtin_amdgcn_readfirstlane(entry_at(t0));
+            after = entry_at(t0 + HOP);
+            load_keys<D, ROWS>(k, block_of(page), P, t0 & (P - 1), lane);
+            asm volatile("" ::: "memory");
+            load_values<D, ROWS>(v, block_of(page), P, t0 & (P - 1), lane);
+            asm volatile("" ::: "memory");
+        }
+        set_query<D, ROWS, T>(st, sq, q, a.scale, wave, lane);
+    }
+    if (!H::QREG) __syncthreads();
+    st.mrow = st.mo = NONE;
+    st.thr = NONE / fmaxf(st.qs, 1.0f);
+    st.dlim = 0;
+    st.l = st.z = 0.0f;
+#pragma unroll
+    for (int i = 0; i < S::TILES; i++)
+#pragma unroll
+        for (int j = 0; j < M::ACC; j++) st.o[i][j] = 0.0f;
+    if (any) {
         do {
             const int32_t ahead = __builtin_amdgcn_readfirstlane(after);
             after = entry_at(t0 + 2 * HOP);
             const uint8_t *block = block_of(ahead);
             const int tn = (t0 + HOP) & (P - 1);
-            Scores<D, TILE> s;
-            Probs<D, TILE> hi, lo;
-            scores<D, TILE>(s, st, sq + lane, k, mk);
+            Scores<D, ROWS> s;
+            Probs<D, ROWS> hi, lo;
+            scores<D, ROWS>(s, st, sq + lane, k, mk, lane);
             // the scores are done here, not where they are used, so that the
             // keys' registers are free
 #pragma unroll
             for (int i = 0; i < H::TG; i++)
 #pragma unroll
                 for (int b = 0; b < 4; b++) asm volatile("" : "+v"(s[i][b]));
-            load_keys<D, TILE>(k, block, P, tn, lane);
+            load_keys<D, ROWS>(k, block, P, tn, lane);
             if (!present(page))
-                hide<D, TILE>(s, v, t0, Span{0, 0}, lane);
-            else if (t0 < all_lo || t0 + STEP > all_hi || t.rows < TILE)
-                hide<D, TILE>(s, v, t0, seen, lane);
-            fit<D, TILE>(st, s, v);
-            probabilities<D, TILE, FINE>(hi, lo, st, s, v);
-            gather<D, TILE, FINE>(st, hi, lo, v, mk, lane);
-            load_values<D, TILE>(v, block, P, tn, lane);
+                hide<D, ROWS>(s, v, t0, Span{0, 0}, lane);
+            else if (t0 < all_lo || t0 + STEP > all_hi || t.rows < ROWS)
+                hide<D, ROWS>(s, v, t0, seen, lane);
+            fit<D, ROWS>(st, s, v);
+            probabilities<D, ROWS, FINE>(hi, lo, st, s, v);
+            // the values are unpacked here, not above the branch in fit()
+#pragma unroll
+            for (int i = 0; i < H::VG; i++)
+#pragma unroll
+                for (int r = 0; r < H::REPS; r++)
+                    asm volatile("" : "+v"(v.w[i][r].x), "+v"(v.w[i][r].y), "+v"(v.w[i][r].z), "+v"(v.w[i][r].w));
+            gather<D, ROWS, FINE>(st, hi, lo, v, mk, lane);
+            load_values<D, ROWS>(v, block, P, tn, lane);
             asm volatile("" ::: "memory");                   // (or they are moved to the next step's start)
             t0 += HOP;
             page = ahead;
@@ -601,19 +672,20 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, TILE>)) void k_kv_attend(KvAtten
 
     // the lanes that share a row, then the wavefronts
 #pragma unroll
-    for (int o = TILE; o < 64; o *= 2) {
+    for (int o = Mma<ROWS>::WIDE; o < 64; o *= 2) {
         st.l += __shfl_xor(st.l, o);
         st.z += __shfl_xor(st.z, o);
     }
     if (g == 0) {
-        sl[wave][m] = st.l;
-        sm[wave][m] = st.mo;
+        sl[wave * H::WIDE + m] = st.l;
+        sm[wave * H::WIDE + m] = st.mo;
     }
     __syncthreads();
-    float mo = sm[0][m];
+    constexpr int MEET = NW * H::COPIES;                     // results of a row, at every ROWS entries
+    float mo = sm[m % ROWS];
 #pragma unroll
-    for (int w = 1; w < NW; w++) mo = fmaxf(mo, sm[w][m]);
-    float *part = a.splits > 1 ? part_of<D, TILE>(a, x, head, blockIdx.z) : nullptr;
+    for (int w = 1; w < MEET; w++) mo = fmaxf(mo, sm[w * ROWS + m % ROWS]);
+    float *part = a.splits > 1 ? part_of<D, ROWS>(a, x, head, split) : nullptr;
     const float f = __builtin_amdgcn_exp2f(st.mo - mo), fixed = st.z * f;
 #pragma unroll
     for (int pass = 0; pass < H::PASSES; pass++) {
@@ -623,32 +695,32 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, TILE>)) void k_kv_attend(KvAtten
 #pragma unroll
             for (int j = 0; j < M::ACC; j++) {
                 const int r = i / H::NT, n = i % H::NT;
-                const int row = TILE == 16 ? 4 * g + j : 8 * (j / 4) + 4 * g + j % 4;     // along the head
-                const int d = 8 * (row % H::DW + r * TILE) + (row / H::DW) * H::NT + n;
+                const int row = H::WIDE == 16 ? 4 * g + j : 8 * (j / 4) + 4 * g + j % 4;  // along the head
+                const int d = 8 * (row % H::DW + r * H::WIDE) + (row / H::DW) * H::NT + n;
                 // (a pass is the first or second half of j, or of r)
                 if (H::PASSES > 1 && (H::REPS > 1 ? r : j / (M::ACC / 2)) != pass) continue;
-                so[(wave * TILE + m) * H::ROWF + d % H::PD] = fmaf(st.o[i][j], n % 2 ? 0x1p-4f * f : f, fixed);
+                so[(wave * H::WIDE + m) * H::ROWF + d % H::PD] = fmaf(st.o[i][j], n % 2 ? 0x1p-4f * f : f, fixed);
             }
         __syncthreads();
         for (int i = threadIdx.x; i < t.rows * (H::PD / 8); i += NW * 64) {
             const int r = i / (H::PD / 8), d0 = i % (H::PD / 8) * 8;
-            float y[8], top = sm[0][r], l = 0.0f;
+            float y[8], top = sm[r], l = 0.0f;
 #pragma unroll
-            for (int w = 1; w < NW; w++) top = fmaxf(top, sm[w][r]);
+            for (int w = 1; w < MEET; w++) top = fmaxf(top, sm[w * ROWS + r]);
 #pragma unroll
-            for (int w = 0; w < NW; w++) l += sl[w][r] * __builtin_amdgcn_exp2f(sm[w][r] - top);
+            for (int w = 0; w < MEET; w++) l += sl[w * ROWS + r] * __builtin_amdgcn_exp2f(sm[w * ROWS + r] - top);
 #pragma unroll
             for (int j = 0; j < 8; j++) y[j] = 0.0f;
 #pragma unroll
-            for (int w = 0; w < NW; w++)
+            for (int w = 0; w < MEET; w++)
 #pragma unroll
-                for (int j = 0; j < 8; j++) y[j] += so[(w * TILE + r) * H::ROWF + d0 + j];
+                for (int j = 0; j < 8; j++) y[j] += so[(w * ROWS + r) * H::ROWF + d0 + j];
             const int d = pass * H::PD + d0;
             if (part) {
 #pragma unroll
                 for (int j = 0; j < 8; j += 4)
                     *reinterpret_cast<float4 *>(part + r * D + d + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
-                if (d == 0) *reinterpret_cast<float2 *>(part + TILE * D + 2 * r) = make_float2(top, l);
+                if (d == 0) *reinterpret_cast<float2 *>(part + ROWS * D + 2 * r) = make_float2(top, l);
             } else {
                 write_row<D, T>(a, t, head, r, d, y, l, top);
             }
@@ -658,7 +730,7 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, TILE>)) void k_kv_attend(KvAtten
 
 // Joins the chunks of one row: D/8 threads take eight dimensions each, in
 // 2048/D slices that take the chunks in turn and meet in LDS.
-template <int D, int TILE, class T>
+template <int D, int ROWS, class T>
 __global__ __launch_bounds__(256) void k_kv_join(KvAttend a)
 {
     constexpr int C = D / 8, SLICES = 256 / C;
@@ -666,7 +738,7 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttend a)
     __shared__ float2 sml[SLICES];
     const int64_t x = blockIdx.x;
     const int head = blockIdx.y, r = blockIdx.z;
-    const RowTile t = row_tile<TILE>(a, (int)x);
+    const RowTile t = row_tile<ROWS>(a, (int)x);
     if (r >= t.rows) return;
     const int used = max(min((t.hi - t.lo + a.chunk - 1) / a.chunk, a.splits), 1);
     const int slice = threadIdx.x / C, d0 = threadIdx.x % C * 8;
@@ -682,8 +754,8 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttend a)
         for (int j = 0; j < 8; j++) y[j] = y[j] * fo + v[j] * fn;
     };
     for (int z = slice; z < used; z += SLICES) {
-        const float *p = part_of<D, TILE>(a, x, head, z);
-        const float2 ml = *reinterpret_cast<const float2 *>(p + TILE * D + 2 * r);
+        const float *p = part_of<D, ROWS>(a, x, head, z);
+        const float2 ml = *reinterpret_cast<const float2 *>(p + ROWS * D + 2 * r);
         float v[8];
         *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(p + r * D + d0);
         *reinterpret_cast<float4 *>(v + 4) = *reinterpret_cast<const float4 *>(p + r * D + d0 + 4);
@@ -700,21 +772,21 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttend a)
     write_row<D, T>(a, t, head, r, d0, y, l, top);
 }
 
-template <int D, int TILE, class T>
+template <int D, int ROWS, class T>
 hipError_t launch(const KvAttend &a, const KvPlan &p, hipStream_t s)
 {
-    hipLaunchKernelGGL((k_kv_attend<D, TILE, T>), dim3((unsigned)p.tiles, a.g.kv_heads, p.splits), dim3(NW * 64), 0, s, a);
+    hipLaunchKernelGGL((k_kv_attend<D, ROWS, T>), dim3(p.splits, a.g.kv_heads, (unsigned)p.tiles), dim3(NW * 64), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
-    hipLaunchKernelGGL((k_kv_join<D, TILE, T>), dim3((unsigned)p.tiles, a.g.kv_heads, TILE), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_kv_join<D, ROWS, T>), dim3((unsigned)p.tiles, a.g.kv_heads, ROWS), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
 template <int D>
 hipError_t launch_dim(const KvAttend &a, int dtype, const KvPlan &p, hipStream_t s)
 {
-    if (p.tile == 16)
-        return dtype == LW_F16 ? launch<D, 16, _Float16>(a, p, s) : launch<D, 16, __bf16>(a, p, s);
+    if (p.tile == 8) return dtype == LW_F16 ? launch<D, 8, _Float16>(a, p, s) : launch<D, 8, __bf16>(a, p, s);
+    if (p.tile == 16) return dtype == LW_F16 ? launch<D, 16, _Float16>(a, p, s) : launch<D, 16, __bf16>(a, p, s);
     return dtype == LW_F16 ? launch<D, 32, _Float16>(a, p, s) : launch<D, 32, __bf16>(a, p, s);
 }
 
@@ -724,7 +796,7 @@ KvPlan lw_kv_plan(int head_dim, int kv_heads, int group, int64_t n_seqs, int64_t
                   int most)
 {
     KvPlan p;
-    p.tile = n_tokens * group <= 16 * n_seqs ? 16 : 32;
+    p.tile = n_tokens * group <= 8 * n_seqs ? 8 : n_tokens * group <= 16 * n_seqs ? 16 : 32;
     p.tiles = n_tokens * group / p.tile + n_seqs;
     // tokens a row tile may see
     int64_t span = max_len;

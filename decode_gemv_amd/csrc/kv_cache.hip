@@ -61,31 +61,30 @@ __device__ __forceinline__ void store8(T *p, int wide, const float *x)
     }
 }
 
+// The cached token of a packed row.
+struct Place {
+    bool known;                  // the row belongs to a sequence
+    int32_t pos;
+    int64_t page;                // < 0: the token is absent
+};
+
 // Where the row of each lane's vector lies.  The rows of a wavefront are
 // consecutive; each is looked up by the whole wavefront.
 template <int D>
-__device__ __forceinline__ KvPlace place(const KvGeom &g, int row0)
+__device__ __forceinline__ Place place(const KvGeom &g, int row0)
 {
     constexpr int LANES = D / 8, ROWS = 64 / LANES;
-    const int mine = (threadIdx.x & 63) / LANES;
-    KvPlace r = {-1, -1, -1};
+    const int mine = (threadIdx.x & 63) / LANES, row = row0 + mine;
+    KvSeq q = {-1, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < ROWS; i++) {
-        const int s = kv_count_le(g.n_seqs, row0 + i, [&](int k) { return g.start[k + 1]; });
-        if (i == mine) r.seq = s;
+        const KvSeq s = kv_find(g, row0 + i, [](int next, int) { return next; });
+        if (i == mine) q = s;
     }
-    const int row = row0 + mine;
-    if (row >= g.n_tokens || r.seq >= g.n_seqs) {
-        r.seq = -1;
-        return r;
-    }
-    const int2 rows = kv_rows(g, r.seq);
-    if (row < rows.x || row >= rows.y) {      // rows before start[0]
-        r.seq = -1;
-        return r;
-    }
-    r.pos = max(g.lens[r.seq], 0) - (rows.y - row);
-    r.page = kv_page(g, r.seq, r.pos);
+    Place r = {q.seq >= 0 && row >= q.row0 && row < q.row0 + q.n_new, 0, -1};
+    if (!r.known) return r;      // past the batch, or before its start
+    r.pos = q.len - (q.row0 + q.n_new - row);
+    r.page = kv_page(g, q.seq, r.pos);
     return r;
 }
 
@@ -103,7 +102,7 @@ __global__ __launch_bounds__(THREADS) void k_kv_append(KvGeom g, KvTensor k, KvT
     for (int i = 0; i < 8; i++) x[i] = 0.0f;
     if (row < g.n_tokens)
         load8(static_cast<const T *>(t.data) + row * t.token + blockIdx.y * t.head + w * 8, t.wide, x);
-    const KvPlace p = place<D>(g, row0);
+    const Place p = place<D>(g, row0);
     float lo = x[0], hi = x[0];
     bool fine = true;
 #pragma unroll
@@ -148,8 +147,8 @@ __global__ __launch_bounds__(THREADS) void k_kv_read(KvGeom g, KvTensor k, KvTen
     if (row0 >= g.n_tokens) return;
     const int row = row0 + (threadIdx.x & 63) / LANES;
     const KvTensor &t = blockIdx.z ? v : k;
-    const KvPlace p = place<D>(g, row0);
-    if (p.seq < 0) return;
+    const Place p = place<D>(g, row0);
+    if (!p.known) return;
     float x[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) x[i] = 0.0f;

@@ -124,7 +124,9 @@ extern "C" size_t lw_kv_attend_scratch_bytes(const lw_kv_cache *cache, const lw_
 {
     KvGeom g;
     if (geom(cache, batch, n_tokens, g) || !batch->n_seqs || !n_tokens) return 0;
-    if (q_heads < 1 || q_heads % cache->kv_heads || q_heads / cache->kv_heads > 1024) return 0;
+    if (q_heads < 1 || q_heads % cache->kv_heads || q_heads / cache->kv_heads > 1024 ||
+        n_tokens * (q_heads / cache->kv_heads) > (1 << 30))
+        return 0;
     return plan_of(cache, batch, n_tokens, q_heads, 0, INT_MAX).work_bytes;
 }
 
@@ -139,6 +141,8 @@ extern "C" lw_status lw_kv_attend(const lw_kv_cache *cache, const lw_kv_batch *b
     if (q_heads < 1 || q_heads % cache->kv_heads)
         return lw_fail(LW_E_ARG, "q_heads must be a positive multiple of kv_heads");
     if (q_heads / cache->kv_heads > 1024) return lw_fail(LW_E_ARG, "more than 1024 query heads per kv head");
+    if (n_tokens * (q_heads / cache->kv_heads) > (1 << 30))
+        return lw_fail(LW_E_ARG, "more than 2^30 query rows per kv head");
     if (!(scale > 0.0f) || !std::isfinite(scale)) return lw_fail(LW_E_ARG, "scale must be positive and finite");
     if (window < 0) return lw_fail(LW_E_ARG, "negative window");
     if (!batch->n_seqs || !n_tokens) return LW_OK;
@@ -150,9 +154,13 @@ extern "C" lw_status lw_kv_attend(const lw_kv_cache *cache, const lw_kv_batch *b
         const size_t fit = work ? work_bytes / (p.work_bytes / p.splits) : 0;
         p = plan_of(cache, batch, n_tokens, q_heads, window, fit < 1 ? 1 : (int)fit);
     }
+    if (p.tiles > 65535)
+        return lw_fail(LW_E_UNSUPPORTED, "more than 65535 tiles of query rows (n_seqs + n_tokens * q_heads / kv_heads / 32, "
+                                         "or / 8 for few rows a sequence)");
     a.lse = lse;
     a.part = static_cast<float *>(work);
     a.group = q_heads / cache->kv_heads;
+    a.group_inv = ((1u << 21) + (unsigned)a.group - 1) / (unsigned)a.group;
     a.causal = causal != 0;
     a.window = window;
     a.splits = p.splits;
