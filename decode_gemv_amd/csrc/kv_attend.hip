@@ -75,7 +75,7 @@ template <> struct Mma<32> {           // 32 x 32 x 16: lane = row/column l % 32
 };
 
 // Wavefronts a SIMD is to hold (the registers that leaves).
-template <int D, int ROWS> constexpr int WAVES = D <= 128 && ROWS <= 16 ? 3 : D * ROWS <= 4096 ? 2 : 1;
+template <int D, int ROWS> constexpr int WAVES = D * ROWS <= 1024 ? 4 : D * ROWS <= 2048 ? 3 : D * ROWS <= 4096 ? 2 : 1;
 
 __device__ __forceinline__ float half_lo(uint32_t w) { return (float)__builtin_bit_cast(h2, w)[0]; }
 __device__ __forceinline__ float half_hi(uint32_t w) { return (float)__builtin_bit_cast(h2, w)[1]; }
@@ -242,50 +242,64 @@ __device__ __forceinline__ int group_token(int i, int lane)
     return 4 * ((H::COPIES > 1 ? lane % H::WIDE / ROWS : i) * H::G + lane / H::WIDE);
 }
 
-// The loads of a step.  t0 is a multiple of 32, so a step's part of each
-// array starts at a uniform address, and a lane's place in it is the same for
-// all steps.
+// One head's part of a page as a buffer: its loads take a uniform offset (t0
+// is a multiple of 32, so a step's part of each array starts at one) and a
+// lane's own, which is the same for all steps; those of a buffer of no bytes
+// (absent pages, steps past the end) give zeros and cost no traffic, and need
+// no branch.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t *block, uint32_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(block), 0, bytes, 0x00027000);
+}
+
+template <class T>
+__device__ __forceinline__ T load_part(__amdgpu_buffer_rsrc_t b, uint32_t lane, uint32_t uniform)
+{
+    if constexpr (sizeof(T) == 16)
+        return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b128(b, lane, uniform, 0));
+    else
+        return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b64(b, lane, uniform, 0));
+}
+
 template <int D, int ROWS>
-__device__ __forceinline__ void load_keys(Keys<D, ROWS> &o, const uint8_t *block, int P, int t0, int lane)
+__device__ __forceinline__ void load_keys(Keys<D, ROWS> &o, __amdgpu_buffer_rsrc_t block, int P, int t0, int lane)
 {
     using H = Shape<D, ROWS>;
     constexpr int W = D >= 128 ? 4 : 2;
     const int m = lane % H::WIDE, g = lane / H::WIDE;
-    const uint8_t *w = block + t0 * (D / 2), *dm = block + P * D + t0 * 4;
 #pragma unroll
     for (int u = 0; u < H::SUB; u++)
 #pragma unroll
         for (int j = 0; j < H::PER; j += W) {
-            const uint8_t *p = w + (unsigned)(kv_kword<D>(m, g * H::PER) * 4 + kv_kword<D>(u * H::WIDE, j) * 4);
+            const uint32_t at = 4 * (kv_kword<D>(m, g * H::PER) + kv_kword<D>(u * H::WIDE, j));
             uint32_t *q = &o.w[u][j];
             if constexpr (W == 4) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(p);
+                const uint4 x = load_part<uint4>(block, at, t0 * (D / 2));
                 q[0] = x.x, q[1] = x.y, q[2] = x.z, q[3] = x.w;
             } else {
-                const uint2 x = *reinterpret_cast<const uint2 *>(p);
+                const uint2 x = load_part<uint2>(block, at, t0 * (D / 2));
                 q[0] = x.x, q[1] = x.y;
             }
         }
 #pragma unroll
     for (int i = 0; i < H::TG; i++)
-        o.dm[i] = *reinterpret_cast<const uint4 *>(dm + (unsigned)(4 * group_token<D, ROWS>(0, lane) + 16 * i * H::G));
+        o.dm[i] = load_part<uint4>(block, 4 * group_token<D, ROWS>(0, lane) + 16 * i * H::G, P * D + t0 * 4);
 }
 
 template <int D, int ROWS>
-__device__ __forceinline__ void load_values(Values<D, ROWS> &o, const uint8_t *block, int P, int t0, int lane)
+__device__ __forceinline__ void load_values(Values<D, ROWS> &o, __amdgpu_buffer_rsrc_t block, int P, int t0, int lane)
 {
     using H = Shape<D, ROWS>;
     const int m = lane % H::WIDE, g = lane / H::WIDE;
-    const uint8_t *w = block + P * (D / 2) + t0 * (D / 2), *dm = block + P * D + P * 4 + t0 * 4;
 #pragma unroll
     for (int i = 0; i < H::VG; i++)
 #pragma unroll
         for (int r = 0; r < H::REPS; r++)
-            o.w[i][r] = *reinterpret_cast<const uint4 *>(w + (unsigned)((g * H::DW + m % H::DW) * 16 +
-                                                                        (i * H::G * H::DW + r * H::WIDE) * 16));
+            o.w[i][r] = load_part<uint4>(block, (g * H::DW + m % H::DW) * 16 + (i * H::G * H::DW + r * H::WIDE) * 16,
+                                         P * (D / 2) + t0 * (D / 2));
 #pragma unroll
     for (int i = 0; i < H::TG; i++)
-        o.dm[i] = *reinterpret_cast<const uint4 *>(dm + (unsigned)(4 * group_token<D, ROWS>(0, lane) + 16 * i * H::G));
+        o.dm[i] = load_part<uint4>(block, 4 * group_token<D, ROWS>(0, lane) + 16 * i * H::G, P * D + P * 4 + t0 * 4);
 }
 
 // One wavefront's running state for its row tile.  Sums are relative to 2^mo
@@ -584,7 +598,6 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, ROWS>)) void k_kv_attend(KvAtten
     const RowTile t = row_tile<ROWS>(a, x);
     if (t.rows == 0) return;
     Span mine = chunk_of(a, t, split);
-    if (a.g.n_pages == 0) mine.hi = mine.lo;                 // nothing to load from
     if (split > 0 && mine.lo >= mine.hi) return;             // (chunk 0 always leaves a result)
 
     const Span seen = span_of(a, t, m % ROWS);
@@ -595,22 +608,23 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, ROWS>)) void k_kv_attend(KvAtten
     const int32_t *pages = a.g.table + (int64_t)t.seq * a.g.stride;
     auto entry_at = [&](int t0) { return pages[min(t0, mine.hi - 1) >> a.g.page_shift]; };
     auto present = [&](int32_t entry) { return (uint32_t)entry < a.g.n_pages; };
-    auto block_of = [&](int32_t entry) {
-        return a.g.pages + (uint64_t)(present(entry) ? (uint32_t)entry : 0u) * (uint64_t)a.g.page_bytes +
-               (uint32_t)head * (uint32_t)a.g.block_bytes;
+    auto block_of = [&](int32_t entry, int t0) {
+        const bool there = present(entry) && t0 < mine.hi;
+        return buffer_of(a.g.pages + (uint64_t)(there ? (uint32_t)entry : 0u) * (uint64_t)a.g.page_bytes +
+                             (uint32_t)head * (uint32_t)a.g.block_bytes,
+                         there ? a.g.block_bytes : 0);
     };
     constexpr int HOP = NW * STEP;
     const Masks mk = masks();
-    // Absent pages and steps past the end load page 0, unused: no branches
-    // around the loads.  A step's keys are loaded once the scores have used
-    // up the last step's, its values after the second product, so both are
-    // under way for most of a step and need no second set of registers.
+    // A step's key registers are loaded anew once the
+    // scores have used them, its value registers after the second product, so
+    // both are under way nearly all the time.
     State<D, ROWS> st;
     Keys<D, ROWS> k;
     Values<D, ROWS> v;
+    int32_t page = -1, after = -1;
     int t0 = mine.lo + wave * STEP;
     const bool any = t0 < mine.hi;
-    int32_t page = -1, after = -1;
     {
         Query<D, ROWS, T> q;
         load_query<D, ROWS, T>(q, a, t, head, lane);
@@ -618,9 +632,9 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, ROWS>)) void k_kv_attend(KvAtten
             // (the loads' order is the loop's, or its waits would fit neither)
             page = __builtin_amdgcn_readfirstlane(entry_at(t0));
             after = entry_at(t0 + HOP);
-            load_keys<D, ROWS>(k, block_of(page), P, t0 & (P - 1), lane);
+            load_keys<D, ROWS>(k, block_of(page, t0), P, t0 & (P - 1), lane);
             asm volatile("" ::: "memory");
-            load_values<D, ROWS>(v, block_of(page), P, t0 & (P - 1), lane);
+            load_values<D, ROWS>(v, block_of(page, t0), P, t0 & (P - 1), lane);
             asm volatile("" ::: "memory");
         }
         set_query<D, ROWS, T>(st, sq, q, a.scale, wave, lane);
@@ -638,7 +652,7 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, ROWS>)) void k_kv_attend(KvAtten
         do {
             const int32_t ahead = __builtin_amdgcn_readfirstlane(after);
             after = entry_at(t0 + 2 * HOP);
-            const uint8_t *block = block_of(ahead);
+            const auto block = block_of(ahead, t0 + HOP);
             const int tn = (t0 + HOP) & (P - 1);
             Scores<D, ROWS> s;
             Probs<D, ROWS> hi, lo;
@@ -646,9 +660,9 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, ROWS>)) void k_kv_attend(KvAtten
             // the scores are done here, not where they are used, so that the
             // keys' registers are free
 #pragma unroll
-            for (int i = 0; i < H::TG; i++)
+            for (int n = 0; n < H::TG; n++)
 #pragma unroll
-                for (int b = 0; b < 4; b++) asm volatile("" : "+v"(s[i][b]));
+                for (int b = 0; b < 4; b++) asm volatile("" : "+v"(s[n][b]));
             load_keys<D, ROWS>(k, block, P, tn, lane);
             if (!present(page))
                 hide<D, ROWS>(s, v, t0, Span{0, 0}, lane);
@@ -658,10 +672,10 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, ROWS>)) void k_kv_attend(KvAtten
             probabilities<D, ROWS, FINE>(hi, lo, st, s, v);
             // the values are unpacked here, not above the branch in fit()
 #pragma unroll
-            for (int i = 0; i < H::VG; i++)
+            for (int n = 0; n < H::VG; n++)
 #pragma unroll
                 for (int r = 0; r < H::REPS; r++)
-                    asm volatile("" : "+v"(v.w[i][r].x), "+v"(v.w[i][r].y), "+v"(v.w[i][r].z), "+v"(v.w[i][r].w));
+                    asm volatile("" : "+v"(v.w[n][r].x), "+v"(v.w[n][r].y), "+v"(v.w[n][r].z), "+v"(v.w[n][r].w));
             gather<D, ROWS, FINE>(st, hi, lo, v, mk, lane);
             load_values<D, ROWS>(v, block, P, tn, lane);
             asm volatile("" ::: "memory");                   // (or they are moved to the next step's start)

@@ -13,24 +13,28 @@
 //
 // D/8 lanes hold a vector, eight elements each, so a lane makes one word of
 // codes and the extremes meet in log2(D/8) lane exchanges.  A workgroup takes
-// 16 or 32 consecutive rows of one head and one side: the words of 16 tokens
-// are 1 KiB of the cache in one piece (D = 128), written from one compute
-// unit.  Both kernels are bound by memory: nothing is read twice.
+// 2048/D consecutive rows and some of the heads, keys and values both: a row
+// is looked up once for all of them, and the words of 16 tokens, 1 KiB of the
+// cache in one piece at D = 128, come from one compute unit.  Both kernels
+// are bound by memory: nothing is read twice.
+#include <algorithm>
+#include <type_traits>
+
 #include "kv.h"
 
 namespace {
 
 constexpr int THREADS = 256;
 
-template <class T> struct Eight { T v[8]; };
-
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(_Float16 x) { return (float)x; }
 __device__ __forceinline__ float to_f(__bf16 x) { return (float)x; }
 
 // Eight consecutive elements: 16-byte accesses where the tensor allows them.
+template <class T> struct Eight { T v[8]; };
+
 template <class T>
-__device__ __forceinline__ void load8(const T *p, int wide, float *x)
+__device__ __forceinline__ Eight<T> load8(const T *p, int wide)
 {
     Eight<T> e;
     if (wide) {
@@ -41,129 +45,196 @@ __device__ __forceinline__ void load8(const T *p, int wide, float *x)
 #pragma unroll
         for (int i = 0; i < 8; i++) e.v[i] = p[i];
     }
-#pragma unroll
-    for (int i = 0; i < 8; i++) x[i] = to_f(e.v[i]);
+    return e;
 }
 
 template <class T>
-__device__ __forceinline__ void store8(T *p, int wide, const float *x)
+__device__ __forceinline__ void store8(T *p, int wide, const Eight<T> &e)
 {
-    Eight<T> e;
-#pragma unroll
-    for (int i = 0; i < 8; i++) e.v[i] = (T)x[i];
     if (wide) {
 #pragma unroll
         for (unsigned i = 0; i < sizeof(e) / 16; i++)
-            reinterpret_cast<uint4 *>(p)[i] = reinterpret_cast<uint4 *>(&e)[i];
+            reinterpret_cast<uint4 *>(p)[i] = reinterpret_cast<const uint4 *>(&e)[i];
     } else {
 #pragma unroll
         for (int i = 0; i < 8; i++) p[i] = e.v[i];
     }
 }
 
-// The cached token of a packed row.
+// f over x of the D/8 lanes that hold a vector.
+template <int D, class F>
+__device__ __forceinline__ float over_lanes(float x, F f)
+{
+    auto swap = [](float y, auto ctrl) {
+        return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, y), ctrl.value, 0xF, 0xF, false));
+    };
+    x = f(x, swap(x, std::integral_constant<int, 0xB1>{}));                   // lane ^ 1
+    x = f(x, swap(x, std::integral_constant<int, 0x4E>{}));                   // lane ^ 2
+    x = f(x, swap(x, std::integral_constant<int, 0x141>{}));                  // 7 - lane of eight
+    if (D >= 128) x = f(x, swap(x, std::integral_constant<int, 0x140>{}));    // 15 - lane of sixteen
+    if (D >= 256) x = f(x, __shfl_xor(x, 16));
+    return x;
+}
+
+// The cached token of a lane's row.
 struct Place {
     bool known;                  // the row belongs to a sequence
-    int32_t pos;
-    int64_t page;                // < 0: the token is absent
+    int32_t tok;                 // place in its page
+    uint8_t *page;               // null: the token is absent
 };
 
 // Where the row of each lane's vector lies.  The rows of a wavefront are
-// consecutive; each is looked up by the whole wavefront.
+// consecutive, mostly of one sequence.
 template <int D>
 __device__ __forceinline__ Place place(const KvGeom &g, int row0)
 {
     constexpr int LANES = D / 8, ROWS = 64 / LANES;
     const int mine = (threadIdx.x & 63) / LANES, row = row0 + mine;
-    KvSeq q = {-1, 0, 0, 0};
+    auto next_row = [](int next, int) { return next; };
+    KvSeq q = kv_find(g, row0, next_row);
+    if (q.seq >= 0 && row0 + ROWS > q.row0 + q.n_new) {
 #pragma unroll
-    for (int i = 0; i < ROWS; i++) {
-        const KvSeq s = kv_find(g, row0 + i, [](int next, int) { return next; });
-        if (i == mine) q = s;
+        for (int i = 1; i < ROWS; i++) {
+            const KvSeq s = kv_find(g, row0 + i, next_row);
+            if (i == mine) q = s;
+        }
     }
-    Place r = {q.seq >= 0 && row >= q.row0 && row < q.row0 + q.n_new, 0, -1};
+    Place r = {q.seq >= 0 && row >= q.row0 && row < q.row0 + q.n_new, 0, nullptr};
     if (!r.known) return r;      // past the batch, or before its start
-    r.pos = q.len - (q.row0 + q.n_new - row);
-    r.page = kv_page(g, q.seq, r.pos);
+    const int pos = q.len - (q.row0 + q.n_new - row);
+    const int64_t page = kv_page(g, q.seq, pos);
+    r.tok = pos & ((1 << g.page_shift) - 1);
+    if (page >= 0) r.page = g.pages + page * g.page_bytes;
     return r;
 }
 
+// Places in a head's block (words) of a token's word w and pair.
+template <int D>
+struct Slots {
+    int k, v, kdm, vdm;
+    __device__ __forceinline__ Slots(int P, int tok, int w)
+        : k(kv_kword<D>(tok, w)), v(P * (D / 8) + kv_vword<D>(tok, w)), kdm(P * (D / 4) + tok), vdm(kdm + P)
+    {
+    }
+};
+
+// A lane's word of codes of its vector, and the vector's pair.
 template <int D, class T>
-__global__ __launch_bounds__(THREADS) void k_kv_append(KvGeom g, KvTensor k, KvTensor v)
+__device__ __forceinline__ uint2 quantise(const Eight<T> &e)
 {
-    constexpr int LANES = D / 8, ROWS = 64 / LANES;
-    const int w = threadIdx.x % LANES;
-    const int row0 = blockIdx.x * (THREADS / LANES) + (threadIdx.x >> 6) * ROWS;
-    if (row0 >= g.n_tokens) return;
-    const int row = row0 + (threadIdx.x & 63) / LANES;
-    const KvTensor &t = blockIdx.z ? v : k;
     float x[8];
 #pragma unroll
-    for (int i = 0; i < 8; i++) x[i] = 0.0f;
-    if (row < g.n_tokens)
-        load8(static_cast<const T *>(t.data) + row * t.token + blockIdx.y * t.head + w * 8, t.wide, x);
-    const Place p = place<D>(g, row0);
-    float lo = x[0], hi = x[0];
-    bool fine = true;
+    for (int i = 0; i < 8; i++) x[i] = to_f(e.v[i]);
+    float lo = x[0], hi = x[0], odd = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
         lo = fminf(lo, x[i]);
         hi = fmaxf(hi, x[i]);
-        fine &= fabsf(x[i]) < __builtin_inff();
+        odd = fmaf(x[i], 0.0f, odd);                          // NaN for a NaN or an infinity, else 0
     }
-    int bad = !fine;
-#pragma unroll
-    for (int o = 1; o < LANES; o *= 2) {
-        lo = fminf(lo, __shfl_xor(lo, o));
-        hi = fmaxf(hi, __shfl_xor(hi, o));
-        bad |= __shfl_xor(bad, o);
-    }
-    if (p.page < 0) return;
+    lo = over_lanes<D>(lo, [](float a, float b) { return fminf(a, b); });
+    hi = over_lanes<D>(hi, [](float a, float b) { return fmaxf(a, b); });
+    constexpr uint64_t GROUP = D == 256 ? 0xFFFFFFFFu : (1u << (D / 8)) - 1;
+    const bool bad = (__ballot(!(odd == 0.0f)) >> (threadIdx.x & 63 & ~(D / 8 - 1)) & GROUP) != 0;
     _Float16 m = (_Float16)fminf(fmaxf(-lo, -65504.0f), 65504.0f);
     _Float16 d = (_Float16)fminf((hi - lo) * (1.0f / 15.0f), 65504.0f);
-    if (bad) d = m = (_Float16)__builtin_nanf("");
     const float inv = (float)d == 0.0f ? 0.0f : 1.0f / (float)d;
-    uint32_t word = 0;
+    float half[2];
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const float q = fminf(fmaxf(rintf((x[i] + (float)m) * inv), 0.0f), 15.0f);
-        word |= (bad ? 0u : (uint32_t)q) << (4 * i);
+    for (int i = 0; i < 2; i++) {
+        float q[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) q[j] = fminf(fmaxf(rintf((x[4 * i + j] + (float)m) * inv), 0.0f), 15.0f);
+        half[i] = fmaf(q[3], 4096.0f, fmaf(q[2], 256.0f, fmaf(q[1], 16.0f, q[0])));      // 16 bits, exact
     }
-    const int P = 1 << g.page_shift, tok = p.pos & (P - 1);
-    uint32_t *block = reinterpret_cast<uint32_t *>(g.pages + p.page * g.page_bytes +
-                                                   (int64_t)blockIdx.y * g.block_bytes);
-    block[blockIdx.z ? P * (D / 8) + kv_vword<D>(tok, w) : kv_kword<D>(tok, w)] = word;
-    if (w == 0)
-        block[P * (D / 4) + (blockIdx.z ? P : 0) + tok] =
-            __builtin_bit_cast(uint16_t, d) | (uint32_t)__builtin_bit_cast(uint16_t, m) << 16;
+    if (bad) {
+        d = m = (_Float16)__builtin_nanf("");
+        half[0] = half[1] = 0.0f;
+    }
+    return make_uint2((uint32_t)half[0] | (uint32_t)half[1] << 16,
+                      __builtin_bit_cast(uint16_t, d) | (uint32_t)__builtin_bit_cast(uint16_t, m) << 16);
+}
+
+// d q - m of a word's eight codes.
+template <class T>
+__device__ __forceinline__ Eight<T> dequantise(uint32_t word, uint32_t dm)
+{
+    const float d = (float)__builtin_bit_cast(_Float16, (uint16_t)dm);
+    const float m = (float)__builtin_bit_cast(_Float16, (uint16_t)(dm >> 16));
+    const uint32_t q[2] = {word & 0x0F0F0F0Fu, word >> 4 & 0x0F0F0F0Fu};
+    Eight<T> e;
+#pragma unroll
+    for (int i = 0; i < 8; i++) e.v[i] = (T)fmaf((float)(q[i % 2] >> (i / 2 * 8) & 0xFFu), d, -m);   // d q is exact
+    return e;
 }
 
 template <int D, class T>
-__global__ __launch_bounds__(THREADS) void k_kv_read(KvGeom g, KvTensor k, KvTensor v)
+__global__ __launch_bounds__(THREADS) void k_kv_append(KvGeom g, KvTensor k, KvTensor v, int per)
+{
+    constexpr int LANES = D / 8, ROWS = 64 / LANES;
+    const int w = threadIdx.x % LANES;
+    const int row0 = blockIdx.x * (THREADS / LANES) + (threadIdx.x >> 6) * ROWS;
+    if (row0 >= g.n_tokens) return;
+    const int row = min(row0 + (int)(threadIdx.x & 63) / LANES, g.n_tokens - 1);
+    const int h0 = blockIdx.y * per, h1 = min(h0 + per, g.kv_heads);
+    const T *pk = static_cast<const T *>(k.data) + row * k.token + h0 * k.head + w * 8;
+    const T *pv = static_cast<const T *>(v.data) + row * v.token + h0 * v.head + w * 8;
+    Eight<T> xk = load8(pk, k.wide), xv = load8(pv, v.wide);
+    const Place p = place<D>(g, row0);
+    const Slots<D> at(1 << g.page_shift, p.tok, w);
+    uint8_t *block = p.page + (int64_t)h0 * g.block_bytes;
+    for (int h = h0; h < h1; h++) {
+        const Eight<T> ck = xk, cv = xv;
+        if (h + 1 < h1) {                                     // the next head's, while this one is worked on
+            pk += k.head;
+            pv += v.head;
+            xk = load8(pk, k.wide);
+            xv = load8(pv, v.wide);
+        }
+        const uint2 qk = quantise<D>(ck), qv = quantise<D>(cv);
+        if (p.page) {
+            uint32_t *to = reinterpret_cast<uint32_t *>(block);
+            to[at.k] = qk.x;
+            to[at.v] = qv.x;
+            if (w == 0) {
+                to[at.kdm] = qk.y;
+                to[at.vdm] = qv.y;
+            }
+        }
+        block += g.block_bytes;
+    }
+}
+
+template <int D, class T>
+__global__ __launch_bounds__(THREADS) void k_kv_read(KvGeom g, KvTensor k, KvTensor v, int per)
 {
     constexpr int LANES = D / 8, ROWS = 64 / LANES;
     const int w = threadIdx.x % LANES;
     const int row0 = blockIdx.x * (THREADS / LANES) + (threadIdx.x >> 6) * ROWS;
     if (row0 >= g.n_tokens) return;
     const int row = row0 + (threadIdx.x & 63) / LANES;
-    const KvTensor &t = blockIdx.z ? v : k;
+    const int h0 = blockIdx.y * per, h1 = min(h0 + per, g.kv_heads);
     const Place p = place<D>(g, row0);
     if (!p.known) return;
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 8; i++) x[i] = 0.0f;
-    if (p.page >= 0) {
-        const int P = 1 << g.page_shift, tok = p.pos & (P - 1);
-        const uint32_t *block = reinterpret_cast<const uint32_t *>(g.pages + p.page * g.page_bytes +
-                                                                   (int64_t)blockIdx.y * g.block_bytes);
-        const uint32_t word = block[blockIdx.z ? P * (D / 8) + kv_vword<D>(tok, w) : kv_kword<D>(tok, w)];
-        const uint32_t dm = block[P * (D / 4) + (blockIdx.z ? P : 0) + tok];
-        const float d = (float)__builtin_bit_cast(_Float16, (uint16_t)dm);
-        const float m = (float)__builtin_bit_cast(_Float16, (uint16_t)(dm >> 16));
-#pragma unroll
-        for (int i = 0; i < 8; i++) x[i] = fmaf((float)(word >> (4 * i) & 15u), d, -m);   // d q is exact in fp32
+    const Slots<D> at(1 << g.page_shift, p.tok, w);
+    T *pk = static_cast<T *>(k.data) + row * k.token + h0 * k.head + w * 8;
+    T *pv = static_cast<T *>(v.data) + row * v.token + h0 * v.head + w * 8;
+    const uint8_t *block = p.page + (int64_t)h0 * g.block_bytes;
+    uint4 x = make_uint4(0, 0, 0, 0);                         // an absent token's: zeros
+    auto load = [&]() {
+        const uint32_t *from = reinterpret_cast<const uint32_t *>(block);
+        if (p.page) x = make_uint4(from[at.k], from[at.kdm], from[at.v], from[at.vdm]);
+    };
+    load();
+    for (int h = h0; h < h1; h++) {
+        const uint4 c = x;
+        block += g.block_bytes;
+        if (h + 1 < h1) load();                               // the next head's, while this one is worked on
+        store8(pk, k.wide, dequantise<T>(c.x, c.y));
+        store8(pv, v.wide, dequantise<T>(c.z, c.w));
+        pk += k.head;
+        pv += v.head;
     }
-    store8(static_cast<T *>(t.data) + row * t.token + blockIdx.y * t.head + w * 8, t.wide, x);
 }
 
 template <class F>
@@ -181,11 +252,18 @@ hipError_t with_types(int head_dim, int dtype, F f)
     return hipErrorInvalidValue;
 }
 
-dim3 grid_of(const KvGeom &g, int head_dim)
-{
-    const int rows = THREADS / (head_dim / 8);
-    return dim3((unsigned)((g.n_tokens + rows - 1) / rows), (unsigned)g.kv_heads, 2);
-}
+// Workgroups by rows and heads: as many heads each as leave the chip full.
+struct Cut {
+    dim3 grid;
+    int per;
+    Cut(const KvGeom &g, int head_dim)
+    {
+        const int rows = THREADS / (head_dim / 8);
+        const int64_t blocks = (g.n_tokens + rows - 1) / rows;
+        per = (int)std::min<int64_t>(g.kv_heads, std::max<int64_t>(1, blocks * g.kv_heads / 2048));
+        grid = dim3((unsigned)blocks, (unsigned)((g.kv_heads + per - 1) / per));
+    }
+};
 
 }  // namespace
 
@@ -193,7 +271,8 @@ hipError_t lw_launch_kv_append(const KvGeom &g, int head_dim, const KvTensor &k,
                                hipStream_t s)
 {
     return with_types(head_dim, dtype, [&](auto dim, auto type) {
-        hipLaunchKernelGGL((k_kv_append<dim.value, decltype(type)>), grid_of(g, head_dim), dim3(THREADS), 0, s, g, k, v);
+        const Cut c(g, head_dim);
+        hipLaunchKernelGGL((k_kv_append<dim.value, decltype(type)>), c.grid, dim3(THREADS), 0, s, g, k, v, c.per);
         return hipGetLastError();
     });
 }
@@ -202,7 +281,8 @@ hipError_t lw_launch_kv_read(const KvGeom &g, int head_dim, const KvTensor &k, c
                              hipStream_t s)
 {
     return with_types(head_dim, dtype, [&](auto dim, auto type) {
-        hipLaunchKernelGGL((k_kv_read<dim.value, decltype(type)>), grid_of(g, head_dim), dim3(THREADS), 0, s, g, k, v);
+        const Cut c(g, head_dim);
+        hipLaunchKernelGGL((k_kv_read<dim.value, decltype(type)>), c.grid, dim3(THREADS), 0, s, g, k, v, c.per);
         return hipGetLastError();
     });
 }

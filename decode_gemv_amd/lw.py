@@ -339,8 +339,12 @@ def lw_last_error() -> str:
 
 def _stream(stream):
     import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return C.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return C.c_void_p(stream.cuda_stream)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)      # the handle without a Stream object: 0.3 us, not 3
+    if raw is not None and torch.cuda.is_initialized():
+        return C.c_void_p(raw(torch.cuda.current_device()))
+    return C.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
 def _dptr(t, what):
@@ -527,42 +531,53 @@ class KvBatch:
 _KV_TYPES = {}
 
 
-def _kv_tensor(t, what: str, heads: int, cache: KvCache):
-    """(descriptor, dtype) of a packed device tensor [n][heads][head_dim] with any row and head strides."""
+def _kv_types():
     import torch
-    if not _KV_TYPES:
-        _KV_TYPES.update({torch.float16: LW_F16, torch.bfloat16: LW_BF16, torch.float32: LW_F32})
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3:
-        raise LwError(LW_E_ARG, f"{what} must be a device tensor [tokens][heads][head_dim]")
-    if t.shape[1] != heads or t.shape[2] != cache.head_dim:
-        raise LwError(LW_E_ARG, f"{what} must be [tokens][{heads}][{cache.head_dim}]")
-    s0, s1, s2 = t.stride()
-    if s2 != 1:
-        raise LwError(LW_E_ARG, f"{what} must have its head vectors contiguous")
-    kind = _KV_TYPES.get(t.dtype)
+    _KV_TYPES.update({torch.float16: LW_F16, torch.bfloat16: LW_BF16, torch.float32: LW_F32})
+    return _KV_TYPES
+
+
+def _kv_tensor(t, what: str, cache: KvCache, like=None):
+    """Descriptor of a packed device tensor [n][heads][head_dim] with any row and head strides, of like's shape and
+    type where that is given."""
+    try:
+        shape, (s0, s1, s2), ok = t.shape, t.stride(), t.is_cuda
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok or shape[2] != cache.head_dim or s2 != 1:
+        raise LwError(LW_E_ARG, f"{what} must be a device tensor [tokens][heads][{cache.head_dim}] with contiguous "
+                                "head vectors")
+    if like is not None and (shape != like.shape or t.dtype != like.dtype):
+        raise LwError(LW_E_ARG, f"{what} must have the shape and type of the tensor before it")
+    return lw_kv_tensor(t.data_ptr(), s0, s1)
+
+
+def _kv_type(t) -> int:
+    kind = (_KV_TYPES or _kv_types()).get(t.dtype)
     if kind is None:
-        raise LwError(LW_E_ARG, f"{what} must be fp16, bf16 or fp32")
-    return lw_kv_tensor(t.data_ptr(), s0, s1), kind
+        raise LwError(LW_E_ARG, "the tensors must be fp16, bf16 or fp32")
+    return kind
 
 
-def _kv_pair(cache, a, b, names, heads):
-    ta, ka = _kv_tensor(a, names[0], heads, cache)
-    tb, kb = _kv_tensor(b, names[1], heads, cache)
-    if ka != kb or a.shape[0] != b.shape[0]:
-        raise LwError(LW_E_ARG, f"{names[0]} and {names[1]} must have the same rows and type")
-    return C.byref(ta), C.byref(tb), ka, a.shape[0]
+def _kv_rows(k, v, cache):
+    tk, tv = _kv_tensor(k, "k", cache), _kv_tensor(v, "v", cache, k)
+    if k.shape[1] != cache.kv_heads:
+        raise LwError(LW_E_ARG, f"k and v must have {cache.kv_heads} heads")
+    return k.shape[0], C.byref(tk), C.byref(tv), _kv_type(k)
 
 
 def lw_kv_append(cache: KvCache, batch: KvBatch, k, v, stream=None) -> None:
     """Quantise the new tokens' keys and values [n][kv_heads][head_dim] into the cache."""
-    tk, tv, kind, n = _kv_pair(cache, k, v, ("k", "v"), cache.kv_heads)
-    _check(_L.lw_kv_append(cache.ref, batch.ref, n, tk, tv, kind, _stream(stream)))
+    st = _L.lw_kv_append(cache.ref, batch.ref, *_kv_rows(k, v, cache), _stream(stream))
+    if st:
+        _check(st)
 
 
 def lw_kv_read(cache: KvCache, batch: KvBatch, k, v, stream=None) -> None:
     """Dequantise the batch's tokens into k and v [n][kv_heads][head_dim]."""
-    tk, tv, kind, n = _kv_pair(cache, k, v, ("k", "v"), cache.kv_heads)
-    _check(_L.lw_kv_read(cache.ref, batch.ref, n, tk, tv, kind, _stream(stream)))
+    st = _L.lw_kv_read(cache.ref, batch.ref, *_kv_rows(k, v, cache), _stream(stream))
+    if st:
+        _check(st)
 
 
 def lw_kv_attend_scratch_bytes(cache: KvCache, batch: KvBatch, n_tokens: int, q_heads: int) -> int:
@@ -572,17 +587,21 @@ def lw_kv_attend_scratch_bytes(cache: KvCache, batch: KvBatch, n_tokens: int, q_
 def lw_kv_attend(cache: KvCache, batch: KvBatch, q, out, scale: float | None = None, causal: bool = True,
                  window: int = 0, lse=None, work=None, stream=None) -> None:
     """out = attention of q [n][q_heads][head_dim] over the cache; scale None: head_dim ** -0.5."""
-    heads = q.shape[1] if getattr(q, "ndim", 0) == 3 else 0
-    tq, to, kind, n = _kv_pair(cache, q, out, ("q", "out"), heads)
-    pl = None
+    tq = _kv_tensor(q, "q", cache)
+    to = _kv_tensor(out, "out", cache, q)
+    n, heads = q.shape[0], q.shape[1]
+    pl, wp, wn = None, None, 0
     if lse is not None:
         pl = _dptr(lse, "lse")
         if lse.numel() != n * heads or lse.element_size() != 4:
             raise LwError(LW_E_ARG, "lse must be fp32 [tokens][q_heads]")
-    wp, wn = _wbuf(work) if work is not None and work.numel() else (None, 0)
-    _check(_L.lw_kv_attend(cache.ref, batch.ref, n, tq, to, kind, heads,
-                           cache.head_dim ** -0.5 if scale is None else scale, int(causal), int(window), pl, wp, wn,
-                           _stream(stream)))
+    if work is not None and work.numel():
+        wp, wn = _wbuf(work)
+    st = _L.lw_kv_attend(cache.ref, batch.ref, n, C.byref(tq), C.byref(to), _kv_type(q), heads,
+                         cache.head_dim ** -0.5 if scale is None else scale, causal, window, pl, wp, wn,
+                         _stream(stream))
+    if st:
+        _check(st)
 
 
 # ---------------------------------------------------------------- conveniences
