@@ -362,36 +362,41 @@ __device__ __forceinline__ void hide(Scores<D, ROWS> &s, Values<D, ROWS> &v, int
     }
 }
 
-// Sees to it that the tokens' p dv fit fp16: where a score or a pair has
-// outgrown the offset (rarely, after the first steps), sets a new one, for
+// Sees to it that the tokens' p dv fit fp16: where a score or a pair of a row
+// has outgrown its offset (rarely, after the first steps), sets a new one, for
 // which p dv is below 2^7 for all seen so far, and brings the sums to it.
-// Scores may then exceed the reference 2^7 times before the next.
+// Scores may then exceed the reference 2^7 times before the next.  A row's
+// offset depends on what the row sees and on nothing else.
 template <int D, int ROWS>
 __device__ __forceinline__ void fit(State<D, ROWS> &st, const Scores<D, ROWS> &s, const Values<D, ROWS> &v)
 {
     using H = Shape<D, ROWS>;
     float top = -__builtin_inff();
-    uint16_t d = 0;
+    h2 pair = {(_Float16)0.0f, (_Float16)0.0f};
 #pragma unroll
     for (int i = 0; i < H::TG; i++) {
         const uint32_t *dv = reinterpret_cast<const uint32_t *>(&v.dm[i]);
 #pragma unroll
         for (int b = 0; b < 4; b++) {
             top = fmaxf(top, s[i][b]);
-            d = __builtin_elementwise_max(d, (uint16_t)dv[b]);     // d >= 0: its bits are in order
+            pair = __builtin_elementwise_max(pair, halves(dv[b]));  // (a NaN asks for nothing)
         }
     }
-    uint32_t dtop = min((uint32_t)d, 0x7BFFu);                     // (a NaN asks for nothing)
+    uint32_t dtop = __builtin_bit_cast(uint32_t, pair) & 0xFFFFu;  // d >= 0: its bits are in order
     if (!__any(top > st.thr || dtop > st.dlim)) return;
 #pragma unroll
-    for (int o = Mma<ROWS>::WIDE; o < 64; o *= 2) top = fmaxf(top, __shfl_xor(top, o));
-#pragma unroll
-    for (int o = 1; o < 64; o *= 2) dtop = max(dtop, (uint32_t)__shfl_xor((int)dtop, o));
-    st.dlim = max(st.dlim, dtop | 0x03FFu);                        // up to the next power of two
+    for (int o = H::WIDE; o < 64; o *= 2) {
+        top = fmaxf(top, __shfl_xor(top, o));
+        dtop = max(dtop, (uint32_t)__shfl_xor((int)dtop, o));
+    }
+    const bool need = top > st.thr || dtop > st.dlim;
     const float old = st.mo;
-    st.mrow = fmaxf(st.mrow, top * st.qs);
-    st.mo = st.mrow - (float)(6 + 15 - (int)(st.dlim >> 10));
-    st.thr = (st.mrow + 7.0f) / st.qs;
+    if (need) {
+        st.dlim = max(st.dlim, min(dtop, 0x7BFFu) | 0x03FFu);       // up to the next power of two
+        st.mrow = fmaxf(st.mrow, top * st.qs);
+        st.mo = st.mrow - (float)(6 + 15 - (int)(st.dlim >> 10));
+        st.thr = (st.mrow + 7.0f) / st.qs;
+    }
     const float f = __builtin_amdgcn_exp2f(old - st.mo);
     st.l *= f;
     st.z *= f;
