@@ -38,7 +38,8 @@ struct KvAttend {
     int32_t group;               // query heads per kv head
     uint32_t group_inv;          // ceil(2^21 / group): (x * group_inv) >> 21 = x / group for x < 2048
     int32_t causal, window;      // window 0: none
-    int32_t splits, chunk;       // token chunks per row tile, tokens per chunk
+    int32_t splits, chunk;       // token chunks per row tile at most, tokens per chunk
+    int32_t slices;              // of k_kv_join's workgroups
     float scale;                 // > 0
 };
 
@@ -58,6 +59,7 @@ hipError_t lw_launch_kv_append(const KvGeom &g, int head_dim, const KvTensor &k,
 hipError_t lw_launch_kv_read(const KvGeom &g, int head_dim, const KvTensor &k, const KvTensor &v, int dtype,
                              hipStream_t s);
 hipError_t lw_launch_kv_attend(const KvAttend &a, int head_dim, int dtype, const KvPlan &p, hipStream_t s);
+hipError_t lw_launch_kv_prompt(const KvAttend &a, int head_dim, int dtype, const KvPlan &p, hipStream_t s);
 
 #ifdef __HIPCC__
 // ------------------------------------------------------------ device helpers

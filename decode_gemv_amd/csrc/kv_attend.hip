@@ -16,7 +16,7 @@
 // only afterwards.  The codes' own bits, as fp16 denormals, would save the
 // subtraction, but the matrix cores align products by the operands' exponents
 // and cut off what is far below the largest: measured over 131071 tokens, the
-// output's error against 64 bits is then 7e-4 and not 3e-4.
+// logarithm of the sum is then off by 1e-5, and so by 6e-8.
 //
 // The scores are formed transposed, S^T = K Q^T: a lane then owns one query
 // row and a few tokens, four in a row, and these are at once the operand of
@@ -30,28 +30,22 @@
 // its wavefronts take 32-token tiles in turn and meet in LDS at the end.
 // Where row tiles are few, a sequence is cut into several chunks and
 // k_kv_join adds the chunks' partial results, in order: results do not
-// depend on timing.
+// depend on timing.  (More than 64 rows a sequence: kv_prompt.hip.)
 //
 // Rounding: q is scaled by a power of two per row and held in fp16 (exact for
-// fp16 and bf16 inputs but for elements 2^29 below the row's largest);
-// p dv is rounded to fp16 once, scaled to lie high in fp16's range, and
-// multiplies the centred code, so the output's error from it is a random
-// 2^-12 of the centred part; scores, maxima, sums and outputs are fp32.
+// fp16 and bf16 inputs but for elements 2^29 below the row's largest); p dv
+// is scaled to lie high in fp16's range and rounded to fp16, which is less
+// than a bf16 output's own rounding by a factor of eight; for fp16 outputs,
+// whose rounding it would match, what the rounding left makes a second fp16
+// operand (2^-21 in all).  Scores, maxima, sums and outputs are fp32.
 #include <algorithm>
 #include <type_traits>
 
-#include "kv.h"
+#include "kv_attend.hpp"
 
 namespace {
 
-typedef _Float16 h8 __attribute__((ext_vector_type(8)));
-typedef _Float16 h2 __attribute__((ext_vector_type(2)));
-typedef float f4 __attribute__((ext_vector_type(4)));
-typedef float f16v __attribute__((ext_vector_type(16)));
-
 constexpr int NW = 4;                  // wavefronts of a workgroup
-constexpr int STEP = 32;               // tokens of a wavefront's step
-constexpr float NONE = -1e30f;         // log2 of "nothing seen yet"
 
 // A row tile has 8, 16 or 32 rows.  16 and 32 are the columns of a matrix
 // instruction; 8 rows take both halves of the 16, with the same queries, and
@@ -76,123 +70,6 @@ template <> struct Mma<32> {           // 32 x 32 x 16: lane = row/column l % 32
 
 // Wavefronts a SIMD is to hold (the registers that leaves).
 template <int D, int ROWS> constexpr int WAVES = D * ROWS <= 1024 ? 4 : D * ROWS <= 2048 ? 3 : D * ROWS <= 4096 ? 2 : 1;
-
-__device__ __forceinline__ float half_lo(uint32_t w) { return (float)__builtin_bit_cast(h2, w)[0]; }
-__device__ __forceinline__ float half_hi(uint32_t w) { return (float)__builtin_bit_cast(h2, w)[1]; }
-
-__device__ __forceinline__ h2 halves(uint32_t w) { return __builtin_bit_cast(h2, w); }
-
-// Constants that the compiler is to keep in registers: an AND and an OR with
-// two of them are one instruction, with two literals they are two.
-struct Masks {
-    uint32_t low, high, exp;     // codes at bits 0..3 and 4..7 of each half, fp16's exponent of 1024
-};
-
-__device__ __forceinline__ Masks masks()
-{
-    Masks k;
-    asm("s_mov_b32 %0, 0x000f000f" : "=s"(k.low));
-    asm("s_mov_b32 %0, 0x00f000f0" : "=s"(k.high));
-    asm("v_mov_b32 %0, 0x64006400" : "=v"(k.exp));
-    return k;
-}
-
-// Two codes, one in each half at bits 0..3 (SHIFTED: 4..7), as fp16 c - 8
-// (16 (c - 8)): under the exponent of 1024 they are 1024 + c, and one packed
-// subtraction is exact.
-template <bool SHIFTED>
-__device__ __forceinline__ h2 centred(uint32_t w, Masks k)
-{
-    return SHIFTED ? halves((w & k.high) | k.exp) - h2{(_Float16)1152.0f, (_Float16)1152.0f}
-                   : halves((w & k.low) | k.exp) - h2{(_Float16)1032.0f, (_Float16)1032.0f};
-}
-
-// Eight codes of a word in the order 0 4 1 5 2 6 3 7, those of odd dimensions
-// times 16.
-__device__ __forceinline__ h8 spread8(uint32_t w, Masks k)
-{
-    const h2 a = centred<false>(w, k), b = centred<true>(w, k);
-    const h2 c = centred<false>(w >> 8, k), d = centred<true>(w >> 8, k);
-    return h8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-
-template <class T> __device__ __forceinline__ float to_f(T x) { return (float)x; }
-
-// The visible tokens of a packed row: first and one past the last.
-struct Span {
-    int lo, hi;
-};
-
-// Everything the parts of a call agree on about a row tile.
-struct RowTile {
-    int seq, rows;               // rows in use (0: nothing to do)
-    int row0, n_new, len;        // the sequence's first packed row, new tokens and length
-    int tok0, rem0;              // new token and head of the tile's first row
-    int lo, hi;                  // tokens any of the rows may see: [lo, hi), lo a multiple of STEP
-};
-
-// New token (x) and head of the kv head's group (y) of row r of the tile.
-__device__ __forceinline__ int2 token_of(const KvAttend &a, const RowTile &t, int r)
-{
-    const unsigned i = t.rem0 + r, q = (i * a.group_inv) >> 21;
-    return make_int2(t.tok0 + (int)q, (int)(i - q * a.group));
-}
-
-__device__ __forceinline__ Span span_of(const KvAttend &a, const RowTile &t, int r)
-{
-    const int pos = t.len - t.n_new + token_of(a, t, r).x;
-    Span s = {0, a.causal ? pos + 1 : t.len};
-    if (a.window && pos >= a.window) s.lo = pos - a.window + 1;
-    if (r >= t.rows || s.hi < s.lo) s.hi = s.lo;
-    return s;
-}
-
-// Row tile x of the call.  Sequence s owns the tiles from
-// floor(start[s] * group / ROWS) + s on, as many as its rows need at most, so
-// its tiles are found without a prefix sum (and one may find nothing to do).
-template <int ROWS>
-__device__ __forceinline__ RowTile row_tile(const KvAttend &a, int x)
-{
-    const KvGeom &g = a.g;
-    RowTile t = {};
-    auto first = [&](int row, int s) { return min(max(row, 0), g.n_tokens) * a.group / ROWS + s; };   // < 2^31
-    const KvSeq q = kv_find(g, x, [&](int next, int s) { return first(next, s + 1); });
-    t.seq = q.seq;
-    if (q.seq < 0) return t;
-    t.row0 = q.row0;
-    t.n_new = q.n_new;
-    t.len = q.len;
-    const int local = x - first(q.row0, q.seq), r0 = local * ROWS, all = q.n_new * a.group;
-    if (local < 0 || r0 >= all) return t;
-    t.rows = min(ROWS, all - r0);
-    t.tok0 = r0 / a.group;
-    t.rem0 = r0 - t.tok0 * a.group;
-    const Span b = span_of(a, t, 0), e = span_of(a, t, t.rows - 1);
-    t.lo = b.lo & ~(STEP - 1);
-    const int64_t cap = min(g.stride << g.page_shift, (int64_t)0x7FFF0000);     // the table names no more
-    t.hi = max((int)min((int64_t)e.hi, cap), t.lo);
-    return t;
-}
-
-// The row tile that workgroups of number z take: the last first, as later rows
-// see more tokens, and those of one parity before the others.  Row tiles with
-// nothing to do come at regular distances (every second where sequences fill
-// one tile each), and workgroups go round the eight XCDs: in plain order all
-// the work could fall to every second XCD (48 us where this takes 32, one
-// sequence of 131071 tokens).
-__device__ __forceinline__ int tile_at(int tiles, int z)
-{
-    const int first = (tiles + 1) / 2;
-    return z < first ? 2 * (first - 1 - z) : 2 * (tiles - first - 1 - (z - first)) + 1;
-}
-
-// Chunk z of a row tile's tokens; the last takes what is left.
-__device__ __forceinline__ Span chunk_of(const KvAttend &a, const RowTile &t, int z)
-{
-    Span s = {t.lo + z * a.chunk, t.hi};
-    if (z + 1 < a.splits && (int64_t)s.lo + a.chunk < t.hi) s.hi = s.lo + a.chunk;
-    return s;
-}
 
 // What a lane holds of 32 tokens: key words and value words, and the pairs of
 // the tokens whose scores it will have (groups of four).
@@ -349,13 +226,14 @@ template <int D, int ROWS>
 __device__ __forceinline__ void hide(Scores<D, ROWS> &s, Values<D, ROWS> &v, int t0, Span seen, int lane)
 {
     using H = Shape<D, ROWS>;
+    int first = t0 + group_token<D, ROWS>(0, lane) - seen.lo;
+    asm volatile("" : "+v"(first));                          // (kept from being worked out ahead of the loop)
 #pragma unroll
     for (int i = 0; i < H::TG; i++) {
         uint32_t *dv = reinterpret_cast<uint32_t *>(&v.dm[i]);
 #pragma unroll
         for (int b = 0; b < 4; b++) {
-            const int t = t0 + group_token<D, ROWS>(i, lane) + b;
-            const bool out = (unsigned)(t - seen.lo) >= (unsigned)(seen.hi - seen.lo);
+            const bool out = (unsigned)(first + 4 * i * H::G + b) >= (unsigned)(seen.hi - seen.lo);
             s[i][b] = out ? -__builtin_inff() : s[i][b];
             dv[b] = out ? 0u : dv[b];                        // what lies there may be NaN
         }
@@ -490,103 +368,6 @@ __device__ __forceinline__ void gather(State<D, ROWS> &st, const Probs<D, ROWS> 
     }
 }
 
-// A lane's part of its row's query.
-template <int D, int ROWS, class T>
-struct Query {
-    T x[Shape<D, ROWS>::PER][8];
-};
-
-template <int D, int ROWS, class T>
-__device__ __forceinline__ void load_query(Query<D, ROWS, T> &o, const KvAttend &a, const RowTile &t, int head, int lane)
-{
-    using H = Shape<D, ROWS>;
-    const int m = lane % H::WIDE, g = lane / H::WIDE;
-    const int2 at = token_of(a, t, min(m % ROWS, t.rows - 1));
-    const T *p = static_cast<const T *>(a.q.data) + (int64_t)(t.row0 + at.x) * a.q.token +
-                 (int64_t)(head * a.group + at.y) * a.q.head + g * (H::PER * 8);
-#pragma unroll
-    for (int j = 0; j < H::PER; j++) {
-        if (a.q.wide) {
-            *reinterpret_cast<uint4 *>(o.x[j]) = *reinterpret_cast<const uint4 *>(p + 8 * j);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; i++) o.x[j][i] = p[8 * j + i];
-        }
-    }
-}
-
-// The row's query as matrix operand (in st or, for the workgroup, in sq) and
-// the factors of its scores.
-template <int D, int ROWS, class T>
-__device__ __forceinline__ void set_query(State<D, ROWS> &st, h8 *sq, const Query<D, ROWS, T> &q, float scale, int wave,
-                                          int lane)
-{
-    using H = Shape<D, ROWS>;
-    float top = 0.0f, sum = 0.0f;
-#pragma unroll
-    for (int j = 0; j < H::PER; j++)
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            top = fmaxf(top, fabsf((float)q.x[j][i]));
-            sum += (float)q.x[j][i];
-        }
-#pragma unroll
-    for (int o = H::WIDE; o < 64; o *= 2) {
-        top = fmaxf(top, __shfl_xor(top, o));
-        sum += __shfl_xor(sum, o);
-    }
-    // the largest element goes to [2^14, 2^15); an infinity stays one and
-    // makes the row NaN, as its scores are
-    const int e = top > 0.0f ? (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127 : 0;
-    st.qs = scale * 1.44269504088896341f * ldexpf(1.0f, e - 14);
-    st.qsum = ldexpf(sum, 14 - e);
-#pragma unroll
-    for (int j = 0; j < H::PER; j++) {
-        constexpr int order[8] = {0, 4, 1, 5, 2, 6, 3, 7};
-        h8 y;
-#pragma unroll
-        for (int i = 0; i < 8; i++)
-            y[i] = (_Float16)ldexpf((float)q.x[j][order[i]], 14 - e - (order[i] % 2 ? 4 : 0));
-        if constexpr (H::QREG)
-            st.q[j] = y;
-        else if (wave == j % NW)
-            sq[j * 64 + lane] = y;
-    }
-}
-
-// Partial results of the call's row tile (x, head) and chunk z: [ROWS] rows of
-// D values, then [ROWS] of (mo, l).
-template <int D, int ROWS>
-__device__ __forceinline__ float *part_of(const KvAttend &a, int64_t x, int head, int z)
-{
-    return a.part + (((x * a.g.kv_heads + head) * a.splits) + z) * (ROWS * (D + 2));
-}
-
-template <int D, class T>
-__device__ __forceinline__ void write_row(const KvAttend &a, const RowTile &t, int head, int r, int d0, const float *y,
-                                          float l, float mo)
-{
-    const int2 at = token_of(a, t, r);
-    const int64_t tok = t.row0 + at.x, h = (int64_t)head * a.group + at.y;
-    T *p = static_cast<T *>(a.out.data) + tok * a.out.token + h * a.out.head + d0;
-    T e[8];
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-    for (int i = 0; i < 8; i++) e[i] = (T)(y[i] * inv);
-    if (a.out.wide) {
-        *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(e);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; i++) p[i] = e[i];
-    }
-    if (a.lse && d0 == 0) {
-        int e = 0;                                           // l's power of two joins mo exactly
-        const float f = frexpf(l, &e);
-        a.lse[tok * ((int64_t)a.g.kv_heads * a.group) + h] =
-            l == 0.0f ? -__builtin_inff() : (__builtin_amdgcn_logf(f) + ((float)e + mo)) * 0.693147180559945309f;
-    }
-}
-
 template <int D, int ROWS, class T>
 __global__ __launch_bounds__(NW * 64, (WAVES<D, ROWS>)) void k_kv_attend(KvAttend a)
 {
@@ -631,8 +412,9 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, ROWS>)) void k_kv_attend(KvAtten
     int t0 = mine.lo + wave * STEP;
     const bool any = t0 < mine.hi;
     {
-        Query<D, ROWS, T> q;
-        load_query<D, ROWS, T>(q, a, t, head, lane);
+        Query<D, H::WIDE, T> q;
+        const int2 at = token_of(a, t, min(m % ROWS, t.rows - 1));
+        q.load(a.q, t.row0 + at.x, (int64_t)head * a.group + at.y, lane);
         if (any) {
             // (the loads' order is the loop's, or its waits would fit neither)
             page = __builtin_amdgcn_readfirstlane(entry_at(t0));
@@ -642,7 +424,12 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, ROWS>)) void k_kv_attend(KvAtten
             load_values<D, ROWS>(v, block_of(page, t0), P, t0 & (P - 1), lane);
             asm volatile("" ::: "memory");
         }
-        set_query<D, ROWS, T>(st, sq, q, a.scale, wave, lane);
+        q.make(st.qs, st.qsum, a.scale, [&](int j, h8 y) {
+            if constexpr (H::QREG)
+                st.q[j] = y;
+            else if (wave == j % NW)
+                sq[j * 64 + lane] = y;
+        });
     }
     if (!H::QREG) __syncthreads();
     st.mrow = st.mo = NONE;
@@ -704,7 +491,7 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, ROWS>)) void k_kv_attend(KvAtten
     float mo = sm[m % ROWS];
 #pragma unroll
     for (int w = 1; w < MEET; w++) mo = fmaxf(mo, sm[w * ROWS + m % ROWS]);
-    float *part = a.splits > 1 ? part_of<D, ROWS>(a, x, head, split) : nullptr;
+    float *part = chunks_of(a, t) > 1 ? part_of<D, ROWS>(a, x, head, split) : nullptr;
     const float f = __builtin_amdgcn_exp2f(st.mo - mo), fixed = st.z * f;
 #pragma unroll
     for (int pass = 0; pass < H::PASSES; pass++) {
@@ -747,58 +534,13 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, ROWS>)) void k_kv_attend(KvAtten
     }
 }
 
-// Joins the chunks of one row: D/8 threads take eight dimensions each, in
-// 2048/D slices that take the chunks in turn and meet in LDS.
-template <int D, int ROWS, class T>
-__global__ __launch_bounds__(256) void k_kv_join(KvAttend a)
-{
-    constexpr int C = D / 8, SLICES = 256 / C;
-    __shared__ __align__(16) float sy[SLICES][D];
-    __shared__ float2 sml[SLICES];
-    const int64_t x = blockIdx.x;
-    const int head = blockIdx.y, r = blockIdx.z;
-    const RowTile t = row_tile<ROWS>(a, (int)x);
-    if (r >= t.rows) return;
-    const int used = max(min((t.hi - t.lo + a.chunk - 1) / a.chunk, a.splits), 1);
-    const int slice = threadIdx.x / C, d0 = threadIdx.x % C * 8;
-    float y[8], top = NONE, l = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; j++) y[j] = 0.0f;
-    auto add = [&](float mo, float n, const float *v) {
-        const float now = fmaxf(top, mo);
-        const float fo = __builtin_amdgcn_exp2f(top - now), fn = __builtin_amdgcn_exp2f(mo - now);
-        top = now;
-        l = l * fo + n * fn;
-#pragma unroll
-        for (int j = 0; j < 8; j++) y[j] = y[j] * fo + v[j] * fn;
-    };
-    for (int z = slice; z < used; z += SLICES) {
-        const float *p = part_of<D, ROWS>(a, x, head, z);
-        const float2 ml = *reinterpret_cast<const float2 *>(p + ROWS * D + 2 * r);
-        float v[8];
-        *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(p + r * D + d0);
-        *reinterpret_cast<float4 *>(v + 4) = *reinterpret_cast<const float4 *>(p + r * D + d0 + 4);
-        add(ml.x, ml.y, v);
-    }
-    if (slice) {
-        *reinterpret_cast<float4 *>(&sy[slice][d0]) = make_float4(y[0], y[1], y[2], y[3]);
-        *reinterpret_cast<float4 *>(&sy[slice][d0 + 4]) = make_float4(y[4], y[5], y[6], y[7]);
-        if (d0 == 0) sml[slice] = make_float2(top, l);
-    }
-    __syncthreads();
-    if (slice) return;
-    for (int z = 1; z < min(SLICES, used); z++) add(sml[z].x, sml[z].y, &sy[z][d0]);
-    write_row<D, T>(a, t, head, r, d0, y, l, top);
-}
-
 template <int D, int ROWS, class T>
 hipError_t launch(const KvAttend &a, const KvPlan &p, hipStream_t s)
 {
     hipLaunchKernelGGL((k_kv_attend<D, ROWS, T>), dim3(p.splits, a.g.kv_heads, (unsigned)p.tiles), dim3(NW * 64), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
-    hipLaunchKernelGGL((k_kv_join<D, ROWS, T>), dim3((unsigned)p.tiles, a.g.kv_heads, ROWS), dim3(256), 0, s, a);
-    return hipGetLastError();
+    return launch_join<D, ROWS, T>(a, p, s);
 }
 
 template <int D>
@@ -815,14 +557,24 @@ KvPlan lw_kv_plan(int head_dim, int kv_heads, int group, int64_t n_seqs, int64_t
                   int most)
 {
     KvPlan p;
-    p.tile = n_tokens * group <= 8 * n_seqs ? 8 : n_tokens * group <= 16 * n_seqs ? 16 : 32;
+    const int64_t rows = n_tokens * group;
+    // Query rows of a tile, by the rows a sequence has on average.  128
+    // (kv_prompt.hip) against 32, heads of 128, 32 on 8 with 64 new tokens
+    // and more: 512 on 2048 54 and 59 us, 1024 on 4096 123 and 127, 4096 on
+    // themselves 210 and 264; with fewer new tokens the smaller tile wins
+    // (64 on 8192: 49 and 44).
+    p.tile = rows <= 8 * n_seqs ? 8 : rows <= 16 * n_seqs ? 16 : rows <= 64 * n_seqs ? 32 : 128;
     p.tiles = n_tokens * group / p.tile + n_seqs;
     // tokens a row tile may see
     int64_t span = max_len;
     if (window) span = std::min<int64_t>(span, (int64_t)window + (p.tile + group - 1) / group + STEP);
     span = std::max<int64_t>(span, 1);
     const int64_t base = std::max(std::min(n_seqs, n_tokens), (n_tokens * group + p.tile - 1) / p.tile) * kv_heads;
-    int64_t splits = std::min((1024 + base - 1) / base, (span + 2 * NW * STEP - 1) / (2 * NW * STEP));
+    // workgroups that fill the chip; with 128 rows two stand on a CU, and more
+    // chunks than they need cost their results' way through memory (2048 new
+    // tokens on themselves: 101 us with 1024, 93 with 512)
+    const int64_t full = p.tile == 128 ? 512 : 1024;
+    int64_t splits = std::min((full + base - 1) / base, (span + 2 * NW * STEP - 1) / (2 * NW * STEP));
     splits = std::max<int64_t>(1, std::min<int64_t>(splits, std::min(most, 1024)));
     p.chunk = (int)(((span + splits - 1) / splits + NW * STEP - 1) / (NW * STEP) * (NW * STEP));
     p.splits = (int)((span + p.chunk - 1) / p.chunk);
@@ -832,6 +584,7 @@ KvPlan lw_kv_plan(int head_dim, int kv_heads, int group, int64_t n_seqs, int64_t
 
 hipError_t lw_launch_kv_attend(const KvAttend &a, int head_dim, int dtype, const KvPlan &p, hipStream_t s)
 {
+    if (p.tile == 128) return lw_launch_kv_prompt(a, head_dim, dtype, p, s);
     if (head_dim == 64) return launch_dim<64>(a, dtype, p, s);
     if (head_dim == 128) return launch_dim<128>(a, dtype, p, s);
     if (head_dim == 256) return launch_dim<256>(a, dtype, p, s);

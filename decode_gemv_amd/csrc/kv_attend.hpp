@@ -1,0 +1,292 @@
+// kv_attend.hpp -- what the attention kernels of the 4-bit key/value cache
+// share: the unpacking of codes, the cutting of a call into row tiles and
+// chunks of tokens, the queries as matrix operands, and the writing of
+// results.  Internal to the library.
+#ifndef LW_KV_ATTEND_HPP
+#define LW_KV_ATTEND_HPP
+
+#include "kv.h"
+
+namespace {
+
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef float f16v __attribute__((ext_vector_type(16)));
+
+constexpr int STEP = 32;               // tokens of a wavefront's step
+constexpr float NONE = -1e30f;         // log2 of "nothing seen yet"
+
+__device__ __forceinline__ float half_lo(uint32_t w) { return (float)__builtin_bit_cast(h2, w)[0]; }
+__device__ __forceinline__ float half_hi(uint32_t w) { return (float)__builtin_bit_cast(h2, w)[1]; }
+
+__device__ __forceinline__ h2 halves(uint32_t w) { return __builtin_bit_cast(h2, w); }
+
+// Constants that the compiler is to keep in registers: an AND and an OR with
+// two of them are one instruction, with two literals they are two.
+struct Masks {
+    uint32_t low, high, exp;     // codes at bits 0..3 and 4..7 of each half, fp16's exponent of 1024
+};
+
+__device__ __forceinline__ Masks masks()
+{
+    Masks k;
+    asm("s_mov_b32 %0, 0x000f000f" : "=s"(k.low));
+    asm("s_mov_b32 %0, 0x00f000f0" : "=s"(k.high));
+    asm("v_mov_b32 %0, 0x64006400" : "=v"(k.exp));
+    return k;
+}
+
+// Two codes, one in each half at bits 0..3 (SHIFTED: 4..7), as fp16 c - 8
+// (16 (c - 8)): under the exponent of 1024 they are 1024 + c, and one packed
+// subtraction is exact.
+template <bool SHIFTED>
+__device__ __forceinline__ h2 centred(uint32_t w, Masks k)
+{
+    return SHIFTED ? halves((w & k.high) | k.exp) - h2{(_Float16)1152.0f, (_Float16)1152.0f}
+                   : halves((w & k.low) | k.exp) - h2{(_Float16)1032.0f, (_Float16)1032.0f};
+}
+
+// Eight codes of a word in the order 0 4 1 5 2 6 3 7, those of odd dimensions
+// times 16.
+__device__ __forceinline__ h8 spread8(uint32_t w, Masks k)
+{
+    const h2 a = centred<false>(w, k), b = centred<true>(w, k);
+    const h2 c = centred<false>(w >> 8, k), d = centred<true>(w >> 8, k);
+    return h8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// The visible tokens of a packed row: first and one past the last.
+struct Span {
+    int lo, hi;
+};
+
+// Everything the parts of a call agree on about a row tile.
+struct RowTile {
+    int seq, rows;               // rows in use (0: nothing to do)
+    int row0, n_new, len;        // the sequence's first packed row, new tokens and length
+    int tok0, rem0;              // new token and head of the tile's first row
+    int lo, hi;                  // tokens any of the rows may see: [lo, hi), lo a multiple of STEP
+};
+
+// New token (x) and head of the kv head's group (y) of row r of the tile.
+__device__ __forceinline__ int2 token_of(const KvAttend &a, const RowTile &t, int r)
+{
+    const unsigned i = t.rem0 + r, q = (i * a.group_inv) >> 21;
+    return make_int2(t.tok0 + (int)q, (int)(i - q * a.group));
+}
+
+__device__ __forceinline__ Span span_of(const KvAttend &a, const RowTile &t, int r)
+{
+    const int pos = t.len - t.n_new + token_of(a, t, r).x;
+    Span s = {0, a.causal ? pos + 1 : t.len};
+    if (a.window && pos >= a.window) s.lo = pos - a.window + 1;
+    if (r >= t.rows || s.hi < s.lo) s.hi = s.lo;
+    return s;
+}
+
+// Row tile x of the call.  Sequence s owns the tiles from
+// floor(start[s] * group / ROWS) + s on, as many as its rows need at most, so
+// its tiles are found without a prefix sum (and one may find nothing to do).
+template <int ROWS>
+__device__ __forceinline__ RowTile row_tile(const KvAttend &a, int x)
+{
+    const KvGeom &g = a.g;
+    RowTile t = {};
+    auto first = [&](int row, int s) { return min(max(row, 0), g.n_tokens) * a.group / ROWS + s; };   // < 2^31
+    const KvSeq q = kv_find(g, x, [&](int next, int s) { return first(next, s + 1); });
+    t.seq = q.seq;
+    if (q.seq < 0) return t;
+    t.row0 = q.row0;
+    t.n_new = q.n_new;
+    t.len = q.len;
+    const int local = x - first(q.row0, q.seq), r0 = local * ROWS, all = q.n_new * a.group;
+    if (local < 0 || r0 >= all) return t;
+    t.rows = min(ROWS, all - r0);
+    t.tok0 = r0 / a.group;
+    t.rem0 = r0 - t.tok0 * a.group;
+    const Span b = span_of(a, t, 0), e = span_of(a, t, t.rows - 1);
+    t.lo = b.lo & ~(STEP - 1);
+    const int64_t cap = min(g.stride << g.page_shift, (int64_t)0x7FFF0000);     // the table names no more
+    t.hi = max((int)min((int64_t)e.hi, cap), t.lo);
+    return t;
+}
+
+// The row tile that workgroups of number z take: the last first, as later rows
+// see more tokens, and those of one parity before the others.  Row tiles with
+// nothing to do come at regular distances (every second where sequences fill
+// one tile each), and workgroups go round the eight XCDs: in plain order all
+// the work could fall to every second XCD (48 us where this takes 32, one
+// sequence of 131071 tokens).
+__device__ __forceinline__ int tile_at(int tiles, int z)
+{
+    const int first = (tiles + 1) / 2;
+    return z < first ? 2 * (first - 1 - z) : 2 * (tiles - first - 1 - (z - first)) + 1;
+}
+
+// Chunks that a row tile's tokens fill, at least one.  A tile of one chunk
+// writes its outputs itself, those of more are joined.
+__device__ __forceinline__ int chunks_of(const KvAttend &a, const RowTile &t)
+{
+    return min(max((t.hi - t.lo + a.chunk - 1) / a.chunk, 1), a.splits);
+}
+
+// Chunk z; the last takes what is left.
+__device__ __forceinline__ Span chunk_of(const KvAttend &a, const RowTile &t, int z)
+{
+    Span s = {t.lo + z * a.chunk, t.hi};
+    if (z + 1 < a.splits && (int64_t)s.lo + a.chunk < t.hi) s.hi = s.lo + a.chunk;
+    return s;
+}
+
+// A lane's part of its row's query, for matrix instructions of WIDE columns.
+template <int D, int WIDE, class T>
+struct Query {
+    static constexpr int G = 64 / WIDE, PER = D / 8 / G;     // lanes that share a column, words of a lane's part
+    T x[PER][8];
+
+    // head vector of new token tok (of the sequence whose rows start at row0) and query head h
+    __device__ __forceinline__ void load(const KvTensor &q, int64_t row, int64_t h, int lane)
+    {
+        const T *p = static_cast<const T *>(q.data) + row * q.token + h * q.head + lane / WIDE * (PER * 8);
+#pragma unroll
+        for (int j = 0; j < PER; j++) {
+            if (q.wide) {
+                *reinterpret_cast<uint4 *>(x[j]) = *reinterpret_cast<const uint4 *>(p + 8 * j);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i++) x[j][i] = p[8 * j + i];
+            }
+        }
+    }
+
+    // Factors of the row's scores (score = qs * (acc dk + (8 dk - mk) qsum),
+    // in log2 units, for the accumulated products acc), and put(j, operand)
+    // for each word.
+    template <class F>
+    __device__ __forceinline__ void make(float &qs, float &qsum, float scale, F put) const
+    {
+        float top = 0.0f, sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < PER; j++)
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                top = fmaxf(top, fabsf((float)x[j][i]));
+                sum += (float)x[j][i];
+            }
+#pragma unroll
+        for (int o = WIDE; o < 64; o *= 2) {
+            top = fmaxf(top, __shfl_xor(top, o));
+            sum += __shfl_xor(sum, o);
+        }
+        // the largest element goes to [2^14, 2^15); an infinity stays one and
+        // makes the row NaN, as its scores are
+        const int e = top > 0.0f ? (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127 : 0;
+        qs = scale * 1.44269504088896341f * ldexpf(1.0f, e - 14);
+        qsum = ldexpf(sum, 14 - e);
+#pragma unroll
+        for (int j = 0; j < PER; j++) {
+            constexpr int order[8] = {0, 4, 1, 5, 2, 6, 3, 7};
+            h8 y;
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                y[i] = (_Float16)ldexpf((float)x[j][order[i]], 14 - e - (order[i] % 2 ? 4 : 0));
+            put(j, y);
+        }
+    }
+};
+
+// Partial results of the call's row tile (x, head) and chunk z: [ROWS] rows of
+// D values, then [ROWS] of (mo, l).
+template <int D, int ROWS>
+__device__ __forceinline__ float *part_of(const KvAttend &a, int64_t x, int head, int z)
+{
+    return a.part + (((x * a.g.kv_heads + head) * a.splits) + z) * (ROWS * (D + 2));
+}
+
+template <int D, class T>
+__device__ __forceinline__ void write_row(const KvAttend &a, const RowTile &t, int head, int r, int d0, const float *y,
+                                          float l, float mo)
+{
+    const int2 at = token_of(a, t, r);
+    const int64_t tok = t.row0 + at.x, h = (int64_t)head * a.group + at.y;
+    T *p = static_cast<T *>(a.out.data) + tok * a.out.token + h * a.out.head + d0;
+    T e[8];
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int i = 0; i < 8; i++) e[i] = (T)(y[i] * inv);
+    if (a.out.wide) {
+        *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(e);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++) p[i] = e[i];
+    }
+    if (a.lse && d0 == 0) {
+        int e = 0;                                           // l's power of two joins mo exactly
+        const float f = frexpf(l, &e);
+        a.lse[tok * ((int64_t)a.g.kv_heads * a.group) + h] =
+            l == 0.0f ? -__builtin_inff() : (__builtin_amdgcn_logf(f) + ((float)e + mo)) * 0.693147180559945309f;
+    }
+}
+
+// Joins the chunks of rows: D/8 threads take eight dimensions each of a row,
+// in a.slices slices (a power of two) that take the chunks in turn and meet
+// in LDS.
+template <int D, int ROWS, class T>
+__global__ __launch_bounds__(256) void k_kv_join(KvAttend a)
+{
+    constexpr int C = D / 8;
+    __shared__ __align__(16) float sy[256 / C][D];
+    __shared__ float2 sml[256 / C];
+    const int64_t x = blockIdx.x;
+    const int head = blockIdx.y, part = threadIdx.x / C, slice = part % a.slices;
+    const int r = blockIdx.z * (256 / C / a.slices) + part / a.slices;
+    const RowTile t = row_tile<ROWS>(a, (int)x);
+    const int used = chunks_of(a, t);
+    if (t.rows == 0 || used == 1) return;
+    const int d0 = threadIdx.x % C * 8;
+    float y[8], top = NONE, l = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; j++) y[j] = 0.0f;
+    auto add = [&](float mo, float n, const float *v) {
+        const float now = fmaxf(top, mo);
+        const float fo = __builtin_amdgcn_exp2f(top - now), fn = __builtin_amdgcn_exp2f(mo - now);
+        top = now;
+        l = l * fo + n * fn;
+#pragma unroll
+        for (int j = 0; j < 8; j++) y[j] = y[j] * fo + v[j] * fn;
+    };
+    for (int z = slice; z < used && r < t.rows; z += a.slices) {
+        const float *p = part_of<D, ROWS>(a, x, head, z);
+        const float2 ml = *reinterpret_cast<const float2 *>(p + ROWS * D + 2 * r);
+        float v[8];
+        *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(p + r * D + d0);
+        *reinterpret_cast<float4 *>(v + 4) = *reinterpret_cast<const float4 *>(p + r * D + d0 + 4);
+        add(ml.x, ml.y, v);
+    }
+    if (slice) {
+        *reinterpret_cast<float4 *>(&sy[part][d0]) = make_float4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<float4 *>(&sy[part][d0 + 4]) = make_float4(y[4], y[5], y[6], y[7]);
+        if (d0 == 0) sml[part] = make_float2(top, l);
+    }
+    __syncthreads();
+    if (slice || r >= t.rows) return;
+    for (int z = 1; z < min(a.slices, used); z++) add(sml[part + z].x, sml[part + z].y, &sy[part + z][d0]);
+    write_row<D, T>(a, t, head, r, d0, y, l, top);
+}
+
+template <int D, int ROWS, class T>
+hipError_t launch_join(const KvAttend &a, const KvPlan &p, hipStream_t s)
+{
+    constexpr int PARTS = 2048 / D;                          // rows times slices of a workgroup
+    KvAttend b = a;
+    b.slices = 1;
+    while (b.slices < p.splits && b.slices < PARTS) b.slices *= 2;
+    const unsigned z = (ROWS + PARTS / b.slices - 1) / (PARTS / b.slices);
+    hipLaunchKernelGGL((k_kv_join<D, ROWS, T>), dim3((unsigned)p.tiles, b.g.kv_heads, z), dim3(256), 0, s, b);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+#endif

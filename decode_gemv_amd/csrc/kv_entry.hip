@@ -165,6 +165,7 @@ extern "C" lw_status lw_kv_attend(const lw_kv_cache *cache, const lw_kv_batch *b
     a.window = window;
     a.splits = p.splits;
     a.chunk = p.chunk;
+    a.slices = 1;
     a.scale = scale;
     return device(lw_launch_kv_attend(a, cache->head_dim, dtype, p, (hipStream_t)stream), "kv attend launch");
 }

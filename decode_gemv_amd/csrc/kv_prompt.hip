@@ -1,0 +1,410 @@
+// kv_prompt.hip -- attention of many new tokens over the 4-bit key/value cache.
+//
+// The mathematics is kv_attend.hip's.  There each wavefront unpacks the codes
+// that it uses, which for many query rows is most of its work: 152 of some 400
+// instructions for 32 tokens and 32 rows.  Here a workgroup has 128 rows of a
+// sequence, 32 for each wavefront, and goes through the tokens in tiles of 64
+// (32 for heads of 256): each wavefront unpacks a quarter of a tile's keys and
+// values into LDS, laid out as the matrix operands that all four then read in
+// whole 16-byte lanes, and turns their pairs into the factors of scores and
+// values, once per token instead of once per lane.  Two buffers: a tile is
+// unpacked, and the one after it loaded, while the one before is used, with
+// one barrier a tile.  No tokens are shared out between wavefronts, so nothing
+// has to be joined at the end, and two workgroups stand on a CU whose phases
+// (unpacking, products, exponentials) fill each other's gaps.
+//
+// What bounds it: per 64 tokens a wavefront has 1024 cycles of matrix
+// instructions, some 2000 of other vector instructions (half of them the
+// exponentials, sums and conversions of its 32 scores a lane) and reads 48 KB
+// of LDS; on a SIMD with two of them that takes 6500 cycles, with all three
+// pipes between 30 and 65 % busy.  One workgroup alone on a CU takes 5700 for
+// its own, so the calls that leave the longest rows' workgroups alone at the
+// end (prompts of up to 2048 tokens, where all are there from the start) are
+// bound by those.
+//
+// Measured, heads of 128 in bf16, 32 of them on 8: 16384 tokens on themselves
+// 811 TFLOP/s (tiles of 32 rows of kv_attend.hip: 633), 2048 on 16384 750
+// (638), 2048 on themselves 372 (354).
+//
+// Rounding: as in kv_attend.hip, but p dv is rounded to fp16 once for fp16
+// outputs too.  Its error, at random 2^-12 of a part of the output, comes to
+// about that of rounding the output; the second operand that would remove it
+// costs a quarter of the rate (623 TFLOP/s and not 790, 4096 on 16384).
+#include <stddef.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "kv_attend.hpp"
+
+namespace {
+
+constexpr int WV = 4, WIDE = 32, ROWS = WV * WIDE;
+
+template <int D>
+struct Tile {
+    static constexpr int TT = D > 128 ? 32 : 64;             // tokens of a tile
+    static constexpr int SUBS = TT / 32;
+    static constexpr int DW = D / 8, PER = DW / 2;           // words of a token, and of a half of the lanes
+    static constexpr int W = D >= 128 ? 4 : 2, U = DW / W;   // words of a key unit, units of a token
+    static constexpr int NT = D / 32;                        // output tiles along the head
+    static constexpr int TPW = TT / WV;                      // tokens of a wavefront's value words and pairs
+    static constexpr int KS = 64 * WV / (TT * U);            // threads that share a key unit, by words,
+    static constexpr int VS = 64 * WV / (TT / 4 * DW);       // and a value unit, by halves of its words
+    static constexpr int KW = W / KS;                        // key words of a thread
+    uint4 k[SUBS][PER][64];                                  // operands of K Q^T
+    uint2 v[SUBS][2][NT][64][2];                             // operands of V^T P^T
+    float2 kf[TT], vf[TT];                                   // dk, 8 dk - mk; dv, 8 dv - mv
+    uint32_t here[WV];                                       // whether the tokens a wavefront unpacked are present
+    float dmax[WV];                                          // and their largest dv
+};
+
+// What a wavefront has loaded of a tile.
+template <int D>
+struct Raw {
+    uint32_t k[Tile<D>::KW];
+    uint4 v;
+    uint32_t dm;                 // lanes below TPW: a key's pair, the next TPW: a value's
+    bool here;
+};
+
+// Where a thread's operands go in a tile, in bytes: its first key word's, its
+// first code's of the value words' halves, and its pair's; what follows lies at
+// fixed distances (kept in registers as they are, not as what they are made of).
+template <int D>
+struct Put {
+    static constexpr int HALVES = 2 / Tile<D>::VS;
+    uint32_t k, v[HALVES];
+    __device__ __forceinline__ Put(int thread)
+    {
+        using L = Tile<D>;
+        const int ku = thread / L::KS, t = ku / (L::U * 16) * 16 + ku % 16, w = ku / 16 % L::U * L::W + thread % L::KS * L::KW;
+        k = ((t / 32 * L::PER + w % L::PER) * 64 + t % 32 + w / L::PER * 32) * 16;
+        asm("" : "+v"(k));
+        // token group g of the tile: half g % 2 of the lanes, place g / 2 % 2 of the operand
+        const int vu = thread / L::VS, g = vu / L::DW, c = vu % L::DW;
+#pragma unroll
+        for (int i = 0; i < HALVES; i++) {
+            const int n = 4 * (L::VS == 2 ? thread % 2 : i);
+            v[i] = offsetof(Tile<D>, v) +
+                   ((g / 4 * L::NT + n % L::NT) * 64 + c + L::DW * (n / L::NT) + g % 2 * 32) * 16 + g / 2 % 2 * 8;
+            asm("" : "+v"(v[i]));
+        }
+    }
+};
+
+template <int D>
+__device__ __forceinline__ void unpack(Tile<D> &o, const Raw<D> &r, const Put<D> &at, Masks mk, int wave, int lane)
+{
+    using L = Tile<D>;
+    char *base = reinterpret_cast<char *>(&o);
+#pragma unroll
+    for (int i = 0; i < L::KW; i++) *reinterpret_cast<h8 *>(base + at.k + i * 1024) = spread8(r.k[i], mk);
+    const uint32_t *x = reinterpret_cast<const uint32_t *>(&r.v);
+#pragma unroll
+    for (int i = 0; i < Put<D>::HALVES; i++) {
+        const uint32_t sel = (L::VS == 2 ? lane % 2 : i) ? 0x07060302u : 0x05040100u;
+        const uint32_t a = __builtin_amdgcn_perm(x[1], x[0], sel), b = __builtin_amdgcn_perm(x[3], x[2], sel);
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const uint32_t p = j >= 2 ? a >> 8 : a, q = j >= 2 ? b >> 8 : b;
+            const h2 lo = j % 2 ? centred<true>(p, mk) : centred<false>(p, mk);
+            const h2 hi = j % 2 ? centred<true>(q, mk) : centred<false>(q, mk);
+            *reinterpret_cast<uint2 *>(base + at.v[i] + j % L::NT * 1024 + j / L::NT * L::DW * 16) =
+                make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
+        }
+    }
+    // A value's pair that is not finite makes its token's score NaN instead
+    // (so that it reaches the rows that see it, and only zeros the others)
+    float d = half_lo(r.dm), c = fmaf(d, 8.0f, -half_hi(r.dm));
+    const bool odd = !(fabsf(c) < __builtin_inff());
+    const bool bad = __shfl((int)odd, lane + L::TPW) != 0;
+    if (lane < L::TPW) {
+        o.kf[wave * L::TPW + lane] = make_float2(d, bad ? __builtin_nanf("") : c);
+    } else {
+        d = odd ? 0.0f : d;
+        if (lane < 2 * L::TPW) o.vf[wave * L::TPW + lane % L::TPW] = make_float2(d, odd ? 0.0f : c);
+    }
+#pragma unroll
+    for (int i = 1; i < L::TPW; i *= 2) d = fmaxf(d, __shfl_xor(d, i));
+    if (lane == L::TPW) {
+        o.here[wave] = r.here;
+        o.dmax[wave] = d;
+    }
+}
+
+template <int D>
+struct Rows {
+    static constexpr int NT = Tile<D>::NT;
+    h8 q[Tile<D>::PER];
+    f16v o[NT];
+    float qs, qsum;
+    float mo, mrow, thr, dlim;   // offset, its reference, and what calls for a new one (kv_attend.hip)
+    float l, z;
+};
+
+// 32 tokens of a tile, the first being t0.  masked: some of them may be hidden
+// from some rows; a hidden token's score is -infinity.
+template <int D>
+__device__ __forceinline__ void step(Rows<D> &st, const Tile<D> &tile, int sub, int t0, bool masked, Span seen, int lane)
+{
+    using L = Tile<D>;
+    constexpr int PIECES = 32 / L::TPW;
+    const int g = lane / WIDE;
+    f16v acc;
+#pragma unroll
+    for (int i = 0; i < 16; i++) acc[i] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < L::PER; j++)
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, tile.k[sub][j][lane]), st.q[j], acc, 0, 0, 0);
+    // a lane's tokens: 8 a + 4 g + b, its four of every eight
+    float s[4][4], top = -__builtin_inff(), dtop = 0.0f;
+    const float4 *kf = reinterpret_cast<const float4 *>(&tile.kf[sub * 32 + 4 * g]);
+    const float4 *vf = reinterpret_cast<const float4 *>(&tile.vf[sub * 32 + 4 * g]);
+#pragma unroll
+    for (int a = 0; a < 4; a++) {
+        const float4 x = kf[4 * a], y = kf[4 * a + 1];
+        s[a][0] = fmaf(acc[4 * a], x.x, x.y * st.qsum);
+        s[a][1] = fmaf(acc[4 * a + 1], x.z, x.w * st.qsum);
+        s[a][2] = fmaf(acc[4 * a + 2], y.x, y.y * st.qsum);
+        s[a][3] = fmaf(acc[4 * a + 3], y.z, y.w * st.qsum);
+    }
+#pragma unroll
+    for (int i = 0; i < PIECES; i++) dtop = fmaxf(dtop, tile.dmax[sub * PIECES + i]);
+    if (masked) {
+        int first = t0 + 4 * g - seen.lo;
+        asm volatile("" : "+v"(first));                      // (kept from being worked out ahead of the loop)
+        uint32_t here = 0;
+#pragma unroll
+        for (int i = 0; i < PIECES; i++)
+            here |= (tile.here[sub * PIECES + i] ? (L::TPW == 16 ? 0xFFFFu : 0xFFu) : 0u) << (i * L::TPW);
+        here >>= 4 * g;
+        dtop = 0.0f;                                         // of what the row sees
+#pragma unroll
+        for (int a = 0; a < 4; a++) {
+            const float4 x = vf[4 * a], y = vf[4 * a + 1];
+            const float dv[4] = {x.x, x.z, y.x, y.z};
+#pragma unroll
+            for (int b = 0; b < 4; b++) {
+                const bool out = (unsigned)(first + 8 * a + b) >= (unsigned)(seen.hi - seen.lo) ||
+                                 !(here >> (8 * a + b) & 1u);
+                s[a][b] = out ? -__builtin_inff() : s[a][b];
+                dtop = fmaxf(dtop, out ? 0.0f : dv[b]);
+            }
+        }
+    }
+#pragma unroll
+    for (int a = 0; a < 4; a++)
+#pragma unroll
+        for (int b = 0; b < 4; b++) top = fmaxf(top, s[a][b]);
+    if (__any(top > st.thr || dtop > st.dlim)) {             // rare: a new offset, as in kv_attend.hip
+        top = fmaxf(top, __shfl_xor(top, 32));
+        dtop = fmaxf(dtop, __shfl_xor(dtop, 32));
+        const bool need = top > st.thr || dtop > st.dlim;
+        const float old = st.mo;
+        if (need) {
+            const uint32_t up = __builtin_bit_cast(uint32_t, fminf(fmaxf(dtop, 0x1p-24f), 65504.0f)) + 0x7FFFFFu;
+            st.dlim = fmaxf(st.dlim, __builtin_bit_cast(float, up & 0xFF800000u));          // up to a power of two
+            st.mrow = fmaxf(st.mrow, top * st.qs);
+            st.mo = st.mrow - (float)(7 + 127 - (int)(__builtin_bit_cast(uint32_t, st.dlim) >> 23));
+            st.thr = (st.mrow + 7.0f) / st.qs;
+        }
+        const float f = __builtin_amdgcn_exp2f(old - st.mo);
+        st.l *= f;
+        st.z *= f;
+#pragma unroll
+        for (int n = 0; n < L::NT; n++)
+#pragma unroll
+            for (int j = 0; j < 16; j++) st.o[n][j] *= f;
+    }
+#pragma unroll
+    for (int kk = 0; kk < 2; kk++) {
+        h8 e;
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+            const int a = 2 * kk + c / 2;
+            const float4 x = vf[4 * a + c % 2];              // (dv, 8 dv - mv) of two tokens
+#pragma unroll
+            for (int b = 0; b < 2; b++) {
+                const float p = __builtin_amdgcn_exp2f(fmaf(s[a][c % 2 * 2 + b], st.qs, -st.mo));
+                st.l += p;
+                st.z = fmaf(p, b ? x.w : x.y, st.z);
+                e[2 * c + b] = (_Float16)(p * (b ? x.z : x.x));
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < L::NT; n++) {
+            const h8 v = __builtin_bit_cast(h8, *reinterpret_cast<const uint4 *>(&tile.v[sub][kk][n][lane][0]));
+            st.o[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, e, st.o[n], 0, 0, 0);
+        }
+    }
+}
+
+// The row tile of workgroups y: the last first, as later rows see more tokens,
+// every second four the other way round, as consecutive workgroups of an XCD
+// go round its four shader engines and would give the first of them the
+// longest of each four.  (Chunks come last in the grid for the same reason:
+// with a tile's two chunks side by side, half of the engines got the short
+// ones, and 2048 tokens on themselves took 112 us and not 93.)
+__device__ __forceinline__ int order_of(int tiles, int y)
+{
+    if ((y | 3) < tiles && y & 4) y ^= 3;
+    return tiles - 1 - y;
+}
+
+template <int D, class T>
+__global__ __launch_bounds__(WV * 64, (D > 128 ? 1 : D > 64 ? 2 : 3)) void k_kv_prompt(KvAttend a)
+{
+    using L = Tile<D>;
+    constexpr int PD = 64, ROWF = PD + 4;                    // dimensions of a pass of the end, and a row in LDS
+    constexpr size_t BYTES = std::max(2 * sizeof(Tile<D>), sizeof(float) * ROWS * ROWF);
+    __shared__ uint4 mem[BYTES / 16];
+    __shared__ float sl[ROWS], sm[ROWS];
+    Tile<D> *tiles = reinterpret_cast<Tile<D> *>(mem);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int m = lane % WIDE, g = lane / WIDE, head = blockIdx.x;
+    const int split = blockIdx.z, x = order_of(gridDim.y, blockIdx.y);
+    const RowTile t = row_tile<ROWS>(a, x);
+    if (t.rows == 0) return;
+    const Span mine = chunk_of(a, t, split);
+    if (split > 0 && mine.lo >= mine.hi) return;             // (chunk 0 always leaves a result)
+    const int P = 1 << a.g.page_shift;
+
+    const int32_t *pages = a.g.table + (int64_t)t.seq * a.g.stride;
+    // a wavefront's tokens of the tile at t0 lie in one page: its place there,
+    // and its table entry (of a tile past the end: the last one's)
+    const int piece = wave * L::TPW & ~15;
+    auto entry_at = [&](int t0) { return pages[min(t0 + piece, mine.hi - 1) >> a.g.page_shift]; };
+    Raw<D> raw;
+    auto load = [&](int t0, int32_t entry) {
+        raw.here = (uint32_t)entry < a.g.n_pages && t0 + piece < mine.hi;
+        const auto block = __builtin_amdgcn_make_buffer_rsrc(
+            a.g.pages + (uint64_t)(raw.here ? (uint32_t)entry : 0u) * (uint64_t)a.g.page_bytes +
+                (uint32_t)head * (uint32_t)a.g.block_bytes,
+            0, raw.here ? a.g.block_bytes : 0, 0x00027000);
+        const uint32_t at = (t0 + piece) & (P - 1), in = wave * L::TPW & 15;     // (TPW 8: half of the piece's tokens)
+        const uint32_t k = (threadIdx.x / L::KS % (L::U * 16) * L::W + threadIdx.x % L::KS * L::KW) * 4;
+        if constexpr (L::KW == 4) {
+            const uint4 w = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(block, k, at * (D / 2), 0));
+            raw.k[0] = w.x, raw.k[1] = w.y, raw.k[2] = w.z, raw.k[3] = w.w;
+        } else {
+            const uint2 w = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(block, k, at * (D / 2), 0));
+            raw.k[0] = w.x, raw.k[1] = w.y;
+        }
+        raw.v = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
+            block, lane / L::VS * 16, P * (D / 2) + (at + in) * (D / 2), 0));
+        raw.dm = __builtin_bit_cast(uint32_t, __builtin_amdgcn_raw_buffer_load_b32(
+            block, lane % L::TPW * 4 + (lane < L::TPW ? 0 : P * 4), P * D + (at + in) * 4, 0));
+    };
+
+    Rows<D> st;
+    const Masks mk = masks();
+    const Put<D> put(threadIdx.x);
+    const bool any = mine.lo < mine.hi;
+    int32_t after = -1;
+    {
+        Query<D, WIDE, T> q;
+        const int2 at = token_of(a, t, min(wave * WIDE + m, t.rows - 1));
+        q.load(a.q, t.row0 + at.x, (int64_t)head * a.group + at.y, lane);
+        if (any) {
+            load(mine.lo, __builtin_amdgcn_readfirstlane(entry_at(mine.lo)));
+            after = entry_at(mine.lo + L::TT);
+        }
+        q.make(st.qs, st.qsum, a.scale, [&](int j, h8 y) { st.q[j] = y; });
+    }
+    st.mrow = st.mo = NONE;
+    st.thr = NONE / fmaxf(st.qs, 1.0f);
+    st.l = st.z = st.dlim = 0.0f;
+#pragma unroll
+    for (int n = 0; n < L::NT; n++)
+#pragma unroll
+        for (int j = 0; j < 16; j++) st.o[n][j] = 0.0f;
+    // what the lane's row sees, what any of the wavefront's rows do, and all
+    const Span seen = span_of(a, t, wave * WIDE + m);
+    const int rows = min(t.rows - wave * WIDE, WIDE);
+    const Span first = span_of(a, t, wave * WIDE), last = span_of(a, t, wave * WIDE + max(rows, 1) - 1);
+    if (any) {
+        unpack<D>(tiles[0], raw, put, mk, wave, lane);
+        load(mine.lo + L::TT, __builtin_amdgcn_readfirstlane(after));
+        after = entry_at(mine.lo + 2 * L::TT);
+        __syncthreads();
+        int buf = 0;
+        for (int t0 = mine.lo; t0 < mine.hi; t0 += L::TT) {
+            // the next tile's other buffer was last read before the barrier
+            if (t0 + L::TT < mine.hi) unpack<D>(tiles[buf ^ 1], raw, put, mk, wave, lane);
+            load(t0 + 2 * L::TT, __builtin_amdgcn_readfirstlane(after));
+            after = entry_at(t0 + 3 * L::TT);
+            const Tile<D> &tile = tiles[buf];
+#pragma unroll
+            for (int sub = 0; sub < L::SUBS; sub++) {
+                const int ts = t0 + sub * 32;
+                if (rows <= 0 || ts >= last.hi || ts + 32 <= first.lo || ts >= mine.hi) continue;
+                bool whole = true;
+#pragma unroll
+                for (int i = 0; i < 32 / L::TPW; i++)
+                    whole &= __builtin_amdgcn_readfirstlane(tile.here[sub * (32 / L::TPW) + i]) != 0;
+                step<D>(st, tile, sub, ts, !whole || rows < WIDE || ts < last.lo || ts + 32 > first.hi, seen, lane);
+            }
+            __syncthreads();
+            buf ^= 1;
+        }
+    }
+
+    st.l += __shfl_xor(st.l, 32);
+    st.z += __shfl_xor(st.z, 32);
+    if (g == 0) {
+        sl[wave * WIDE + m] = st.l;
+        sm[wave * WIDE + m] = st.mo;
+    }
+    float *part = chunks_of(a, t) > 1 ? part_of<D, ROWS>(a, x, head, split) : nullptr;
+    float *so = reinterpret_cast<float *>(mem) + wave * (WIDE * ROWF);
+#pragma unroll
+    for (int pass = 0; pass < D / PD; pass++) {
+        if (pass) __syncthreads();
+#pragma unroll
+        for (int n = 0; n < L::NT; n++)
+#pragma unroll
+            for (int j = 0; j < 16; j++) {
+                const int r = 8 * (j / 4) + 4 * g + j % 4, d = 8 * (r % L::DW) + r / L::DW * L::NT + n;
+                if (D > 64 && j / 4 % (D / PD) != pass) continue;             // (d / 64 is that)
+                so[m * ROWF + d % PD] = fmaf(st.o[n][j], n % 2 ? 0x1p-4f : 1.0f, st.z);
+            }
+        __syncthreads();
+#pragma unroll
+        for (int i = lane; i < WIDE * PD / 8; i += 64) {
+            const int r = wave * WIDE + i / (PD / 8), d0 = i % (PD / 8) * 8, d = pass * PD + d0;
+            if (r >= t.rows) break;
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 8; j += 4)
+                *reinterpret_cast<float4 *>(y + j) = *reinterpret_cast<const float4 *>(so + i / (PD / 8) * ROWF + d0 + j);
+            if (part) {
+#pragma unroll
+                for (int j = 0; j < 8; j += 4)
+                    *reinterpret_cast<float4 *>(part + r * D + d + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+                if (d == 0) *reinterpret_cast<float2 *>(part + ROWS * D + 2 * r) = make_float2(sm[r], sl[r]);
+            } else {
+                write_row<D, T>(a, t, head, r, d, y, sl[r], sm[r]);
+            }
+        }
+    }
+}
+
+template <int D, class T>
+hipError_t launch(const KvAttend &a, const KvPlan &p, hipStream_t s)
+{
+    hipLaunchKernelGGL((k_kv_prompt<D, T>), dim3(a.g.kv_heads, (unsigned)p.tiles, p.splits), dim3(WV * 64), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess || p.splits == 1 ? e : launch_join<D, ROWS, T>(a, p, s);
+}
+
+}  // namespace
+
+hipError_t lw_launch_kv_prompt(const KvAttend &a, int head_dim, int dtype, const KvPlan &p, hipStream_t s)
+{
+    const bool half = dtype == LW_F16;
+    if (head_dim == 64) return half ? launch<64, _Float16>(a, p, s) : launch<64, __bf16>(a, p, s);
+    if (head_dim == 128) return half ? launch<128, _Float16>(a, p, s) : launch<128, __bf16>(a, p, s);
+    if (head_dim == 256) return half ? launch<256, _Float16>(a, p, s) : launch<256, __bf16>(a, p, s);
+    return hipErrorInvalidValue;
+}

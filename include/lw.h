@@ -491,8 +491,10 @@ lw_status lw_kv_read(const lw_kv_cache *cache, const lw_kv_batch *batch, int64_t
  *             (NULL/0 where that is 0), contents not kept between calls; a
  *             smaller one lowers the number of chunks that a sequence is cut
  *             into, and LW_E_ARG is given only for a misaligned one
- * Scores, sums and the output's accumulation are fp32, p times a value's d
- * is rounded to fp16; sums run in a fixed order: results are deterministic.
+ * Scores, sums and the output's accumulation are fp32; p times a value's d
+ * is rounded to fp16 (for fp16 results of up to 64 rows a sequence, with what
+ * that leaves as a second term); sums run in a fixed order: results are
+ * deterministic.  At most 2^30 query rows per kv head and 65535 row tiles.
  * Errors: LW_E_ARG, LW_E_UNSUPPORTED (head_dim, page_tokens, dtype),
  * LW_E_DEVICE. */
 lw_status lw_kv_attend(const lw_kv_cache *cache, const lw_kv_batch *batch, int64_t n_tokens, const lw_kv_tensor *q,

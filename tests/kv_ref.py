@@ -120,15 +120,15 @@ def attend(cache, table, start, lens, q, scale, causal=True, window=0):
     return out, lse, dict(size=size, mean=mean, grid=grid, seen=seen)
 
 
-def bounds(ref, lse, by, D, bf16):
+def bounds(ref, lse, by, D, bf16, many=False):
     """Largest errors of out and lse.  A score is a sum of D products and two more in fp32, each addition off by at
     most a last place (the matrix cores cut off): d = (D + 8) 2^-23 of the sum of magnitudes.  An output then moves by
-    2 d of the mean |v|; p dv is rounded to fp16's 2^-11 (with its remainder: 2^-21), as a factor of |c - 8| <= 8, or
-    to 2^-25 where it is below 2^-20 of the largest (2^-31 after scaling: the reference lies at 2^6); the output is
+    2 d of the mean |v|; p dv is rounded to fp16's 2^-11 (with its remainder, which fp16 results take along where a
+    sequence has not many rows: 2^-21), as a factor of |c - 8| <= 8, or to 2^-25 where it is below 2^-20 of the largest (2^-31 after scaling: the reference lies at 2^6); the output is
     rounded to its type."""
     delta = (D + 8) * 2.0 ** -23 * by["size"] + 2.0 ** -21
     unit = 2.0 ** -8 if bf16 else 2.0 ** -11
-    moved = 2 * delta * by["mean"] + (2.0 ** -11 if bf16 else 2.0 ** -21) * by["grid"] + 2.0 ** -30 * by["seen"]
+    moved = 2 * delta * by["mean"] + (2.0 ** -11 if bf16 or many else 2.0 ** -21) * by["grid"] + 2.0 ** -30 * by["seen"]
     out = moved[..., None] * (1 + unit) + unit * np.abs(ref) + (0 if bf16 else 2.0 ** -25)
     with np.errstate(invalid="ignore"):
         return out, delta + 2.0 ** -21 * (1 + np.where(np.isfinite(lse), np.abs(lse), 0))

@@ -198,7 +198,8 @@ def test_absent_tokens_and_rows_of_no_sequence(torch, dg):
 def check(s, q, out, lse, dtype, rows=None, **kw):
     ref, rl, by = R.attend(R.Cache(s.pages.cpu().numpy(), s.kv, s.D, s.P), s.table, s.start, s.lens,
                            host(q).astype(np.float64), s.D ** -0.5, **kw)
-    tol, tl = R.bounds(ref, rl, by, s.D, dtype == "bf16")
+    many = q.shape[0] * (q.shape[1] // s.kv) > 64 * len(s.lens)      # of the tiles of 128 rows
+    tol, tl = R.bounds(ref, rl, by, s.D, dtype == "bf16", many)
     rows = np.isfinite(ref).all((1, 2)) if rows is None else rows
     got, gl = host(out).astype(np.float64)[rows], host(lse)[rows]
     ref, rl, tol, tl = ref[rows], rl[rows], tol[rows], tl[rows]
