@@ -38,21 +38,26 @@ struct KvAttend {
     int32_t group;               // query heads per kv head
     uint32_t group_inv;          // ceil(2^21 / group): (x * group_inv) >> 21 = x / group for x < 2048
     int32_t causal, window;      // window 0: none
-    int32_t splits, chunk;       // token chunks per row tile at most, tokens per chunk
+    int32_t target;              // chunks of tokens per kv head to cut the batch into (kv_attend.hpp), or 0:
+    int32_t splits, chunk;       // every row tile into that many at most, of so many tokens
+    int2 *first;                 // target > 0: each row tile's first chunk's number, and the tokens of a chunk
     int32_t slices;              // of k_kv_join's workgroups
     float scale;                 // > 0
 };
 
-// How a call is cut up: rows per tile, row tiles, splits and chunk.
+// How a call is cut up: rows per tile, row tiles, and chunks as in KvAttend;
+// all of a kv head's chunks at most, with target; the bytes of their results.
 struct KvPlan {
     int tile;
     int64_t tiles;
-    int splits, chunk;
-    size_t work_bytes;
+    int target, splits, chunk;
+    int64_t pieces;
+    size_t first_at, work_bytes;
 };
 
+// `room`: bytes there are for results.
 KvPlan lw_kv_plan(int head_dim, int kv_heads, int group, int64_t n_seqs, int64_t n_tokens, int64_t max_len,
-                  int window, int most);
+                  int window, size_t room);
 
 hipError_t lw_launch_kv_append(const KvGeom &g, int head_dim, const KvTensor &k, const KvTensor &v, int dtype,
                                hipStream_t s);

@@ -28,9 +28,9 @@
 // A workgroup has one tile of 8, 16 or 32 query rows of a sequence (row = token
 // * group + head, all on one kv head) and a chunk of the sequence's tokens;
 // its wavefronts take 32-token tiles in turn and meet in LDS at the end.
-// Where row tiles are few, a sequence is cut into several chunks and
-// k_kv_join adds the chunks' partial results, in order: results do not
-// depend on timing.  (More than 64 rows a sequence: kv_prompt.hip.)
+// Where row tiles are few, sequences are cut into chunks of one size for the
+// whole batch (piece_of) and k_kv_join adds the chunks' partial results, in
+// order: results do not depend on timing.  (More than 64 rows a sequence: kv_prompt.hip.)
 //
 // Rounding: q is scaled by a power of two per row and held in fp16 (exact for
 // fp16 and bf16 inputs but for elements 2^29 below the row's largest); p dv
@@ -68,8 +68,11 @@ template <> struct Mma<32> {           // 32 x 32 x 16: lane = row/column l % 32
     }
 };
 
-// Wavefronts a SIMD is to hold (the registers that leaves).
-template <int D, int ROWS> constexpr int WAVES = D * ROWS <= 1024 ? 4 : D * ROWS <= 2048 ? 3 : D * ROWS <= 4096 ? 2 : 1;
+// Wavefronts a SIMD is to hold (the registers that leaves).  Six of 8 rows of
+// 64 dimensions take 33 us for 96 sequences of 16 heads in a window of 1024
+// tokens, five 36: all workgroups are then there at once.
+template <int D, int ROWS, bool FINE>
+constexpr int WAVES = D * ROWS <= 512 && !FINE ? 6 : D * ROWS <= 1024 ? 4 : D * ROWS <= 2048 ? 3 : D * ROWS <= 4096 ? 2 : 1;
 
 // What a lane holds of 32 tokens: key words and value words, and the pairs of
 // the tokens whose scores it will have (groups of four).
@@ -369,7 +372,7 @@ __device__ __forceinline__ void gather(State<D, ROWS> &st, const Probs<D, ROWS> 
 }
 
 template <int D, int ROWS, class T>
-__global__ __launch_bounds__(NW * 64, (WAVES<D, ROWS>)) void k_kv_attend(KvAttend a)
+__global__ __launch_bounds__(NW * 64, (WAVES<D, ROWS, std::is_same<T, _Float16>::value>)) void k_kv_attend(KvAttend a)
 {
     using M = Mma<ROWS>;
     using S = State<D, ROWS>;
@@ -379,12 +382,12 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, ROWS>)) void k_kv_attend(KvAtten
     __shared__ float sl[NW * H::WIDE], sm[NW * H::WIDE];     // by wavefront and column
     h8 *sq = reinterpret_cast<h8 *>(so);                     // the loop's; so is the end's
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int m = lane % H::WIDE, g = lane / H::WIDE, head = blockIdx.y;
-    const int split = blockIdx.x, x = tile_at(gridDim.z, blockIdx.z);
-    const RowTile t = row_tile<ROWS>(a, x);
+    const int m = lane % H::WIDE, g = lane / H::WIDE, head = blockIdx.x;
+    Piece piece = {0, INT_MAX, 0};
+    const RowTile t = a.target ? piece_of<ROWS>(a, blockIdx.y, piece) : row_tile<ROWS>(a, tile_at(gridDim.y, blockIdx.y));
     if (t.rows == 0) return;
-    Span mine = chunk_of(a, t, split);
-    if (split > 0 && mine.lo >= mine.hi) return;             // (chunk 0 always leaves a result)
+    const Span mine = chunk_of(t, piece.chunk, INT_MAX, piece.split);
+    if (piece.split > 0 && mine.lo >= mine.hi) return;       // (chunk 0 always leaves a result)
 
     const Span seen = span_of(a, t, m % ROWS);
     const Span head_row = span_of(a, t, 0), last_row = span_of(a, t, t.rows - 1);
@@ -491,7 +494,7 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, ROWS>)) void k_kv_attend(KvAtten
     float mo = sm[m % ROWS];
 #pragma unroll
     for (int w = 1; w < MEET; w++) mo = fmaxf(mo, sm[w * ROWS + m % ROWS]);
-    float *part = chunks_of(a, t) > 1 ? part_of<D, ROWS>(a, x, head, split) : nullptr;
+    float *part = chunks_of(t, piece.chunk, INT_MAX) > 1 ? part_of<D, ROWS>(a, piece.n, head) : nullptr;
     const float f = __builtin_amdgcn_exp2f(st.mo - mo), fixed = st.z * f;
 #pragma unroll
     for (int pass = 0; pass < H::PASSES; pass++) {
@@ -537,9 +540,9 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, ROWS>)) void k_kv_attend(KvAtten
 template <int D, int ROWS, class T>
 hipError_t launch(const KvAttend &a, const KvPlan &p, hipStream_t s)
 {
-    hipLaunchKernelGGL((k_kv_attend<D, ROWS, T>), dim3(p.splits, a.g.kv_heads, (unsigned)p.tiles), dim3(NW * 64), 0, s, a);
+    hipLaunchKernelGGL((k_kv_attend<D, ROWS, T>), dim3(a.g.kv_heads, (unsigned)(p.target ? p.pieces : p.tiles)), dim3(NW * 64), 0, s, a);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.splits == 1) return e;
+    if (e != hipSuccess || !p.target) return e;
     return launch_join<D, ROWS, T>(a, p, s);
 }
 
@@ -554,9 +557,9 @@ hipError_t launch_dim(const KvAttend &a, int dtype, const KvPlan &p, hipStream_t
 }  // namespace
 
 KvPlan lw_kv_plan(int head_dim, int kv_heads, int group, int64_t n_seqs, int64_t n_tokens, int64_t max_len, int window,
-                  int most)
+                  size_t room)
 {
-    KvPlan p;
+    KvPlan p = {};
     const int64_t rows = n_tokens * group;
     // Query rows of a tile, by the rows a sequence has on average.  128
     // (kv_prompt.hip) against 32, heads of 128, 32 on 8 with 64 new tokens
@@ -564,21 +567,39 @@ KvPlan lw_kv_plan(int head_dim, int kv_heads, int group, int64_t n_seqs, int64_t
     // themselves 210 and 264; with fewer new tokens the smaller tile wins
     // (64 on 8192: 49 and 44).
     p.tile = rows <= 8 * n_seqs ? 8 : rows <= 16 * n_seqs ? 16 : rows <= 64 * n_seqs ? 32 : 128;
-    p.tiles = n_tokens * group / p.tile + n_seqs;
+    p.tiles = rows / p.tile + n_seqs;
+    p.splits = 1;
     // tokens a row tile may see
     int64_t span = max_len;
     if (window) span = std::min<int64_t>(span, (int64_t)window + (p.tile + group - 1) / group + STEP);
-    span = std::max<int64_t>(span, 1);
-    const int64_t base = std::max(std::min(n_seqs, n_tokens), (n_tokens * group + p.tile - 1) / p.tile) * kv_heads;
-    // workgroups that fill the chip; with 128 rows two stand on a CU, and more
-    // chunks than they need cost their results' way through memory (2048 new
-    // tokens on themselves: 101 us with 1024, 93 with 512)
-    const int64_t full = p.tile == 128 ? 512 : 1024;
-    int64_t splits = std::min((full + base - 1) / base, (span + 2 * NW * STEP - 1) / (2 * NW * STEP));
-    splits = std::max<int64_t>(1, std::min<int64_t>(splits, std::min(most, 1024)));
-    p.chunk = (int)(((span + splits - 1) / splits + NW * STEP - 1) / (NW * STEP) * (NW * STEP));
-    p.splits = (int)((span + p.chunk - 1) / p.chunk);
-    p.work_bytes = p.splits > 1 ? (size_t)p.tiles * kv_heads * p.splits * p.tile * (head_dim + 2) * sizeof(float) : 0;
+    const size_t result = (size_t)kv_heads * p.tile * (head_dim + 2) * sizeof(float);
+    if (p.tile == 128) {
+        // Workgroups that fill the chip: two stand on a CU, and more chunks
+        // than they need cost their results' way through memory (2048 new
+        // tokens on themselves: 101 us with 1024, 93 with 512)
+        const int64_t base = std::max(n_seqs, rows / p.tile) * kv_heads;
+        p.splits = (int)std::min({(512 + base - 1) / base, (span + LEAST - 1) / LEAST, (int64_t)(room / result) / p.tiles});
+        p.splits = std::max(p.splits, 1);
+        p.chunk = (int)(((span + p.splits - 1) / p.splits + CHUNK - 1) / CHUNK * CHUNK);
+        p.work_bytes = p.splits > 1 ? p.tiles * p.splits * result : 0;
+        return p;
+    }
+    // Cut or not, heads of 128, 32 on 8: 8 sequences of 1000 tokens 17.2 us cut
+    // and 15.9 not, one of 1500 16.6 and 18.7; 48 sequences of 500 to 8190
+    // tokens 63 and 79, 256 of 100 to 4000 139 and 132 (workgroups enough, of
+    // which the chip takes the next as it is done with one).
+    if (span <= 1024 || n_seqs * kv_heads >= 1024) return p;
+    // Into about 768 pieces, three for a CU: 16 sequences of 501 to 8190 tokens
+    // take 26.8 us, with 1024 28.1 and with 1536 30.3; one of 131071 43.5,
+    // 43.3 and 47; 32 of 16384 116, 119 and 120.
+    const size_t notes = p.tiles * sizeof(int2);
+    int64_t pieces = std::max(768 / kv_heads, 1) + p.tiles;
+    if (room < notes || (room - notes) / result < (size_t)pieces) pieces = room < notes ? 0 : (room - notes) / result;
+    if (pieces <= p.tiles || pieces > 65535) return p;
+    p.target = (int)(pieces - p.tiles);
+    p.pieces = pieces;
+    p.first_at = pieces * result;
+    p.work_bytes = p.first_at + notes;
     return p;
 }
 

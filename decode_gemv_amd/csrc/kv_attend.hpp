@@ -5,6 +5,8 @@
 #ifndef LW_KV_ATTEND_HPP
 #define LW_KV_ATTEND_HPP
 
+#include <limits.h>
+
 #include "kv.h"
 
 namespace {
@@ -16,6 +18,7 @@ typedef float f16v __attribute__((ext_vector_type(16)));
 
 constexpr int STEP = 32;               // tokens of a wavefront's step
 constexpr float NONE = -1e30f;         // log2 of "nothing seen yet"
+constexpr int CHUNK = 128, LEAST = 512;  // chunks are multiples of the first, and from the second on
 
 __device__ __forceinline__ float half_lo(uint32_t w) { return (float)__builtin_bit_cast(h2, w)[0]; }
 __device__ __forceinline__ float half_hi(uint32_t w) { return (float)__builtin_bit_cast(h2, w)[1]; }
@@ -85,58 +88,139 @@ __device__ __forceinline__ Span span_of(const KvAttend &a, const RowTile &t, int
     return s;
 }
 
-// Row tile x of the call.  Sequence s owns the tiles from
-// floor(start[s] * group / ROWS) + s on, as many as its rows need at most, so
-// its tiles are found without a prefix sum (and one may find nothing to do).
-template <int ROWS>
-__device__ __forceinline__ RowTile row_tile(const KvAttend &a, int x)
+// Tokens that the table can name.
+__device__ __forceinline__ int cap_of(const KvGeom &g)
 {
-    const KvGeom &g = a.g;
+    return (int)min(g.stride << g.page_shift, (int64_t)0x7FFF0000);
+}
+
+// Row tile `local` of a sequence.
+template <int ROWS>
+__device__ __forceinline__ RowTile tile_of(const KvAttend &a, const KvSeq &q, int local)
+{
     RowTile t = {};
-    auto first = [&](int row, int s) { return min(max(row, 0), g.n_tokens) * a.group / ROWS + s; };   // < 2^31
-    const KvSeq q = kv_find(g, x, [&](int next, int s) { return first(next, s + 1); });
     t.seq = q.seq;
     if (q.seq < 0) return t;
     t.row0 = q.row0;
     t.n_new = q.n_new;
     t.len = q.len;
-    const int local = x - first(q.row0, q.seq), r0 = local * ROWS, all = q.n_new * a.group;
+    const int r0 = local * ROWS, all = q.n_new * a.group;
     if (local < 0 || r0 >= all) return t;
     t.rows = min(ROWS, all - r0);
     t.tok0 = r0 / a.group;
     t.rem0 = r0 - t.tok0 * a.group;
     const Span b = span_of(a, t, 0), e = span_of(a, t, t.rows - 1);
     t.lo = b.lo & ~(STEP - 1);
-    const int64_t cap = min(g.stride << g.page_shift, (int64_t)0x7FFF0000);     // the table names no more
-    t.hi = max((int)min((int64_t)e.hi, cap), t.lo);
+    t.hi = max(min(e.hi, cap_of(a.g)), t.lo);
     return t;
+}
+
+// The number of a sequence's first row tile.  Sequence s owns those from
+// floor(start[s] * group / ROWS) + s on, as many as its rows need at most, so
+// its tiles are found without a prefix sum (and one may find nothing to do).
+template <int ROWS>
+__device__ __forceinline__ int first_tile(const KvAttend &a, int row, int s)
+{
+    return min(max(row, 0), a.g.n_tokens) * a.group / ROWS + s;      // < 2^31
+}
+
+template <int ROWS>
+__device__ __forceinline__ RowTile row_tile(const KvAttend &a, int x)
+{
+    const KvSeq q = kv_find(a.g, x, [&](int next, int s) { return first_tile<ROWS>(a, next, s + 1); });
+    return tile_of<ROWS>(a, q, x - first_tile<ROWS>(a, q.row0, q.seq));
 }
 
 // The row tile that workgroups of number z take: the last first, as later rows
 // see more tokens, and those of one parity before the others.  Row tiles with
 // nothing to do come at regular distances (every second where sequences fill
 // one tile each), and workgroups go round the eight XCDs: in plain order all
-// the work could fall to every second XCD (48 us where this takes 32, one
-// sequence of 131071 tokens).
+// the work could fall to every second XCD.
 __device__ __forceinline__ int tile_at(int tiles, int z)
 {
     const int first = (tiles + 1) / 2;
     return z < first ? 2 * (first - 1 - z) : 2 * (tiles - first - 1 - (z - first)) + 1;
 }
 
-// Chunks that a row tile's tokens fill, at least one.  A tile of one chunk
-// writes its outputs itself, those of more are joined.
-__device__ __forceinline__ int chunks_of(const KvAttend &a, const RowTile &t)
+// What a workgroup has to do: chunk `split` of a row tile, of `chunk` tokens,
+// whose results are number n of the kv head's.
+struct Piece {
+    int split, chunk, n;
+};
+
+// Piece y of a batch whose sequences are cut into chunks of one size, the
+// same for all, for which the batch makes about a.target (at most that and
+// one more per row tile): then workgroups have the same work however
+// different the sequences are, and none has nothing to do.  The wavefront's
+// lanes look at 64 sequences at a time.
+template <int ROWS>
+__device__ __forceinline__ RowTile piece_of(const KvAttend &a, int y, Piece &o)
 {
-    return min(max((t.hi - t.lo + a.chunk - 1) / a.chunk, 1), a.splits);
+    const KvGeom &g = a.g;
+    const int lane = threadIdx.x & 63, cap = cap_of(g);
+    int row0, n_new, len, tiles, span;
+    auto look = [&](int s) {
+        const int mine = min(s + lane, g.n_seqs - 1);
+        const int b = g.start[mine], e = g.start[mine + 1];
+        len = max(g.lens[mine], 0);
+        row0 = min(max(b, 0), g.n_tokens);
+        n_new = min(max(e, row0), g.n_tokens) - row0;
+        tiles = s + lane < g.n_seqs ? (n_new * a.group + ROWS - 1) / ROWS : 0;
+        const int pos = len - n_new;                         // the first row's
+        const int lo = a.window && pos >= a.window ? pos - a.window + 1 : 0;
+        span = max(min(len, cap) - (lo & ~(STEP - 1)), 0);
+    };
+    float all = 0.0f;
+    for (int s = 0; s < g.n_seqs; s += 64) {
+        look(s);
+        all += (float)tiles * (float)span;
+    }
+#pragma unroll
+    for (int i = 1; i < 64; i *= 2) all += __shfl_xor(all, i);
+    const float part = fminf(all / (float)a.target, 0x1p30f);
+    o.chunk = max((__builtin_amdgcn_readfirstlane((int)ceilf(part)) + CHUNK - 1) / CHUNK * CHUNK, LEAST);
+    KvSeq q = {-1, 0, 0, 0};
+    int local = 0, before = 0;
+    for (int s = 0; s < g.n_seqs; s += 64) {
+        if (g.n_seqs > 64) look(s);
+        const int chunks = max((int)(((unsigned)span + o.chunk - 1) / (unsigned)o.chunk), 1);
+        int sum = tiles * chunks;
+#pragma unroll
+        for (int i = 1; i < 64; i *= 2) {
+            const int x = __shfl_up(sum, i);
+            sum += lane >= i ? x : 0;
+        }
+        const int c = __popcll(__ballot(before + sum <= y));
+        if (c == 64) {
+            before += __builtin_amdgcn_readlane(sum, 63);
+            continue;
+        }
+        const int each = __builtin_amdgcn_readlane(chunks, c);
+        const int in = y - before - (c ? __builtin_amdgcn_readlane(sum, c - 1) : 0);
+        q = {s + c, __builtin_amdgcn_readlane(row0, c), __builtin_amdgcn_readlane(n_new, c), __builtin_amdgcn_readlane(len, c)};
+        local = in / each;
+        o.split = in - local * each;
+        break;
+    }
+    o.n = y;
+    const RowTile t = tile_of<ROWS>(a, q, local);
+    if (t.rows && o.split == 0 && blockIdx.x == 0 && threadIdx.x == 0)
+        a.first[first_tile<ROWS>(a, q.row0, q.seq) + local] = make_int2(y, o.chunk);
+    return t;
 }
 
-// Chunk z; the last takes what is left.
-__device__ __forceinline__ Span chunk_of(const KvAttend &a, const RowTile &t, int z)
+// Chunks that a row tile's tokens fill, at least one and at most `most`.  A
+// tile of one chunk writes its outputs itself, those of more are joined.
+__device__ __forceinline__ int chunks_of(const RowTile &t, int chunk, int most)
 {
-    Span s = {t.lo + z * a.chunk, t.hi};
-    if (z + 1 < a.splits && (int64_t)s.lo + a.chunk < t.hi) s.hi = s.lo + a.chunk;
-    return s;
+    return min(max((int)(((unsigned)(t.hi - t.lo) + (unsigned)chunk - 1) / (unsigned)chunk), 1), most);
+}
+
+// Chunk z; the last of the most takes what is left.
+__device__ __forceinline__ Span chunk_of(const RowTile &t, int chunk, int most, int z)
+{
+    const int64_t lo = t.lo + (int64_t)z * chunk, hi = z + 1 < most ? lo + chunk : t.hi;
+    return {(int)min(lo, (int64_t)t.hi), (int)min(hi, (int64_t)t.hi)};
 }
 
 // A lane's part of its row's query, for matrix instructions of WIDE columns.
@@ -199,9 +283,9 @@ struct Query {
 // Partial results of the call's row tile (x, head) and chunk z: [ROWS] rows of
 // D values, then [ROWS] of (mo, l).
 template <int D, int ROWS>
-__device__ __forceinline__ float *part_of(const KvAttend &a, int64_t x, int head, int z)
+__device__ __forceinline__ float *part_of(const KvAttend &a, int64_t n, int head)
 {
-    return a.part + (((x * a.g.kv_heads + head) * a.splits) + z) * (ROWS * (D + 2));
+    return a.part + (n * a.g.kv_heads + head) * (ROWS * (D + 2));
 }
 
 template <int D, class T>
@@ -241,9 +325,11 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttend a)
     const int64_t x = blockIdx.x;
     const int head = blockIdx.y, part = threadIdx.x / C, slice = part % a.slices;
     const int r = blockIdx.z * (256 / C / a.slices) + part / a.slices;
+    const int2 at = a.target ? a.first[x] : make_int2((int)x * a.splits, a.chunk);
     const RowTile t = row_tile<ROWS>(a, (int)x);
-    const int used = chunks_of(a, t);
-    if (t.rows == 0 || used == 1) return;
+    if (t.rows == 0) return;                                 // (and the first chunk's number is nobody's)
+    const int used = chunks_of(t, at.y, a.target ? INT_MAX : a.splits);
+    if (used == 1) return;
     const int d0 = threadIdx.x % C * 8;
     float y[8], top = NONE, l = 0.0f;
 #pragma unroll
@@ -256,13 +342,20 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttend a)
 #pragma unroll
         for (int j = 0; j < 8; j++) y[j] = y[j] * fo + v[j] * fn;
     };
-    for (int z = slice; z < used && r < t.rows; z += a.slices) {
-        const float *p = part_of<D, ROWS>(a, x, head, z);
-        const float2 ml = *reinterpret_cast<const float2 *>(p + ROWS * D + 2 * r);
-        float v[8];
-        *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(p + r * D + d0);
-        *reinterpret_cast<float4 *>(v + 4) = *reinterpret_cast<const float4 *>(p + r * D + d0 + 4);
-        add(ml.x, ml.y, v);
+    // (eight chunks' loads at once: their latency is what this takes)
+    for (int z0 = slice; z0 < used && r < t.rows; z0 += 8 * a.slices) {
+        float2 ml[8];
+        float v[8][8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const float *p = part_of<D, ROWS>(a, at.x + min(z0 + i * a.slices, used - 1), head);
+            ml[i] = *reinterpret_cast<const float2 *>(p + ROWS * D + 2 * r);
+            *reinterpret_cast<float4 *>(v[i]) = *reinterpret_cast<const float4 *>(p + r * D + d0);
+            *reinterpret_cast<float4 *>(v[i] + 4) = *reinterpret_cast<const float4 *>(p + r * D + d0 + 4);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (z0 + i * a.slices < used) add(ml[i].x, ml[i].y, v[i]);
     }
     if (slice) {
         *reinterpret_cast<float4 *>(&sy[part][d0]) = make_float4(y[0], y[1], y[2], y[3]);
@@ -281,7 +374,8 @@ hipError_t launch_join(const KvAttend &a, const KvPlan &p, hipStream_t s)
     constexpr int PARTS = 2048 / D;                          // rows times slices of a workgroup
     KvAttend b = a;
     b.slices = 1;
-    while (b.slices < p.splits && b.slices < PARTS) b.slices *= 2;
+    const int64_t chunks = p.target ? 2 * p.pieces / p.tiles : p.splits;      // a row tile's, about
+    while (8 * b.slices < chunks && b.slices < PARTS) b.slices *= 2;
     const unsigned z = (ROWS + PARTS / b.slices - 1) / (PARTS / b.slices);
     hipLaunchKernelGGL((k_kv_join<D, ROWS, T>), dim3((unsigned)p.tiles, b.g.kv_heads, z), dim3(256), 0, s, b);
     return hipGetLastError();

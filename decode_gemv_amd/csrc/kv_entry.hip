@@ -76,13 +76,13 @@ lw_status device(hipError_t e, const char *what)
     return lw_fail(LW_E_DEVICE, std::string(what) + ": " + hipGetErrorString(e));
 }
 
-// `most`: at most that many chunks per sequence.
-KvPlan plan_of(const lw_kv_cache *c, const lw_kv_batch *b, int64_t n_tokens, int q_heads, int window, int most)
+// `room`: bytes of work.
+KvPlan plan_of(const lw_kv_cache *c, const lw_kv_batch *b, int64_t n_tokens, int q_heads, int window, size_t room)
 {
     const int64_t cap = b->table_stride * c->page_tokens;
     const int64_t longest = b->max_len ? (b->max_len < cap ? b->max_len : cap) : cap;
     return lw_kv_plan(c->head_dim, c->kv_heads, q_heads / c->kv_heads, b->n_seqs, n_tokens, longest, window,
-                      most);
+                      room);
 }
 
 }  // namespace
@@ -127,7 +127,7 @@ extern "C" size_t lw_kv_attend_scratch_bytes(const lw_kv_cache *cache, const lw_
     if (q_heads < 1 || q_heads % cache->kv_heads || q_heads / cache->kv_heads > 1024 ||
         n_tokens * (q_heads / cache->kv_heads) > (1 << 30))
         return 0;
-    return plan_of(cache, batch, n_tokens, q_heads, 0, INT_MAX).work_bytes;
+    return plan_of(cache, batch, n_tokens, q_heads, 0, SIZE_MAX).work_bytes;
 }
 
 extern "C" lw_status lw_kv_attend(const lw_kv_cache *cache, const lw_kv_batch *batch, int64_t n_tokens,
@@ -149,11 +149,7 @@ extern "C" lw_status lw_kv_attend(const lw_kv_cache *cache, const lw_kv_batch *b
     if ((st = tensor(q, "q", dtype, a.q)) || (st = tensor(out, "out", dtype, a.out))) return st;
     if (!aligned(lse, 4)) return lw_fail(LW_E_ARG, "lse must be 4-byte aligned");
     if (!aligned(work, 16)) return lw_fail(LW_E_ARG, "work must be 16-byte aligned");
-    KvPlan p = plan_of(cache, batch, n_tokens, q_heads, window, INT_MAX);
-    if (p.work_bytes > (work ? work_bytes : 0)) {             // as many chunks as fit
-        const size_t fit = work ? work_bytes / (p.work_bytes / p.splits) : 0;
-        p = plan_of(cache, batch, n_tokens, q_heads, window, fit < 1 ? 1 : (int)fit);
-    }
+    const KvPlan p = plan_of(cache, batch, n_tokens, q_heads, window, work ? work_bytes : 0);
     if (p.tiles > 65535)
         return lw_fail(LW_E_UNSUPPORTED, "more than 65535 tiles of query rows (n_seqs + n_tokens * q_heads / kv_heads / 32, "
                                          "or / 8 for few rows a sequence)");
@@ -163,8 +159,10 @@ extern "C" lw_status lw_kv_attend(const lw_kv_cache *cache, const lw_kv_batch *b
     a.group_inv = ((1u << 21) + (unsigned)a.group - 1) / (unsigned)a.group;
     a.causal = causal != 0;
     a.window = window;
+    a.target = p.target;
     a.splits = p.splits;
     a.chunk = p.chunk;
+    a.first = reinterpret_cast<int2 *>(static_cast<char *>(work) + p.first_at);
     a.slices = 1;
     a.scale = scale;
     return device(lw_launch_kv_attend(a, cache->head_dim, dtype, p, (hipStream_t)stream), "kv attend launch");

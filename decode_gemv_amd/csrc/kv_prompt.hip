@@ -266,7 +266,7 @@ __global__ __launch_bounds__(WV * 64, (D > 128 ? 1 : D > 64 ? 2 : 3)) void k_kv_
     const int split = blockIdx.z, x = order_of(gridDim.y, blockIdx.y);
     const RowTile t = row_tile<ROWS>(a, x);
     if (t.rows == 0) return;
-    const Span mine = chunk_of(a, t, split);
+    const Span mine = chunk_of(t, a.chunk, a.splits, split);
     if (split > 0 && mine.lo >= mine.hi) return;             // (chunk 0 always leaves a result)
     const int P = 1 << a.g.page_shift;
 
@@ -356,7 +356,7 @@ __global__ __launch_bounds__(WV * 64, (D > 128 ? 1 : D > 64 ? 2 : 3)) void k_kv_
         sl[wave * WIDE + m] = st.l;
         sm[wave * WIDE + m] = st.mo;
     }
-    float *part = chunks_of(a, t) > 1 ? part_of<D, ROWS>(a, x, head, split) : nullptr;
+    float *part = chunks_of(t, a.chunk, a.splits) > 1 ? part_of<D, ROWS>(a, (int64_t)x * a.splits + split, head) : nullptr;
     float *so = reinterpret_cast<float *>(mem) + wave * (WIDE * ROWF);
 #pragma unroll
     for (int pass = 0; pass < D / PD; pass++) {

@@ -261,6 +261,21 @@ def test_attend_in_chunks(torch, dg, D, group, new):
         assert torch.equal(out, again) and torch.equal(lse, lse2), "not deterministic"
 
 
+@pytest.mark.parametrize("seqs,kv,group,new", [(64, 1, 2, 1), (65, 2, 4, 1), (130, 1, 3, 4), (200, 3, 1, 1)])
+def test_ragged_batches_in_chunks(torch, dg, seqs, kv, group, new):
+    """Sequences of all lengths, some without new tokens, cut into chunks of one size for the batch."""
+    rng = np.random.default_rng(seqs)
+    lens = [int(rng.integers(new, 1300)) if i % 3 else new for i in range(seqs)]
+    lens[seqs // 2], lens[-1] = 2600, 1100
+    count = [0 if i % 7 == 5 else 1 + i % new for i in range(seqs)]
+    s = Setup(torch, dg, kv, 64, 64, count, lens, 19 + seqs).fill()
+    q = s.tensor(kv * group, "bf16")
+    for kw in (dict(), dict(window=1500), dict(causal=False)):
+        say("ragged", seqs, kv, group, new, kw)
+        out, lse = run(s, q, "bf16", **kw)
+        check(s, q, out, lse, "bf16", **kw)
+
+
 @pytest.mark.parametrize("how", ["fused", "heads first", "misaligned"])
 def test_attend_strides(torch, dg, how):
     s = Setup(torch, dg, 2, 128, 32, [3, 1], [80, 40], 55).fill()
