@@ -21,6 +21,8 @@ def __getattr__(name):
         return importlib.import_module(__name__ + "." + name)
     lw = importlib.import_module(__name__ + ".lw")
     try:
-        return getattr(lw, name)
+        value = getattr(lw, name)
     except AttributeError:
         raise AttributeError(f"module 'decode_gemv_amd' has no attribute {name!r}") from None
+    globals()[name] = value              # found here from now on: the way through __getattr__ costs 2 us a call
+    return value
