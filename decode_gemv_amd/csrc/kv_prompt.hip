@@ -23,8 +23,8 @@
 // bound by those.
 //
 // Measured, heads of 128 in bf16, 32 of them on 8: 16384 tokens on themselves
-// 811 TFLOP/s (tiles of 32 rows of kv_attend.hip: 633), 2048 on 16384 750
-// (638), 2048 on themselves 372 (354).
+// 823 TFLOP/s (tiles of 32 rows of kv_attend.hip: 633), 2048 on 16384 753
+// (638), 2048 on themselves 389 (354).
 //
 // Rounding: as in kv_attend.hip, but p dv is rounded to fp16 once for fp16
 // outputs too.  Its error, at random 2^-12 of a part of the output, comes to
@@ -154,9 +154,25 @@ __device__ __forceinline__ void step(Rows<D> &st, const Tile<D> &tile, int sub, 
     f16v acc;
 #pragma unroll
     for (int i = 0; i < 16; i++) acc[i] = 0.0f;
+    // operands are read eight ahead of their use, held there by the fences (the
+    // compiler would wait for each; heads of 256: 458 TFLOP/s and not 500), and
+    // where there are registers, those of the values before the exponentials
+    constexpr int KG = L::PER < 8 ? L::PER : 8;
+    constexpr bool EARLYV = D > 64, EARLYF = D > 128;
+    auto values = [&](int kk, int n) { return *reinterpret_cast<const uint4 *>(&tile.v[sub][kk][n][lane][0]); };
+    uint4 kw[KG];
 #pragma unroll
-    for (int j = 0; j < L::PER; j++)
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, tile.k[sub][j][lane]), st.q[j], acc, 0, 0, 0);
+    for (int j = 0; j < KG; j++) kw[j] = tile.k[sub][j][lane];
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int j = 0; j < L::PER; j++) {
+        const h8 k = __builtin_bit_cast(h8, kw[j % KG]);
+        if (j + KG < L::PER) {
+            kw[j % KG] = tile.k[sub][j + KG][lane];
+            asm volatile("" ::: "memory");
+        }
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, st.q[j], acc, 0, 0, 0);
+    }
     // a lane's tokens: 8 a + 4 g + b, its four of every eight
     float s[4][4], top = -__builtin_inff(), dtop = 0.0f;
     const float4 *kf = reinterpret_cast<const float4 *>(&tile.kf[sub * 32 + 4 * g]);
@@ -193,6 +209,17 @@ __device__ __forceinline__ void step(Rows<D> &st, const Tile<D> &tile, int sub, 
             }
         }
     }
+    float4 fv[8];
+    if (EARLYF) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) fv[i] = vf[4 * (i / 2) + i % 2];
+    }
+    uint4 vw[2][L::NT];
+    if (EARLYV) {
+#pragma unroll
+        for (int n = 0; n < L::NT; n++) vw[0][n] = values(0, n);
+    }
+    if (EARLYF || EARLYV) asm volatile("" ::: "memory");
 #pragma unroll
     for (int a = 0; a < 4; a++)
 #pragma unroll
@@ -223,7 +250,7 @@ __device__ __forceinline__ void step(Rows<D> &st, const Tile<D> &tile, int sub, 
 #pragma unroll
         for (int c = 0; c < 4; c++) {
             const int a = 2 * kk + c / 2;
-            const float4 x = vf[4 * a + c % 2];              // (dv, 8 dv - mv) of two tokens
+            const float4 x = EARLYF ? fv[2 * a + c % 2] : vf[4 * a + c % 2];      // (dv, 8 dv - mv) of two tokens
 #pragma unroll
             for (int b = 0; b < 2; b++) {
                 const float p = __builtin_amdgcn_exp2f(fmaf(s[a][c % 2 * 2 + b], st.qs, -st.mo));
@@ -232,9 +259,14 @@ __device__ __forceinline__ void step(Rows<D> &st, const Tile<D> &tile, int sub, 
                 e[2 * c + b] = (_Float16)(p * (b ? x.z : x.x));
             }
         }
+        if (EARLYV && kk == 0) {
+#pragma unroll
+            for (int n = 0; n < L::NT; n++) vw[1][n] = values(1, n);
+            asm volatile("" ::: "memory");
+        }
 #pragma unroll
         for (int n = 0; n < L::NT; n++) {
-            const h8 v = __builtin_bit_cast(h8, *reinterpret_cast<const uint4 *>(&tile.v[sub][kk][n][lane][0]));
+            const h8 v = __builtin_bit_cast(h8, EARLYV ? vw[kk][n] : values(kk, n));
             st.o[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, e, st.o[n], 0, 0, 0);
         }
     }
