@@ -13,17 +13,19 @@
 // has to be joined at the end, and two workgroups stand on a CU whose phases
 // (unpacking, products, exponentials) fill each other's gaps.
 //
-// What bounds it: per 64 tokens a wavefront has 1024 cycles of matrix
-// instructions, some 2000 of other vector instructions (half of them the
-// exponentials, sums and conversions of its 32 scores a lane) and reads 48 KB
-// of LDS; on a SIMD with two of them that takes 6500 cycles, with all three
-// pipes between 30 and 65 % busy.  One workgroup alone on a CU takes 5700 for
-// its own, so the calls that leave the longest rows' workgroups alone at the
-// end (prompts of up to 2048 tokens, where all are there from the start) are
-// bound by those.
+// What bounds it: issue.  For 32 tokens and 32 rows of 128 dimensions a
+// wavefront has 512 cycles of matrix instructions and some 830 of others, at
+// what they were measured to take (4 to 4.6 a multiply-add, a conversion or an
+// operation on packed halves, 2.6 a multiplication or addition, 8.5 an
+// exponential: 16 elements a lane with 9 of them, and 43 operations of
+// unpacking), and a SIMD does one such part in 1430: the two kinds hardly
+// overlap.  A wavefront alone on its SIMD issues one instruction in 5.4 cycles
+// and takes as long for a part as two side by side, so the calls that leave
+// the longest rows' workgroups alone at the end (prompts of up to 2048 tokens,
+// where all are there from the start) are bound by those.
 //
 // Measured, heads of 128 in bf16, 32 of them on 8: 16384 tokens on themselves
-// 823 TFLOP/s (tiles of 32 rows of kv_attend.hip: 633), 2048 on 16384 753
+// 849 TFLOP/s (tiles of 32 rows of kv_attend.hip: 633), 2048 on 16384 778
 // (638), 2048 on themselves 389 (354).
 //
 // Rounding: as in kv_attend.hip, but p dv is rounded to fp16 once for fp16
@@ -55,8 +57,7 @@ struct Tile {
     uint4 k[SUBS][PER][64];                                  // operands of K Q^T
     uint2 v[SUBS][2][NT][64][2];                             // operands of V^T P^T
     float2 kf[TT], vf[TT];                                   // dk, 8 dk - mk; dv, 8 dv - mv
-    uint32_t here[WV];                                       // whether the tokens a wavefront unpacked are present
-    float dmax[WV];                                          // and their largest dv
+    float dmax[WV];                                          // largest dv of the tokens that a wavefront unpacked
 };
 
 // What a wavefront has loaded of a tile.
@@ -64,8 +65,7 @@ template <int D>
 struct Raw {
     uint32_t k[Tile<D>::KW];
     uint4 v;
-    uint32_t dm;                 // lanes below TPW: a key's pair, the next TPW: a value's
-    bool here;
+    uint32_t dm;                 // lanes below TPW: a key's pair, the others: a value's
 };
 
 // Where a thread's operands go in a tile, in bytes: its first key word's, its
@@ -118,19 +118,21 @@ __device__ __forceinline__ void unpack(Tile<D> &o, const Raw<D> &r, const Put<D>
     // (so that it reaches the rows that see it, and only zeros the others)
     float d = half_lo(r.dm), c = fmaf(d, 8.0f, -half_hi(r.dm));
     const bool odd = !(fabsf(c) < __builtin_inff());
-    const bool bad = __shfl((int)odd, lane + L::TPW) != 0;
+    const bool bad = __ballot(odd) >> (lane + L::TPW) & 1;   // (for the lanes of keys)
     if (lane < L::TPW) {
         o.kf[wave * L::TPW + lane] = make_float2(d, bad ? __builtin_nanf("") : c);
-    } else {
-        d = odd ? 0.0f : d;
-        if (lane < 2 * L::TPW) o.vf[wave * L::TPW + lane % L::TPW] = make_float2(d, odd ? 0.0f : c);
+    } else if (lane < 2 * L::TPW) {
+        o.vf[wave * L::TPW + lane % L::TPW] = make_float2(odd ? 0.0f : d, odd ? 0.0f : c);
     }
-#pragma unroll
-    for (int i = 1; i < L::TPW; i *= 2) d = fmaxf(d, __shfl_xor(d, i));
-    if (lane == L::TPW) {
-        o.here[wave] = r.here;
-        o.dmax[wave] = d;
-    }
+    d = odd ? 0.0f : d;
+    auto most = [&](auto ctrl) {
+        d = fmaxf(d, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, d), ctrl.value, 0xF, 0xF, false)));
+    };
+    most(std::integral_constant<int, 0xB1>{});               // lane ^ 1
+    most(std::integral_constant<int, 0x4E>{});               // lane ^ 2
+    most(std::integral_constant<int, 0x141>{});              // 7 - lane of eight
+    if (L::TPW == 16) most(std::integral_constant<int, 0x140>{});             // 15 - lane of sixteen
+    if (lane == L::TPW) o.dmax[wave] = d;
 }
 
 template <int D>
@@ -156,13 +158,24 @@ __device__ __forceinline__ void step(Rows<D> &st, const Tile<D> &tile, int sub, 
     for (int i = 0; i < 16; i++) acc[i] = 0.0f;
     // operands are read eight ahead of their use, held there by the fences (the
     // compiler would wait for each; heads of 256: 458 TFLOP/s and not 500), and
-    // where there are registers, those of the values before the exponentials
+    // where there are registers, those of the values before the exponentials and
+    // the keys' factors before the products
     constexpr int KG = L::PER < 8 ? L::PER : 8;
-    constexpr bool EARLYV = D > 64, EARLYF = D > 128;
+    constexpr bool EARLYV = D > 64, EARLYK = D > 128;
     auto values = [&](int kk, int n) { return *reinterpret_cast<const uint4 *>(&tile.v[sub][kk][n][lane][0]); };
+    const float4 *kf = reinterpret_cast<const float4 *>(&tile.kf[sub * 32 + 4 * g]);
+    const float4 *vf = reinterpret_cast<const float4 *>(&tile.vf[sub * 32 + 4 * g]);
     uint4 kw[KG];
+    float4 fk[8];
 #pragma unroll
     for (int j = 0; j < KG; j++) kw[j] = tile.k[sub][j][lane];
+    if (EARLYK) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) fk[i] = kf[4 * (i / 2) + i % 2];
+    }
+    float dm[PIECES];
+#pragma unroll
+    for (int i = 0; i < PIECES; i++) dm[i] = tile.dmax[sub * PIECES + i];
     asm volatile("" ::: "memory");
 #pragma unroll
     for (int j = 0; j < L::PER; j++) {
@@ -175,26 +188,19 @@ __device__ __forceinline__ void step(Rows<D> &st, const Tile<D> &tile, int sub, 
     }
     // a lane's tokens: 8 a + 4 g + b, its four of every eight
     float s[4][4], top = -__builtin_inff(), dtop = 0.0f;
-    const float4 *kf = reinterpret_cast<const float4 *>(&tile.kf[sub * 32 + 4 * g]);
-    const float4 *vf = reinterpret_cast<const float4 *>(&tile.vf[sub * 32 + 4 * g]);
 #pragma unroll
     for (int a = 0; a < 4; a++) {
-        const float4 x = kf[4 * a], y = kf[4 * a + 1];
+        const float4 x = EARLYK ? fk[2 * a] : kf[4 * a], y = EARLYK ? fk[2 * a + 1] : kf[4 * a + 1];
         s[a][0] = fmaf(acc[4 * a], x.x, x.y * st.qsum);
         s[a][1] = fmaf(acc[4 * a + 1], x.z, x.w * st.qsum);
         s[a][2] = fmaf(acc[4 * a + 2], y.x, y.y * st.qsum);
         s[a][3] = fmaf(acc[4 * a + 3], y.z, y.w * st.qsum);
     }
 #pragma unroll
-    for (int i = 0; i < PIECES; i++) dtop = fmaxf(dtop, tile.dmax[sub * PIECES + i]);
+    for (int i = 0; i < PIECES; i++) dtop = fmaxf(dtop, dm[i]);
     if (masked) {
         int first = t0 + 4 * g - seen.lo;
         asm volatile("" : "+v"(first));                      // (kept from being worked out ahead of the loop)
-        uint32_t here = 0;
-#pragma unroll
-        for (int i = 0; i < PIECES; i++)
-            here |= (tile.here[sub * PIECES + i] ? (L::TPW == 16 ? 0xFFFFu : 0xFFu) : 0u) << (i * L::TPW);
-        here >>= 4 * g;
         dtop = 0.0f;                                         // of what the row sees
 #pragma unroll
         for (int a = 0; a < 4; a++) {
@@ -202,24 +208,18 @@ __device__ __forceinline__ void step(Rows<D> &st, const Tile<D> &tile, int sub, 
             const float dv[4] = {x.x, x.z, y.x, y.z};
 #pragma unroll
             for (int b = 0; b < 4; b++) {
-                const bool out = (unsigned)(first + 8 * a + b) >= (unsigned)(seen.hi - seen.lo) ||
-                                 !(here >> (8 * a + b) & 1u);
+                const bool out = (unsigned)(first + 8 * a + b) >= (unsigned)(seen.hi - seen.lo);
                 s[a][b] = out ? -__builtin_inff() : s[a][b];
                 dtop = fmaxf(dtop, out ? 0.0f : dv[b]);
             }
         }
-    }
-    float4 fv[8];
-    if (EARLYF) {
-#pragma unroll
-        for (int i = 0; i < 8; i++) fv[i] = vf[4 * (i / 2) + i % 2];
     }
     uint4 vw[2][L::NT];
     if (EARLYV) {
 #pragma unroll
         for (int n = 0; n < L::NT; n++) vw[0][n] = values(0, n);
     }
-    if (EARLYF || EARLYV) asm volatile("" ::: "memory");
+    if (EARLYV) asm volatile("" ::: "memory");
 #pragma unroll
     for (int a = 0; a < 4; a++)
 #pragma unroll
@@ -250,7 +250,7 @@ __device__ __forceinline__ void step(Rows<D> &st, const Tile<D> &tile, int sub, 
 #pragma unroll
         for (int c = 0; c < 4; c++) {
             const int a = 2 * kk + c / 2;
-            const float4 x = EARLYF ? fv[2 * a + c % 2] : vf[4 * a + c % 2];      // (dv, 8 dv - mv) of two tokens
+            const float4 x = vf[4 * a + c % 2];              // (dv, 8 dv - mv) of two tokens
 #pragma unroll
             for (int b = 0; b < 2; b++) {
                 const float p = __builtin_amdgcn_exp2f(fmaf(s[a][c % 2 * 2 + b], st.qs, -st.mo));
@@ -303,17 +303,24 @@ __global__ __launch_bounds__(WV * 64, (D > 128 ? 1 : D > 64 ? 2 : 3)) void k_kv_
     const int P = 1 << a.g.page_shift;
 
     const int32_t *pages = a.g.table + (int64_t)t.seq * a.g.stride;
-    // a wavefront's tokens of the tile at t0 lie in one page: its place there,
-    // and its table entry (of a tile past the end: the last one's)
+    // 32 tokens lie in one page: the entries of a tile's (of a tile past the
+    // end: the last one's), one a lane
     const int piece = wave * L::TPW & ~15;
-    auto entry_at = [&](int t0) { return pages[min(t0 + piece, mine.hi - 1) >> a.g.page_shift]; };
+    auto entries_at = [&](int t0) { return pages[min(t0 + lane % L::SUBS * 32, mine.hi - 1) >> a.g.page_shift]; };
+    auto known = [&](int32_t entries) {                      // which of them name a page
+        uint32_t bits = 0;
+#pragma unroll
+        for (int i = 0; i < L::SUBS; i++)
+            bits |= (uint32_t)__builtin_amdgcn_readlane(entries, i) < a.g.n_pages ? 1u << i : 0u;
+        return bits;
+    };
     Raw<D> raw;
-    auto load = [&](int t0, int32_t entry) {
-        raw.here = (uint32_t)entry < a.g.n_pages && t0 + piece < mine.hi;
+    auto load = [&](int t0, int32_t entries) {
+        const uint32_t entry = (uint32_t)__builtin_amdgcn_readlane(entries, piece / 32);
+        const bool here = entry < a.g.n_pages && t0 + piece < mine.hi;
         const auto block = __builtin_amdgcn_make_buffer_rsrc(
-            a.g.pages + (uint64_t)(raw.here ? (uint32_t)entry : 0u) * (uint64_t)a.g.page_bytes +
-                (uint32_t)head * (uint32_t)a.g.block_bytes,
-            0, raw.here ? a.g.block_bytes : 0, 0x00027000);
+            a.g.pages + (uint64_t)(here ? entry : 0u) * (uint64_t)a.g.page_bytes + (uint32_t)head * (uint32_t)a.g.block_bytes,
+            0, here ? a.g.block_bytes : 0, 0x00027000);
         const uint32_t at = (t0 + piece) & (P - 1), in = wave * L::TPW & 15;     // (TPW 8: half of the piece's tokens)
         const uint32_t k = (threadIdx.x / L::KS % (L::U * 16) * L::W + threadIdx.x % L::KS * L::KW) * 4;
         if constexpr (L::KW == 4) {
@@ -333,14 +340,17 @@ __global__ __launch_bounds__(WV * 64, (D > 128 ? 1 : D > 64 ? 2 : 3)) void k_kv_
     const Masks mk = masks();
     const Put<D> put(threadIdx.x);
     const bool any = mine.lo < mine.hi;
-    int32_t after = -1;
+    uint32_t now = 0, next = 0;                              // the parts with a page of the tile in use, and of the one loaded;
+    int32_t after = -1;                                      // the entries of the one after it
     {
         Query<D, WIDE, T> q;
         const int2 at = token_of(a, t, min(wave * WIDE + m, t.rows - 1));
         q.load(a.q, t.row0 + at.x, (int64_t)head * a.group + at.y, lane);
         if (any) {
-            load(mine.lo, __builtin_amdgcn_readfirstlane(entry_at(mine.lo)));
-            after = entry_at(mine.lo + L::TT);
+            const int32_t entries = entries_at(mine.lo);
+            load(mine.lo, entries);
+            now = known(entries);
+            after = entries_at(mine.lo + L::TT);
         }
         q.make(st.qs, st.qsum, a.scale, [&](int j, h8 y) { st.q[j] = y; });
     }
@@ -357,26 +367,27 @@ __global__ __launch_bounds__(WV * 64, (D > 128 ? 1 : D > 64 ? 2 : 3)) void k_kv_
     const Span first = span_of(a, t, wave * WIDE), last = span_of(a, t, wave * WIDE + max(rows, 1) - 1);
     if (any) {
         unpack<D>(tiles[0], raw, put, mk, wave, lane);
-        load(mine.lo + L::TT, __builtin_amdgcn_readfirstlane(after));
-        after = entry_at(mine.lo + 2 * L::TT);
+        load(mine.lo + L::TT, after);
+        next = known(after);
+        after = entries_at(mine.lo + 2 * L::TT);
         __syncthreads();
         int buf = 0;
         for (int t0 = mine.lo; t0 < mine.hi; t0 += L::TT) {
             // the next tile's other buffer was last read before the barrier
             if (t0 + L::TT < mine.hi) unpack<D>(tiles[buf ^ 1], raw, put, mk, wave, lane);
-            load(t0 + 2 * L::TT, __builtin_amdgcn_readfirstlane(after));
-            after = entry_at(t0 + 3 * L::TT);
+            load(t0 + 2 * L::TT, after);
+            const uint32_t behind = known(after);
+            after = entries_at(t0 + 3 * L::TT);
             const Tile<D> &tile = tiles[buf];
 #pragma unroll
             for (int sub = 0; sub < L::SUBS; sub++) {
                 const int ts = t0 + sub * 32;
                 if (rows <= 0 || ts >= last.hi || ts + 32 <= first.lo || ts >= mine.hi) continue;
-                bool whole = true;
-#pragma unroll
-                for (int i = 0; i < 32 / L::TPW; i++)
-                    whole &= __builtin_amdgcn_readfirstlane(tile.here[sub * (32 / L::TPW) + i]) != 0;
-                step<D>(st, tile, sub, ts, !whole || rows < WIDE || ts < last.lo || ts + 32 > first.hi, seen, lane);
+                if (!(now >> sub & 1u)) continue;                      // (32 absent tokens)
+                step<D>(st, tile, sub, ts, rows < WIDE || ts < last.lo || ts + 32 > first.hi, seen, lane);
             }
+            now = next;
+            next = behind;
             __syncthreads();
             buf ^= 1;
         }
