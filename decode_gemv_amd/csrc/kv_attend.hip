@@ -574,13 +574,19 @@ KvPlan lw_kv_plan(int head_dim, int kv_heads, int group, int64_t n_seqs, int64_t
     if (window) span = std::min<int64_t>(span, (int64_t)window + (p.tile + group - 1) / group + STEP);
     const size_t result = (size_t)kv_heads * p.tile * (head_dim + 2) * sizeof(float);
     if (p.tile == 128) {
-        // Workgroups that fill the chip: two stand on a CU, and more chunks
-        // than they need cost their results' way through memory (2048 new
-        // tokens on themselves: 101 us with 1024, 93 with 512)
-        const int64_t base = std::max(n_seqs, rows / p.tile) * kv_heads;
-        p.splits = (int)std::min({(512 + base - 1) / base, (span + LEAST - 1) / LEAST, (int64_t)(room / result) / p.tiles});
-        p.splits = std::max(p.splits, 1);
-        p.chunk = (int)(((span + p.splits - 1) / p.splits + CHUNK - 1) / CHUNK * CHUNK);
+        // Chunks of at least 512 tokens for two workgroups a CU: more cost their
+        // results' way through memory (2048 new tokens on themselves: 101 us
+        // with twice as many, 93 so).  Shorter ones, of 256 tokens (heads of
+        // 256: 128), where all then still find a CU of their own: up to 446
+        // new tokens on 1434, 8 heads of 64, 25.5 us and 32.7; 97 and 7 on up
+        // to 1559, 5 heads of 256 on 1, 28.4 and 51.8.
+        const int64_t base = std::max(n_seqs, (rows + p.tile - 1) / p.tile) * kv_heads;
+        const int64_t least = head_dim > 128 ? CHUNK : 2 * CHUNK;
+        int64_t splits = std::max(std::min((512 + base - 1) / base, (span + LEAST - 1) / LEAST),
+                                  std::min(256 / base, (span + least - 1) / least));
+        splits = std::max<int64_t>(std::min(splits, (int64_t)(room / result) / p.tiles), 1);
+        p.chunk = (int)(((span + splits - 1) / splits + CHUNK - 1) / CHUNK * CHUNK);
+        p.splits = (int)std::max<int64_t>((span + p.chunk - 1) / std::max(p.chunk, 1), 1);
         p.work_bytes = p.splits > 1 ? p.tiles * p.splits * result : 0;
         return p;
     }
