@@ -1,4 +1,5 @@
-"""MI355X (gfx950) GEMV over losslessly entropy-coded LLM weights.
+"""MI355X (gfx950) GEMV over losslessly entropy-coded LLM weights, and a 4-bit
+key/value cache with the attention that reads it.
 
 The product is the C-ABI library liblw.so (include/lw.h); this package holds
 its HIP/C++ sources (csrc/), the build script and a thin ctypes binding (lw)
