@@ -39,14 +39,15 @@ struct KvAttend {
     uint32_t group_inv;          // ceil(2^21 / group): (x * group_inv) >> 21 = x / group for x < 2048
     int32_t causal, window;      // window 0: none
     int32_t target;              // chunks of tokens per kv head to cut the batch into (kv_attend.hpp), or 0:
-    int32_t splits, chunk;       // every row tile into that many at most, of so many tokens
+    int32_t splits, chunk;       // every row tile into that many at most, of so many tokens (kv_prompt.hip)
+    int32_t pieces;              // a kv head's workgroups, all with nothing to do included
     int2 *first;                 // target > 0: each row tile's first chunk's number, and the tokens of a chunk
     int32_t slices;              // of k_kv_join's workgroups
     float scale;                 // > 0
 };
 
 // How a call is cut up: rows per tile, row tiles, and chunks as in KvAttend;
-// all of a kv head's chunks at most, with target; the bytes of their results.
+// a kv head's pieces of work (chunks, or row tiles); the bytes of their results.
 struct KvPlan {
     int tile;
     int64_t tiles;

@@ -30,7 +30,7 @@
 // its wavefronts take 32-token tiles in turn and meet in LDS at the end.
 // Where row tiles are few, sequences are cut into chunks of one size for the
 // whole batch (piece_of) and k_kv_join adds the chunks' partial results, in
-// order: results do not depend on timing.  (More than 64 rows a sequence: kv_prompt.hip.)
+// order: results do not depend on timing.  (Much work: kv_prompt.hip.)
 //
 // Rounding: q is scaled by a power of two per row and held in fp16 (exact for
 // fp16 and bf16 inputs but for elements 2^29 below the row's largest); p dv
@@ -93,9 +93,7 @@ struct Shape {
     // LDS, one copy for the workgroup: D/4 registers fewer, which is a second
     // wavefront per SIMD, for D/16 reads a step
     static constexpr bool QREG = ROWS <= 16;
-    // Passes over the head's dimensions in which the wavefronts' results meet
-    static constexpr int PASSES = NW * WIDE * D > 16384 ? 2 : 1;
-    static constexpr int PD = D / PASSES, ROWF = PD + 4;     // dimensions of a pass; a row in LDS, spread over the banks
+    static constexpr int ROWF = D + 4;                       // a row in LDS where the wavefronts' results meet, spread over the banks
 };
 
 // A lane's tokens of a step: scores, and probabilities in pairs.
@@ -384,7 +382,9 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, ROWS, std::is_same<T, _Float16>:
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int m = lane % H::WIDE, g = lane / H::WIDE, head = blockIdx.x;
     Piece piece = {0, INT_MAX, 0};
-    const RowTile t = a.target ? piece_of<ROWS>(a, blockIdx.y, piece) : row_tile<ROWS>(a, tile_at(gridDim.y, blockIdx.y));
+    const int y = blockIdx.z * gridDim.y + blockIdx.y;
+    if (y >= a.pieces) return;
+    const RowTile t = a.target ? piece_of<ROWS>(a, y, piece) : row_tile<ROWS>(a, tile_at(a.pieces, y));
     if (t.rows == 0) return;
     const Span mine = chunk_of(t, piece.chunk, INT_MAX, piece.split);
     if (piece.split > 0 && mine.lo >= mine.hi) return;       // (chunk 0 always leaves a result)
@@ -497,42 +497,35 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, ROWS, std::is_same<T, _Float16>:
     float *part = chunks_of(t, piece.chunk, INT_MAX) > 1 ? part_of<D, ROWS>(a, piece.n, head) : nullptr;
     const float f = __builtin_amdgcn_exp2f(st.mo - mo), fixed = st.z * f;
 #pragma unroll
-    for (int pass = 0; pass < H::PASSES; pass++) {
-        if (pass) __syncthreads();
+    for (int i = 0; i < S::TILES; i++)
 #pragma unroll
-        for (int i = 0; i < S::TILES; i++)
+        for (int j = 0; j < M::ACC; j++) {
+            const int r = i / H::NT, n = i % H::NT;
+            const int row = H::WIDE == 16 ? 4 * g + j : 8 * (j / 4) + 4 * g + j % 4;  // along the head
+            const int d = 8 * (row % H::DW + r * H::WIDE) + (row / H::DW) * H::NT + n;
+            so[(wave * H::WIDE + m) * H::ROWF + d] = fmaf(st.o[i][j], n % 2 ? 0x1p-4f * f : f, fixed);
+        }
+    __syncthreads();
+    for (int i = threadIdx.x; i < t.rows * (D / 8); i += NW * 64) {
+        const int r = i / (D / 8), d = i % (D / 8) * 8;
+        float y[8], top = sm[r], l = 0.0f;
 #pragma unroll
-            for (int j = 0; j < M::ACC; j++) {
-                const int r = i / H::NT, n = i % H::NT;
-                const int row = H::WIDE == 16 ? 4 * g + j : 8 * (j / 4) + 4 * g + j % 4;  // along the head
-                const int d = 8 * (row % H::DW + r * H::WIDE) + (row / H::DW) * H::NT + n;
-                // (a pass is the first or second half of j, or of r)
-                if (H::PASSES > 1 && (H::REPS > 1 ? r : j / (M::ACC / 2)) != pass) continue;
-                so[(wave * H::WIDE + m) * H::ROWF + d % H::PD] = fmaf(st.o[i][j], n % 2 ? 0x1p-4f * f : f, fixed);
-            }
-        __syncthreads();
-        for (int i = threadIdx.x; i < t.rows * (H::PD / 8); i += NW * 64) {
-            const int r = i / (H::PD / 8), d0 = i % (H::PD / 8) * 8;
-            float y[8], top = sm[r], l = 0.0f;
+        for (int w = 1; w < MEET; w++) top = fmaxf(top, sm[w * ROWS + r]);
 #pragma unroll
-            for (int w = 1; w < MEET; w++) top = fmaxf(top, sm[w * ROWS + r]);
+        for (int w = 0; w < MEET; w++) l += sl[w * ROWS + r] * __builtin_amdgcn_exp2f(sm[w * ROWS + r] - top);
 #pragma unroll
-            for (int w = 0; w < MEET; w++) l += sl[w * ROWS + r] * __builtin_amdgcn_exp2f(sm[w * ROWS + r] - top);
+        for (int j = 0; j < 8; j++) y[j] = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 8; j++) y[j] = 0.0f;
+        for (int w = 0; w < MEET; w++)
 #pragma unroll
-            for (int w = 0; w < MEET; w++)
+            for (int j = 0; j < 8; j++) y[j] += so[(w * ROWS + r) * H::ROWF + d + j];
+        if (part) {
 #pragma unroll
-                for (int j = 0; j < 8; j++) y[j] += so[(w * ROWS + r) * H::ROWF + d0 + j];
-            const int d = pass * H::PD + d0;
-            if (part) {
-#pragma unroll
-                for (int j = 0; j < 8; j += 4)
-                    *reinterpret_cast<float4 *>(part + r * D + d + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
-                if (d == 0) *reinterpret_cast<float2 *>(part + ROWS * D + 2 * r) = make_float2(top, l);
-            } else {
-                write_row<D, T>(a, t, head, r, d, y, l, top);
-            }
+            for (int j = 0; j < 8; j += 4)
+                *reinterpret_cast<float4 *>(part + r * D + d + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+            if (d == 0) *reinterpret_cast<float2 *>(part + ROWS * D + 2 * r) = make_float2(top, l);
+        } else {
+            write_row<D, T>(a, t, head, r, d, y, l, top);
         }
     }
 }
@@ -540,7 +533,8 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, ROWS, std::is_same<T, _Float16>:
 template <int D, int ROWS, class T>
 hipError_t launch(const KvAttend &a, const KvPlan &p, hipStream_t s)
 {
-    hipLaunchKernelGGL((k_kv_attend<D, ROWS, T>), dim3(a.g.kv_heads, (unsigned)(p.target ? p.pieces : p.tiles)), dim3(NW * 64), 0, s, a);
+    const unsigned y = (unsigned)std::min<int64_t>(p.pieces, 1 << 15), z = (unsigned)((p.pieces + y - 1) / y);
+    hipLaunchKernelGGL((k_kv_attend<D, ROWS, T>), dim3(a.g.kv_heads, y, z), dim3(NW * 64), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !p.target) return e;
     return launch_join<D, ROWS, T>(a, p, s);
@@ -550,8 +544,9 @@ template <int D>
 hipError_t launch_dim(const KvAttend &a, int dtype, const KvPlan &p, hipStream_t s)
 {
     if (p.tile == 8) return dtype == LW_F16 ? launch<D, 8, _Float16>(a, p, s) : launch<D, 8, __bf16>(a, p, s);
-    if (p.tile == 16) return dtype == LW_F16 ? launch<D, 16, _Float16>(a, p, s) : launch<D, 16, __bf16>(a, p, s);
-    return dtype == LW_F16 ? launch<D, 32, _Float16>(a, p, s) : launch<D, 32, __bf16>(a, p, s);
+    if constexpr (D <= 128)                                  // (lw_kv_plan)
+        if (p.tile == 32) return dtype == LW_F16 ? launch<D, 32, _Float16>(a, p, s) : launch<D, 32, __bf16>(a, p, s);
+    return dtype == LW_F16 ? launch<D, 16, _Float16>(a, p, s) : launch<D, 16, __bf16>(a, p, s);
 }
 
 }  // namespace
@@ -561,29 +556,37 @@ KvPlan lw_kv_plan(int head_dim, int kv_heads, int group, int64_t n_seqs, int64_t
 {
     KvPlan p = {};
     const int64_t rows = n_tokens * group;
-    // Query rows of a tile, by the rows a sequence has on average.  128
-    // (kv_prompt.hip) against 32, heads of 128, 32 on 8 with 64 new tokens
-    // and more: 512 on 2048 54 and 59 us, 1024 on 4096 123 and 127, 4096 on
-    // themselves 210 and 264; with fewer new tokens the smaller tile wins
-    // (64 on 8192: 49 and 44).
-    p.tile = rows <= 8 * n_seqs ? 8 : rows <= 16 * n_seqs ? 16 : rows <= 64 * n_seqs ? 32 : 128;
-    p.tiles = rows / p.tile + n_seqs;
-    p.splits = 1;
     // tokens a row tile may see
     int64_t span = max_len;
-    if (window) span = std::min<int64_t>(span, (int64_t)window + (p.tile + group - 1) / group + STEP);
+    if (window) span = std::min<int64_t>(span, (int64_t)window + 128 + STEP);
+    // Query rows of a tile.  Up to 8, 16 or 32 a sequence on average: all of
+    // them (8 sequences of 20 rows on 4000 tokens, heads of 128: 28.8 us with
+    // 32 and 30.5 with 16; 32 sequences 62 and 72).  More: 128 (kv_prompt.hip)
+    // where there is work enough, by the products of 128 rows with a token,
+    // as that kernel needs many workgroups to be fast and others to follow
+    // them: 4096 tokens on 8192, 32 heads on 8 of 128, 534 us with 128, 700
+    // with 32 and 813 with 16; 1024 on 4096 (2^20) 120, 128 and 143; 1024 on
+    // themselves (2^18) 50, 43 and 41; 300 on 8000, 8 heads on 2, 48, 46 and
+    // 43.  32 to 64 rows: 16 or 32 alike (8 sequences of 64 on 4000: 39 and
+    // 46).  Heads of 256 have registers for 16 rows and a second wavefront,
+    // but not for more: 1024 on 4096, 16 heads on 4, 136 us, 219 with 32 and
+    // 164 with 128.
+    const bool much = (rows + 127) / 128 * kv_heads * std::min<int64_t>(span, 1 << 20) >= 1 << 19;
+    p.tile = rows <= 8 * n_seqs                       ? 8
+             : rows <= 16 * n_seqs || head_dim > 128 ? 16
+             : rows <= 32 * n_seqs                   ? 32
+             : !much                                 ? 16
+             : rows <= 64 * n_seqs                   ? 32
+                                                     : 128;
+    p.tiles = p.pieces = rows / p.tile + n_seqs;
+    p.splits = 1;
     const size_t result = (size_t)kv_heads * p.tile * (head_dim + 2) * sizeof(float);
     if (p.tile == 128) {
-        // Chunks of at least 512 tokens for two workgroups a CU: more cost their
-        // results' way through memory (2048 new tokens on themselves: 101 us
-        // with twice as many, 93 so).  Shorter ones, of 256 tokens (heads of
-        // 256: 128), where all then still find a CU of their own: up to 446
-        // new tokens on 1434, 8 heads of 64, 25.5 us and 32.7; 97 and 7 on up
-        // to 1559, 5 heads of 256 on 1, 28.4 and 51.8.
+        // Chunks for two workgroups a CU: more cost their results' way through
+        // memory (2048 new tokens on themselves: 101 us with twice as many,
+        // 93 so)
         const int64_t base = std::max(n_seqs, (rows + p.tile - 1) / p.tile) * kv_heads;
-        const int64_t least = head_dim > 128 ? CHUNK : 2 * CHUNK;
-        int64_t splits = std::max(std::min((512 + base - 1) / base, (span + LEAST - 1) / LEAST),
-                                  std::min(256 / base, (span + least - 1) / least));
+        int64_t splits = std::min((512 + base - 1) / base, (span + LEAST - 1) / LEAST);
         splits = std::max<int64_t>(std::min(splits, (int64_t)(room / result) / p.tiles), 1);
         p.chunk = (int)(((span + splits - 1) / splits + CHUNK - 1) / CHUNK * CHUNK);
         p.splits = (int)std::max<int64_t>((span + p.chunk - 1) / std::max(p.chunk, 1), 1);
@@ -594,14 +597,14 @@ KvPlan lw_kv_plan(int head_dim, int kv_heads, int group, int64_t n_seqs, int64_t
     // and 15.9 not, one of 1500 16.6 and 18.7; 48 sequences of 500 to 8190
     // tokens 63 and 79, 256 of 100 to 4000 139 and 132 (workgroups enough, of
     // which the chip takes the next as it is done with one).
-    if (span <= 1024 || n_seqs * kv_heads >= 1024) return p;
+    if (span <= 1024 || std::max(n_seqs, (rows + p.tile - 1) / p.tile) * kv_heads >= 1024) return p;
     // Into about 768 pieces, three for a CU: 16 sequences of 501 to 8190 tokens
     // take 26.8 us, with 1024 28.1 and with 1536 30.3; one of 131071 43.5,
     // 43.3 and 47; 32 of 16384 116, 119 and 120.
     const size_t notes = p.tiles * sizeof(int2);
     int64_t pieces = std::max(768 / kv_heads, 1) + p.tiles;
     if (room < notes || (room - notes) / result < (size_t)pieces) pieces = room < notes ? 0 : (room - notes) / result;
-    if (pieces <= p.tiles || pieces > 65535) return p;
+    if (pieces <= p.tiles) return p;
     p.target = (int)(pieces - p.tiles);
     p.pieces = pieces;
     p.first_at = pieces * result;

@@ -150,9 +150,8 @@ extern "C" lw_status lw_kv_attend(const lw_kv_cache *cache, const lw_kv_batch *b
     if (!aligned(lse, 4)) return lw_fail(LW_E_ARG, "lse must be 4-byte aligned");
     if (!aligned(work, 16)) return lw_fail(LW_E_ARG, "work must be 16-byte aligned");
     const KvPlan p = plan_of(cache, batch, n_tokens, q_heads, window, work ? work_bytes : 0);
-    if (p.tiles > 65535)
-        return lw_fail(LW_E_UNSUPPORTED, "more than 65535 tiles of query rows (n_seqs + n_tokens * q_heads / kv_heads / 32, "
-                                         "or / 8 for few rows a sequence)");
+    if (p.tile == 128 && p.tiles > 65535)
+        return lw_fail(LW_E_UNSUPPORTED, "more than 65535 tiles of query rows (n_seqs + n_tokens * q_heads / kv_heads / 128)");
     a.lse = lse;
     a.part = static_cast<float *>(work);
     a.group = q_heads / cache->kv_heads;
@@ -162,6 +161,7 @@ extern "C" lw_status lw_kv_attend(const lw_kv_cache *cache, const lw_kv_batch *b
     a.target = p.target;
     a.splits = p.splits;
     a.chunk = p.chunk;
+    a.pieces = (int32_t)p.pieces;
     a.first = reinterpret_cast<int2 *>(static_cast<char *>(work) + p.first_at);
     a.slices = 1;
     a.scale = scale;

@@ -1,10 +1,11 @@
-// kv_prompt.hip -- attention of many new tokens over the 4-bit key/value cache.
+// kv_prompt.hip -- attention of many new tokens over the 4-bit key/value cache,
+// for heads of 64 and 128 (lw_kv_plan in kv_attend.hip says when).
 //
 // The mathematics is kv_attend.hip's.  There each wavefront unpacks the codes
 // that it uses, which for many query rows is most of its work: 152 of some 400
 // instructions for 32 tokens and 32 rows.  Here a workgroup has 128 rows of a
 // sequence, 32 for each wavefront, and goes through the tokens in tiles of 64
-// (32 for heads of 256): each wavefront unpacks a quarter of a tile's keys and
+// each wavefront unpacks a quarter of a tile's keys and
 // values into LDS, laid out as the matrix operands that all four then read in
 // whole 16-byte lanes, and turns their pairs into the factors of scores and
 // values, once per token instead of once per lane.  Two buffers: a tile is
@@ -45,15 +46,13 @@ constexpr int WV = 4, WIDE = 32, ROWS = WV * WIDE;
 
 template <int D>
 struct Tile {
-    static constexpr int TT = D > 128 ? 32 : 64;             // tokens of a tile
-    static constexpr int SUBS = TT / 32;
+    static constexpr int TT = 64, SUBS = TT / 32;            // tokens of a tile
     static constexpr int DW = D / 8, PER = DW / 2;           // words of a token, and of a half of the lanes
     static constexpr int W = D >= 128 ? 4 : 2, U = DW / W;   // words of a key unit, units of a token
     static constexpr int NT = D / 32;                        // output tiles along the head
     static constexpr int TPW = TT / WV;                      // tokens of a wavefront's value words and pairs
-    static constexpr int KS = 64 * WV / (TT * U);            // threads that share a key unit, by words,
-    static constexpr int VS = 64 * WV / (TT / 4 * DW);       // and a value unit, by halves of its words
-    static constexpr int KW = W / KS;                        // key words of a thread
+    static constexpr int VS = 64 * WV / (TT / 4 * DW);       // threads that share a value unit, by halves of its words
+    static_assert(TT * U == 64 * WV, "a thread has one key unit");
     uint4 k[SUBS][PER][64];                                  // operands of K Q^T
     uint2 v[SUBS][2][NT][64][2];                             // operands of V^T P^T
     float2 kf[TT], vf[TT];                                   // dk, 8 dk - mk; dv, 8 dv - mv
@@ -63,7 +62,7 @@ struct Tile {
 // What a wavefront has loaded of a tile.
 template <int D>
 struct Raw {
-    uint32_t k[Tile<D>::KW];
+    uint32_t k[Tile<D>::W];
     uint4 v;
     uint32_t dm;                 // lanes below TPW: a key's pair, the others: a value's
 };
@@ -78,7 +77,7 @@ struct Put {
     __device__ __forceinline__ Put(int thread)
     {
         using L = Tile<D>;
-        const int ku = thread / L::KS, t = ku / (L::U * 16) * 16 + ku % 16, w = ku / 16 % L::U * L::W + thread % L::KS * L::KW;
+        const int t = thread / (L::U * 16) * 16 + thread % 16, w = thread / 16 % L::U * L::W;
         k = ((t / 32 * L::PER + w % L::PER) * 64 + t % 32 + w / L::PER * 32) * 16;
         asm("" : "+v"(k));
         // token group g of the tile: half g % 2 of the lanes, place g / 2 % 2 of the operand
@@ -99,7 +98,7 @@ __device__ __forceinline__ void unpack(Tile<D> &o, const Raw<D> &r, const Put<D>
     using L = Tile<D>;
     char *base = reinterpret_cast<char *>(&o);
 #pragma unroll
-    for (int i = 0; i < L::KW; i++) *reinterpret_cast<h8 *>(base + at.k + i * 1024) = spread8(r.k[i], mk);
+    for (int i = 0; i < L::W; i++) *reinterpret_cast<h8 *>(base + at.k + i * 1024) = spread8(r.k[i], mk);
     const uint32_t *x = reinterpret_cast<const uint32_t *>(&r.v);
 #pragma unroll
     for (int i = 0; i < Put<D>::HALVES; i++) {
@@ -131,7 +130,7 @@ __device__ __forceinline__ void unpack(Tile<D> &o, const Raw<D> &r, const Put<D>
     most(std::integral_constant<int, 0xB1>{});               // lane ^ 1
     most(std::integral_constant<int, 0x4E>{});               // lane ^ 2
     most(std::integral_constant<int, 0x141>{});              // 7 - lane of eight
-    if (L::TPW == 16) most(std::integral_constant<int, 0x140>{});             // 15 - lane of sixteen
+    most(std::integral_constant<int, 0x140>{});              // 15 - lane of sixteen
     if (lane == L::TPW) o.dmax[wave] = d;
 }
 
@@ -156,41 +155,28 @@ __device__ __forceinline__ void step(Rows<D> &st, const Tile<D> &tile, int sub, 
     f16v acc;
 #pragma unroll
     for (int i = 0; i < 16; i++) acc[i] = 0.0f;
-    // operands are read eight ahead of their use, held there by the fences (the
-    // compiler would wait for each; heads of 256: 458 TFLOP/s and not 500), and
-    // where there are registers, those of the values before the exponentials and
-    // the keys' factors before the products
-    constexpr int KG = L::PER < 8 ? L::PER : 8;
-    constexpr bool EARLYV = D > 64, EARLYK = D > 128;
+    // Operands are read ahead of their use, held there by the fences: the keys'
+    // before the products, and where there are registers, the values' before
+    // the exponentials (823 TFLOP/s and not 811)
+    constexpr bool EARLYV = D > 64;
     auto values = [&](int kk, int n) { return *reinterpret_cast<const uint4 *>(&tile.v[sub][kk][n][lane][0]); };
     const float4 *kf = reinterpret_cast<const float4 *>(&tile.kf[sub * 32 + 4 * g]);
     const float4 *vf = reinterpret_cast<const float4 *>(&tile.vf[sub * 32 + 4 * g]);
-    uint4 kw[KG];
-    float4 fk[8];
+    uint4 kw[L::PER];
 #pragma unroll
-    for (int j = 0; j < KG; j++) kw[j] = tile.k[sub][j][lane];
-    if (EARLYK) {
-#pragma unroll
-        for (int i = 0; i < 8; i++) fk[i] = kf[4 * (i / 2) + i % 2];
-    }
+    for (int j = 0; j < L::PER; j++) kw[j] = tile.k[sub][j][lane];
     float dm[PIECES];
 #pragma unroll
     for (int i = 0; i < PIECES; i++) dm[i] = tile.dmax[sub * PIECES + i];
     asm volatile("" ::: "memory");
 #pragma unroll
-    for (int j = 0; j < L::PER; j++) {
-        const h8 k = __builtin_bit_cast(h8, kw[j % KG]);
-        if (j + KG < L::PER) {
-            kw[j % KG] = tile.k[sub][j + KG][lane];
-            asm volatile("" ::: "memory");
-        }
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, st.q[j], acc, 0, 0, 0);
-    }
+    for (int j = 0; j < L::PER; j++)
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, kw[j]), st.q[j], acc, 0, 0, 0);
     // a lane's tokens: 8 a + 4 g + b, its four of every eight
     float s[4][4], top = -__builtin_inff(), dtop = 0.0f;
 #pragma unroll
     for (int a = 0; a < 4; a++) {
-        const float4 x = EARLYK ? fk[2 * a] : kf[4 * a], y = EARLYK ? fk[2 * a + 1] : kf[4 * a + 1];
+        const float4 x = kf[4 * a], y = kf[4 * a + 1];
         s[a][0] = fmaf(acc[4 * a], x.x, x.y * st.qsum);
         s[a][1] = fmaf(acc[4 * a + 1], x.z, x.w * st.qsum);
         s[a][2] = fmaf(acc[4 * a + 2], y.x, y.y * st.qsum);
@@ -285,7 +271,7 @@ __device__ __forceinline__ int order_of(int tiles, int y)
 }
 
 template <int D, class T>
-__global__ __launch_bounds__(WV * 64, (D > 128 ? 1 : D > 64 ? 2 : 3)) void k_kv_prompt(KvAttend a)
+__global__ __launch_bounds__(WV * 64, (D > 64 ? 2 : 3)) void k_kv_prompt(KvAttend a)
 {
     using L = Tile<D>;
     constexpr int PD = 64, ROWF = PD + 4;                    // dimensions of a pass of the end, and a row in LDS
@@ -305,7 +291,7 @@ __global__ __launch_bounds__(WV * 64, (D > 128 ? 1 : D > 64 ? 2 : 3)) void k_kv_
     const int32_t *pages = a.g.table + (int64_t)t.seq * a.g.stride;
     // 32 tokens lie in one page: the entries of a tile's (of a tile past the
     // end: the last one's), one a lane
-    const int piece = wave * L::TPW & ~15;
+    const int piece = wave * L::TPW;
     auto entries_at = [&](int t0) { return pages[min(t0 + lane % L::SUBS * 32, mine.hi - 1) >> a.g.page_shift]; };
     auto known = [&](int32_t entries) {                      // which of them name a page
         uint32_t bits = 0;
@@ -321,9 +307,8 @@ __global__ __launch_bounds__(WV * 64, (D > 128 ? 1 : D > 64 ? 2 : 3)) void k_kv_
         const auto block = __builtin_amdgcn_make_buffer_rsrc(
             a.g.pages + (uint64_t)(here ? entry : 0u) * (uint64_t)a.g.page_bytes + (uint32_t)head * (uint32_t)a.g.block_bytes,
             0, here ? a.g.block_bytes : 0, 0x00027000);
-        const uint32_t at = (t0 + piece) & (P - 1), in = wave * L::TPW & 15;     // (TPW 8: half of the piece's tokens)
-        const uint32_t k = (threadIdx.x / L::KS % (L::U * 16) * L::W + threadIdx.x % L::KS * L::KW) * 4;
-        if constexpr (L::KW == 4) {
+        const uint32_t at = (t0 + piece) & (P - 1), k = lane * L::W * 4;
+        if constexpr (L::W == 4) {
             const uint4 w = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(block, k, at * (D / 2), 0));
             raw.k[0] = w.x, raw.k[1] = w.y, raw.k[2] = w.z, raw.k[3] = w.w;
         } else {
@@ -331,9 +316,9 @@ __global__ __launch_bounds__(WV * 64, (D > 128 ? 1 : D > 64 ? 2 : 3)) void k_kv_
             raw.k[0] = w.x, raw.k[1] = w.y;
         }
         raw.v = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
-            block, lane / L::VS * 16, P * (D / 2) + (at + in) * (D / 2), 0));
+            block, lane / L::VS * 16, P * (D / 2) + at * (D / 2), 0));
         raw.dm = __builtin_bit_cast(uint32_t, __builtin_amdgcn_raw_buffer_load_b32(
-            block, lane % L::TPW * 4 + (lane < L::TPW ? 0 : P * 4), P * D + (at + in) * 4, 0));
+            block, lane % L::TPW * 4 + (lane < L::TPW ? 0 : P * 4), P * D + at * 4, 0));
     };
 
     Rows<D> st;
@@ -448,6 +433,5 @@ hipError_t lw_launch_kv_prompt(const KvAttend &a, int head_dim, int dtype, const
     const bool half = dtype == LW_F16;
     if (head_dim == 64) return half ? launch<64, _Float16>(a, p, s) : launch<64, __bf16>(a, p, s);
     if (head_dim == 128) return half ? launch<128, _Float16>(a, p, s) : launch<128, __bf16>(a, p, s);
-    if (head_dim == 256) return half ? launch<256, _Float16>(a, p, s) : launch<256, __bf16>(a, p, s);
     return hipErrorInvalidValue;
 }

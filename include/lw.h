@@ -492,11 +492,11 @@ lw_status lw_kv_read(const lw_kv_cache *cache, const lw_kv_batch *batch, int64_t
  *             smaller one lowers the number of chunks that a sequence is cut
  *             into, and LW_E_ARG is given only for a misaligned one
  * Scores, sums and the output's accumulation are fp32; p times a value's d
- * is rounded to fp16 (for fp16 results of up to 64 rows a sequence, with what
+ * is rounded to fp16 (for fp16 results of calls that are not large, with what
  * that leaves as a second term); sums run in a fixed order: results are
  * deterministic (a batch is cut into chunks of one size, so what else is in it
- * may move a sequence's last bits).  At most 2^30 query rows per kv head and
- * 65535 row tiles.
+ * may move a sequence's last bits).  At most 2^30 query rows per kv head, and
+ * large calls 65535 tiles of 128 rows.
  * Errors: LW_E_ARG, LW_E_UNSUPPORTED (head_dim, page_tokens, dtype),
  * LW_E_DEVICE. */
 lw_status lw_kv_attend(const lw_kv_cache *cache, const lw_kv_batch *batch, int64_t n_tokens, const lw_kv_tensor *q,

@@ -120,6 +120,32 @@ def attend(cache, table, start, lens, q, scale, causal=True, window=0):
     return out, lse, dict(size=size, mean=mean, grid=grid, seen=seen)
 
 
+def attend_one(cache, table, length, q, scale, window):
+    """attend() of one sequence whose tokens are all present, causal, by matrix products (for many rows)."""
+    n, heads, _ = q.shape
+    k, v, dk, dv, here = cache.tokens(table, length)
+    assert here.all()
+    shape = (n, heads)
+    out, lse, by = np.zeros(q.shape), np.zeros(shape), {x: np.zeros(shape) for x in ("size", "mean", "grid", "seen")}
+    pos, j = length - n + np.arange(n), np.arange(length)
+    mask = (j <= pos[:, None]) & (j > pos[:, None] - window)
+    for h in range(heads):
+        g = h * cache.kv // heads
+        kk, vv = k[:, g], v[:, g]
+        x = np.where(mask, q[:, h] @ kk.T * scale, -np.inf)
+        top = x.max(1)
+        p = np.exp(x - top[:, None])
+        total = p.sum(1)
+        out[:, h], lse[:, h] = p @ vv / total[:, None], top + np.log(total)
+        offset = 8 * dk[:, g, 0] - dk[:, g, 1]
+        size = np.abs(q[:, h]) @ np.abs(kk - offset[:, None]).T + np.abs(q[:, h]).sum(1)[:, None] * np.abs(offset)
+        by["size"][:, h] = scale * np.max(np.where(mask, size, 0), 1)
+        by["mean"][:, h] = (p @ np.abs(vv)).max(1) / total
+        by["grid"][:, h] = 8 * (p @ dv[:, g, 0]) / total
+        by["seen"][:, h] = mask.sum(1) * 8 * np.max(np.where(mask, dv[:, g, 0], 0), 1) / total
+    return out, lse, by
+
+
 def bounds(ref, lse, by, D, bf16, many=False):
     """Largest errors of out and lse.  A score is a sum of D products and two more in fp32, each addition off by at
     most a last place (the matrix cores cut off): d = (D + 8) 2^-23 of the sum of magnitudes.  An output then moves by

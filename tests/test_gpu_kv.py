@@ -374,6 +374,126 @@ def test_values_of_very_different_sizes(torch, dg):
         check(s, q, out, lse, dtype)
 
 
+# ------------------------------------------------- attention of many rows
+# Tiles of 128 rows are taken where 128 rows times tokens make 2^19 and more, by the tokens that the batch is planned for:
+# a table with room for many does that for short sequences, too.
+
+def planned_for(s, tokens):
+    wide = np.full((len(s.lens), tokens // s.P), -1, np.int32)
+    wide[:, :s.table.shape[1]] = s.table
+    s.batch = s.dg.KvBatch(s.batch.start, s.batch.lens, s.torch.from_numpy(wide).cuda())
+    return s
+
+
+MANY = [
+    # kv, group, P, new, lens: part of a tile, one and several; pages that end inside a tile of tokens; first tokens;
+    # no new tokens; fewer tokens than a wavefront takes
+    (1, 1, 32, [67], [99]), (2, 2, 32, [40], [40]), (1, 40, 64, [2], [90]), (1, 1, 64, [130], [131]),
+    (2, 1, 128, [200, 70], [260, 500]), (1, 5, 256, [100, 0, 31], [700, 10, 31]), (1, 128, 32, [1], [1]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("case", MANY, ids=lambda c: f"kv{c[0]}x{c[1]}_P{c[2]}_n{'_'.join(map(str, c[3]))}")
+def test_many_rows(torch, dg, case, D, dtype):
+    kv, group, P, new, lens = case
+    say("many", case, D, dtype)
+    s = planned_for(Setup(torch, dg, kv, D, P, new, lens, 200 + sum(lens)).fill(), 1 << 19)
+    q = s.tensor(kv * group, dtype, "fused")
+    for kw in (dict(), dict(causal=False)):
+        for work in (True, 0):
+            out, lse = run(s, q, dtype, work=work, **kw)
+            check(s, q, out, lse, dtype, **kw)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_rows_in_chunks(torch, dg, D):
+    s = planned_for(Setup(torch, dg, 1, D, 64, [128], [3000], 31 + D).fill(), 1 << 17)
+    q = s.tensor(4, "fp16")
+    whole = dg.lw_kv_attend_scratch_bytes(s.cache, s.batch, s.rows, 4)
+    for nb in (whole, whole // 40, 0):                        # 1024 tokens a chunk, 43690, all
+        say("many rows in chunks", D, nb)
+        out, lse = run(s, q, "fp16", work=nb)
+        check(s, q, out, lse, "fp16")
+        again, lse2 = run(s, q, "fp16", work=nb)
+        assert torch.equal(out, again) and torch.equal(lse, lse2), "not deterministic"
+
+
+@pytest.mark.parametrize("how", ["heads first", "misaligned"])
+def test_many_rows_strides(torch, dg, how):
+    s = planned_for(Setup(torch, dg, 2, 128, 32, [33], [80], 57).fill(), 1 << 19)
+    q = s.tensor(8, "bf16", how)
+    out, lse = run(s, q, "bf16", how=how)
+    want, want_lse = run(s, s.tensor(8, "bf16", "dense", host(q)), "bf16")
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    check(s, q, out, lse, "bf16")
+
+
+def test_many_rows_that_see_nothing(torch, dg):
+    table = [[0, -1, -1, 1], [2, 2, 2, 2], [-1, 99, -5, -1]]
+    for D in (64, 128):
+        for dtype in ("fp16", "bf16"):
+            s = Setup(torch, dg, 1, D, 32, [2, 5, 3], [90, 2, 128], 63, table=table, n_pages=3).fill()
+            planned_for(s, 1 << 18)
+            q = s.tensor(40, dtype)
+            for kw in (dict(), dict(causal=False)):
+                say("many, nothing", D, dtype, kw)
+                out, lse = run(s, q, dtype, **kw)
+                check(s, q, out, lse, dtype, **kw)
+            assert torch.isneginf(lse[-3:]).all()
+
+
+def test_many_rows_special_values(torch, dg):
+    """What hidden tokens hold, one NaN that the last rows see, a query with a NaN and one with an infinity, and value
+    pairs of very different sizes."""
+    s = planned_for(Setup(torch, dg, 1, 128, 32, [3], [50], 75).fill(), 1 << 19)
+    raw = s.image.reshape(s.n_pages, 1, -1)
+    def pair(pos, side, d, m):
+        page, t = R.Cache(s.image, 1, 128, 32).at(s.table[0], pos)
+        at = R.places(128, 32, t)[side][2]
+        raw[page, 0, at:at + 4] = np.array([d, m], np.float16).view(np.uint8)
+    for pos in range(50, 64):
+        for side in (0, 1):
+            pair(pos, side, np.nan if pos % 2 else np.inf, np.nan)
+    for pos in range(50):
+        d = np.float16(2.0 ** (-20 + 30 * pos / 50))
+        pair(pos, 1, d, np.float16(7.5) * d)
+    s.pages.copy_(torch.from_numpy(s.image))
+    x = s.rng.standard_normal((3, 40, 128)).astype(np.float32)
+    q = s.tensor(40, "fp16", "dense", x)
+    out, lse = run(s, q, "fp16")
+    check(s, q, out, lse, "fp16")
+    for side in (0, 1):
+        kept = s.image.copy()
+        pair(49, side, np.nan, np.nan)
+        s.pages.copy_(torch.from_numpy(s.image))
+        bad, bad_lse = run(s, q, "fp16")
+        assert torch.equal(bad[:2], out[:2]) and torch.equal(bad_lse[:2], lse[:2])
+        assert torch.isnan(bad[2]).all()
+        s.image[:] = kept
+    s.pages.copy_(torch.from_numpy(s.image))
+    x[0, 7, 5], x[1, 31, 6] = np.nan, np.inf
+    bad, bad_lse = run(s, s.tensor(40, "fp16", "dense", x), "fp16")
+    spoiled = torch.zeros((3, 40), dtype=torch.bool, device="cuda")
+    spoiled[0, 7] = spoiled[1, 31] = True
+    assert torch.isnan(bad[spoiled]).all() and torch.isnan(bad_lse[spoiled]).all()
+    assert torch.equal(bad[~spoiled], out[~spoiled]) and torch.equal(bad_lse[~spoiled], lse[~spoiled])
+
+
+@pytest.mark.parametrize("D,dtype", [(64, "fp16"), (128, "bf16")])
+def test_many_rows_in_a_window(torch, dg, D, dtype):
+    """Rows enough that a window's tokens make the work: 1100 new tokens of 64 heads on 2, on a sequence of 1731."""
+    kv, heads, window = 2, 64, 900
+    s = Setup(torch, dg, kv, D, 32, [1100], [1731], 91 + D).fill()
+    q = s.tensor(heads, dtype)
+    out, lse = run(s, q, dtype, window=window)
+    ref, rl, by = R.attend_one(R.Cache(s.pages.cpu().numpy(), kv, D, 32), s.table[0], 1731, host(q).astype(np.float64),
+                               D ** -0.5, window)
+    tol, tl = R.bounds(ref, rl, by, D, dtype == "bf16", True)
+    assert np.all(np.abs(host(out) - ref) <= tol) and np.all(np.abs(host(lse) - rl) <= tl)
+
+
 def test_batches_of_many_sequences(torch, dg):
     # more sequences than the 64 a lookup takes at a time, some without new tokens
     rng = np.random.default_rng(81)
