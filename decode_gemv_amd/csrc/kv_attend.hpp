@@ -7,6 +7,8 @@
 
 #include <limits.h>
 
+#include <type_traits>
+
 #include "kv.h"
 
 namespace {
@@ -142,6 +144,24 @@ __device__ __forceinline__ int tile_at(int tiles, int z)
     return z < first ? 2 * (first - 1 - z) : 2 * (tiles - first - 1 - (z - first)) + 1;
 }
 
+// Sum of x over the lanes up to this one: along rows of 16 lanes, then what
+// the rows before have in their last lane.
+template <class T>
+__device__ __forceinline__ T prefix(T x)
+{
+    auto add = [&](auto ctrl, auto rows) {
+        x += __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), ctrl.value, rows.value, 0xF, true));
+    };
+    using std::integral_constant;
+    add(integral_constant<int, 0x111>{}, integral_constant<int, 0xF>{});      // one lane on (0 comes in),
+    add(integral_constant<int, 0x112>{}, integral_constant<int, 0xF>{});      // two,
+    add(integral_constant<int, 0x114>{}, integral_constant<int, 0xF>{});      // four,
+    add(integral_constant<int, 0x118>{}, integral_constant<int, 0xF>{});      // eight
+    add(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});      // lane 15 of rows 0 and 2 to the next row
+    add(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});      // lane 31 to rows 2 and 3
+    return x;
+}
+
 // What a workgroup has to do: chunk `split` of a row tile, of `chunk` tokens,
 // whose results are number n of the kv head's.
 struct Piece {
@@ -175,8 +195,7 @@ __device__ __forceinline__ RowTile piece_of(const KvAttend &a, int y, Piece &o)
         look(s);
         all += (float)tiles * (float)span;
     }
-#pragma unroll
-    for (int i = 1; i < 64; i *= 2) all += __shfl_xor(all, i);
+    all = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, prefix(all)), 63));
     const float part = fminf(all / (float)a.target, 0x1p30f);
     o.chunk = max((__builtin_amdgcn_readfirstlane((int)ceilf(part)) + CHUNK - 1) / CHUNK * CHUNK, LEAST);
     KvSeq q = {-1, 0, 0, 0};
@@ -184,12 +203,7 @@ __device__ __forceinline__ RowTile piece_of(const KvAttend &a, int y, Piece &o)
     for (int s = 0; s < g.n_seqs; s += 64) {
         if (g.n_seqs > 64) look(s);
         const int chunks = max((int)(((unsigned)span + o.chunk - 1) / (unsigned)o.chunk), 1);
-        int sum = tiles * chunks;
-#pragma unroll
-        for (int i = 1; i < 64; i *= 2) {
-            const int x = __shfl_up(sum, i);
-            sum += lane >= i ? x : 0;
-        }
+        const int sum = prefix(tiles * chunks);
         const int c = __popcll(__ballot(before + sum <= y));
         if (c == 64) {
             before += __builtin_amdgcn_readlane(sum, 63);
@@ -364,8 +378,21 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttend a)
     }
     __syncthreads();
     if (slice || r >= t.rows) return;
-    for (int z = 1; z < min(a.slices, used); z++) add(sml[part + z].x, sml[part + z].y, &sy[part + z][d0]);
-    write_row<D, T>(a, t, head, r, d0, y, l, top);
+    const int slices = min(a.slices, used);
+    float most = top;
+    for (int z = 1; z < slices; z++) most = fmaxf(most, sml[part + z].x);
+    const float f = __builtin_amdgcn_exp2f(top - most);
+    l *= f;
+#pragma unroll
+    for (int j = 0; j < 8; j++) y[j] *= f;
+    for (int z = 1; z < slices; z++) {
+        const float2 ml = sml[part + z];
+        const float g = __builtin_amdgcn_exp2f(ml.x - most);
+        l = fmaf(ml.y, g, l);
+#pragma unroll
+        for (int j = 0; j < 8; j++) y[j] = fmaf(sy[part + z][d0 + j], g, y[j]);
+    }
+    write_row<D, T>(a, t, head, r, d0, y, l, most);
 }
 
 template <int D, int ROWS, class T>
