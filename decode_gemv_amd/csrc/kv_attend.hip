@@ -72,7 +72,7 @@ template <> struct Mma<32> {           // 32 x 32 x 16: lane = row/column l % 32
 // 64 dimensions take 33 us for 96 sequences of 16 heads in a window of 1024
 // tokens, five 36: all workgroups are then there at once.
 template <int D, int ROWS, bool FINE>
-constexpr int WAVES = D * ROWS <= 512 && !FINE ? 6 : D * ROWS <= 1024 ? 4 : D * ROWS <= 2048 ? 3 : D * ROWS <= 4096 ? 2 : 1;
+constexpr int WAVES = D * ROWS <= 512 && !FINE ? 6 : D * ROWS <= 1024 ? 4 : D * ROWS <= 2048 ? 3 : 2;
 
 // What a lane holds of 32 tokens: key words and value words, and the pairs of
 // the tokens whose scores it will have (groups of four).
