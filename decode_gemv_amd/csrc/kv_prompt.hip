@@ -19,11 +19,14 @@
 // what they were measured to take (4 to 4.6 a multiply-add, a conversion or an
 // operation on packed halves, 2.6 a multiplication or addition, 8.5 an
 // exponential: 16 elements a lane with 9 of them, and 43 operations of
-// unpacking), and a SIMD does one such part in 1430: the two kinds hardly
-// overlap.  A wavefront alone on its SIMD issues one instruction in 5.4 cycles
-// and takes as long for a part as two side by side, so the calls that leave
-// the longest rows' workgroups alone at the end (prompts of up to 2048 tokens,
-// where all are there from the start) are bound by those.
+// unpacking), and a SIMD does one such part in 1430: with two wavefronts the
+// two kinds hardly overlap, and the times of the parts add up (of 1208 us,
+// 4096 tokens on 16384, unpacking takes 320, the values' products 250, the
+// keys' 200, the factors' reads 200, the exponentials 130).  A wavefront alone
+// on its SIMD issues one instruction in 5.4 cycles and takes as long for a
+// part as two side by side, so the calls that leave the longest rows'
+// workgroups alone at the end (prompts of up to 2048 tokens, where all are
+// there from the start) are bound by those.
 //
 // Measured, heads of 128 in bf16, 32 of them on 8: 16384 tokens on themselves
 // 849 TFLOP/s (tiles of 32 rows of kv_attend.hip: 633), 2048 on 16384 778
