@@ -79,21 +79,25 @@ struct KvSeq {
 
 // The sequence that x belongs to, for a bound(start[s + 1], s) that does not
 // decrease with s: the first sequence whose bound is above x.  The
-// wavefront's 64 lanes look at 64 sequences at a time, and what there is to
-// know of the one found is then in a lane already (one load latency where a
-// binary search, and the loads after it, have one for each step).
+// wavefront's 64 lanes look at the ends of 64 parts of what is left, so 64
+// sequences take one step and 4096 two, and what there is to know of the one
+// found is then in a lane already (one load latency a step, where a binary
+// search has one for each halving, and the loads after it).
 template <class F>
 __device__ __forceinline__ KvSeq kv_find(const KvGeom &g, int x, F bound)
 {
     const int lane = threadIdx.x & 63;
     KvSeq r = {-1, 0, 0, 0};
-    for (int s = 0; s < g.n_seqs; s += 64) {
-        const int mine = min(s + lane, g.n_seqs - 1);
+    for (int lo = 0, n = g.n_seqs; n > 0;) {
+        const int part = (n + 63) / 64;
+        const int mine = lo + min(lane * part + part, n) - 1;
         const int a = g.start[mine], b = g.start[mine + 1], len = g.lens[mine];
-        const int c = __popcll(__ballot(s + lane < g.n_seqs && bound(b, mine) <= x));
-        if (c == 64) continue;
-        if (s + c >= g.n_seqs) break;
-        r.seq = s + c;
+        const int c = __popcll(__ballot(lane * part < n && bound(b, mine) <= x));
+        if (c * part >= n) break;
+        lo += c * part;
+        n = min(part, n - c * part);
+        if (part > 1) continue;
+        r.seq = lo;
         r.row0 = min(max(__builtin_amdgcn_readlane(a, c), 0), g.n_tokens);
         r.n_new = min(max(__builtin_amdgcn_readlane(b, c), r.row0), g.n_tokens) - r.row0;
         r.len = max(__builtin_amdgcn_readlane(len, c), 0);

@@ -513,6 +513,35 @@ def test_batches_of_many_sequences(torch, dg):
         assert torch.equal(got.cpu(), torch.from_numpy(want).bfloat16())
 
 
+def test_tens_of_thousands_of_sequences(torch, dg):
+    """40000 sequences that share pages, some without new tokens: three steps of looking for one, and more row tiles
+    than one dimension of a grid; a sample of the rows is compared."""
+    rng = np.random.default_rng(85)
+    n, pages = 40000, 29
+    lens, new = 1 + np.arange(n) % 31, np.where(np.arange(n) % 5 == 3, 0, 1)
+    s = Setup(torch, dg, 1, 64, 32, list(new), list(lens), 86, table=(np.arange(n) % pages)[:, None], n_pages=pages).fill()
+    q = s.tensor(2, "bf16")
+    out, lse = run(s, q, "bf16")
+    some = np.sort(rng.choice(np.flatnonzero(new), 400, replace=False))
+    rows = s.start[some]
+    ref, rl, by = R.attend(R.Cache(s.pages.cpu().numpy(), 1, 64, 32), s.table[some], np.arange(401), s.lens[some],
+                           host(q).astype(np.float64)[rows], 64 ** -0.5)
+    tol, tl = R.bounds(ref, rl, by, 64, True)
+    assert np.all(np.abs(host(out)[rows] - ref) <= tol) and np.all(np.abs(host(lse)[rows] - rl) <= tl)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    # new keys of 5000 sequences that share pages, each in a place of its own
+    few = Setup(torch, dg, 1, 64, 32, [1] * 5000, [1 + i % 32 for i in range(5000)], 87,
+                table=(np.arange(5000) // 32)[:, None], n_pages=5000 // 32 + 1)
+    k, v = few.tensor(1, "bf16"), few.tensor(1, "bf16")
+    dg.lw_kv_append(few.cache, few.batch, k, v)
+    ok, ov = torch.empty_like(k), torch.empty_like(v)
+    dg.lw_kv_read(few.cache, few.batch, ok, ov)
+    for x, got in ((k, ok), (v, ov)):
+        c, d, m = R.quantise(host(x))
+        want = (d.astype(np.float64)[..., None] * c - m.astype(np.float64)[..., None]).astype(np.float32)
+        assert torch.equal(got.cpu(), torch.from_numpy(want).bfloat16())
+
+
 def test_lens_past_the_bound_given(torch, dg):
     # max_len is a hint: a longer sequence is served in full
     s = Setup(torch, dg, 1, 128, 32, [1, 1], [900, 40], 83).fill()
