@@ -165,6 +165,24 @@ def test_append_special_vectors(torch, dg):
     assert np.isnan(host(ok)[1, 0]).all() and np.isfinite(host(ok)[1, 1]).all()
 
 
+def test_append_every_scale(torch, dg):
+    """Vectors whose d is each finite fp16 there is, and values between and on the codes."""
+    d = np.arange(1, 0x7C00, dtype=np.uint16).view(np.float16).astype(np.float32)
+    rng = np.random.default_rng(12)
+    x = rng.uniform(0, 15, (len(d), 1, 64)).astype(np.float32) * d[:, None, None]
+    x[:, 0, 0], x[:, 0, 1], x[:, 0, 2] = 0, 15 * d, 7.5 * d
+    x -= (rng.integers(0, 16, len(d)) * d).astype(np.float32)[:, None, None]
+    s = Setup(torch, dg, 1, 64, 256, [len(d)], [len(d)], 58)
+    k = s.tensor(1, "fp32", "dense", x)
+    dg.lw_kv_append(s.cache, s.batch, k, k)
+    ok, ov = torch.empty_like(k), torch.empty_like(k)
+    dg.lw_kv_read(s.cache, s.batch, ok, ov)
+    q, sd, m = R.quantise(x)
+    assert len(np.unique(sd.view(np.uint16))) > 30000
+    want = (sd.astype(np.float64)[..., None] * q - m.astype(np.float64)[..., None]).astype(np.float32)
+    assert np.array_equal(host(ok), want) and np.array_equal(host(ov), want)
+
+
 def test_absent_tokens_and_rows_of_no_sequence(torch, dg):
     """Pages of -1 or past the pool, positions before 0 and past the table: not written, read as zeros; rows before
     start[0] and from start[n] on keep what they held; pages that no table names keep theirs."""
