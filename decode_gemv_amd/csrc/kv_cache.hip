@@ -18,7 +18,7 @@
 // cache in one piece at D = 128, come from one compute unit.  Both kernels
 // are bound by memory, nothing is read twice: 22 thousand tokens of 8 heads of
 // 128 in fp16 are appended in 24 us (4.8 TB/s) and read back in 20 (5.7), 72
-// thousand read in 59 (6.3).  The quantising is not far behind: 12 vector
+// thousand read in 59 (6.3).  The quantising is not far behind: 13 vector
 // instructions an element (extremes that carry a NaN along, in pairs for fp16)
 // where 19 took 27.5 us.
 #include <algorithm>
