@@ -45,7 +45,10 @@
 
 namespace {
 
-constexpr int NW = 4;                  // wavefronts of a workgroup
+// Wavefronts of a workgroup.  16 sequences of 501 to 8190 tokens (replays of a
+// graph, with the join) take 26.5 us with 4, 28.8 with 2 and 31.0 with 8, one of
+// 131071 42.9, 47.8 and 45.2, 96 in a window of 1024 33.3, 37.3 and 39.2.
+constexpr int NW = 4;
 
 // A row tile has 8, 16 or 32 rows.  16 and 32 are the columns of a matrix
 // instruction; 8 rows take both halves of the 16, with the same queries, and
