@@ -34,10 +34,8 @@
 //
 // Rounding: q is scaled by a power of two per row and held in fp16 (exact for
 // fp16 and bf16 inputs but for elements 2^29 below the row's largest); p dv
-// is scaled to lie high in fp16's range and rounded to fp16, which is less
-// than a bf16 output's own rounding by a factor of eight; for fp16 outputs,
-// whose rounding it would match, what the rounding left makes a second fp16
-// operand (2^-21 in all).  Scores, maxima, sums and outputs are fp32.
+// is scaled to lie high in fp16's range and held in two fp16 operands, rounded
+// and what that left (2^-21 in all).  Scores, maxima, sums and outputs are fp32.
 #include <algorithm>
 #include <type_traits>
 
@@ -72,10 +70,10 @@ template <> struct Mma<32> {           // 32 x 32 x 16: lane = row/column l % 32
 };
 
 // Wavefronts a SIMD is to hold (the registers that leaves).  Six of 8 rows of
-// 64 dimensions take 33 us for 96 sequences of 16 heads in a window of 1024
-// tokens, five 36: all workgroups are then there at once.
-template <int D, int ROWS, bool FINE>
-constexpr int WAVES = D * ROWS <= 512 && !FINE ? 6 : D * ROWS <= 1024 ? 4 : D * ROWS <= 2048 ? 3 : 2;
+// 64 dimensions take 34.4 us for 96 sequences of 16 heads in a window of 1024
+// tokens (bf16, replays of a graph), five 37.4.
+template <int D, int ROWS>
+constexpr int WAVES = D * ROWS <= 512 ? 6 : D * ROWS <= 1024 ? 4 : D * ROWS <= 2048 ? 3 : 2;
 
 // What a lane holds of 32 tokens: key words and value words, and the pairs of
 // the tokens whose scores it will have (groups of four).
@@ -288,11 +286,11 @@ __device__ __forceinline__ void fit(State<D, ROWS> &st, const Scores<D, ROWS> &s
         for (int j = 0; j < Mma<ROWS>::ACC; j++) st.o[i][j] *= f;
 }
 
-// From scores to probabilities p dv, as matrix operand; the sums of p.
-// FINE: what the rounding to fp16 leaves, as a second operand.
-template <int D, int ROWS, bool FINE>
+// From scores to probabilities p dv, as matrix operand, what the rounding to
+// fp16 leaves of them as a second operand, and the sums of p.
+template <int D, int ROWS>
 __device__ __forceinline__ void probabilities(Probs<D, ROWS> &hi, Probs<D, ROWS> &lo, State<D, ROWS> &st,
-                                              const Scores<D, ROWS> &s, const Values<D, ROWS> &v)
+                                              const Scores<D, ROWS> &s, const Values<D, ROWS> &v, Masks mk)
 {
     using H = Shape<D, ROWS>;
 #pragma unroll
@@ -307,37 +305,39 @@ __device__ __forceinline__ void probabilities(Probs<D, ROWS> &hi, Probs<D, ROWS>
             e[b] = fmaf(p, half_lo(dv[b]), 0.0f);            // (takes dv as it is)
         }
 #pragma unroll
-        for (int c = 0; c < 2; c++) {
-            hi[i][c] = h2{(_Float16)e[2 * c], (_Float16)e[2 * c + 1]};
-            if (FINE) lo[i][c] = h2{(_Float16)(e[2 * c] - (float)hi[i][c][0]), (_Float16)(e[2 * c + 1] - (float)hi[i][c][1])};
-        }
+        for (int c = 0; c < 2; c++) split2(e[2 * c], e[2 * c + 1], mk, hi[i][c], lo[i][c]);
     }
 }
 
 // O^T += V^T P^T, eight tokens of a lane a time: the codes of two tokens meet
 // in one word, from which pairs of codes are taken as operands.
-template <int D, int ROWS, bool FINE>
+template <int D, int ROWS>
 __device__ __forceinline__ void gather(State<D, ROWS> &st, const Probs<D, ROWS> &hi,
                                        const Probs<D, ROWS> &lo, const Values<D, ROWS> &v, Masks mk, int lane)
 {
     using M = Mma<ROWS>;
     using H = Shape<D, ROWS>;
     const int m = lane % H::WIDE, part = m / H::DW;
-    const uint32_t keep[2] = {m < ROWS ? ~0u : 0u, m < ROWS ? 0u : ~0u};      // COPIES 2: the half of the tokens that is the column's
+    const uint32_t keep = m < ROWS ? ~0u : 0u;               // COPIES 2: whether the first half of the tokens is the column's
+    auto other = [&](uint32_t x) {                           // x & ~keep
+        uint32_t y;
+        asm("v_bfi_b32 %0, %1, 0, %2" : "=v"(y) : "v"(keep), "v"(x));
+        return y;
+    };
 #pragma unroll
     for (int i = 0; i < H::VG; i += 2) {
         auto operand = [&](const Probs<D, ROWS> &x) {
             uint4 w;
             if constexpr (H::COPIES == 2) {
                 const uint32_t a = __builtin_bit_cast(uint32_t, x[0][0]), b = __builtin_bit_cast(uint32_t, x[0][1]);
-                w = make_uint4(a & keep[0], b & keep[0], a & keep[1], b & keep[1]);
+                w = make_uint4(a & keep, b & keep, other(a), other(b));
             } else {
                 w = make_uint4(__builtin_bit_cast(uint32_t, x[i][0]), __builtin_bit_cast(uint32_t, x[i][1]),
                                __builtin_bit_cast(uint32_t, x[i + 1][0]), __builtin_bit_cast(uint32_t, x[i + 1][1]));
             }
             return __builtin_bit_cast(h8, w);
         };
-        const h8 p = operand(hi), rest = FINE ? operand(lo) : p;
+        const h8 p = operand(hi), rest = operand(lo);
 #pragma unroll
         for (int r = 0; r < H::REPS; r++) {
             uint32_t w[2][4];                                // [halves of a word][pairs of tokens]
@@ -365,7 +365,7 @@ __device__ __forceinline__ void gather(State<D, ROWS> &st, const Probs<D, ROWS> 
                     x[2 * c + 1] = z[1];
                 }
                 st.o[r * H::NT + n] = M::go(x, p, st.o[r * H::NT + n]);
-                if (FINE) st.o[r * H::NT + n] = M::go(x, rest, st.o[r * H::NT + n]);
+                st.o[r * H::NT + n] = M::go(x, rest, st.o[r * H::NT + n]);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -373,12 +373,11 @@ __device__ __forceinline__ void gather(State<D, ROWS> &st, const Probs<D, ROWS> 
 }
 
 template <int D, int ROWS, class T>
-__global__ __launch_bounds__(NW * 64, (WAVES<D, ROWS, std::is_same<T, _Float16>::value>)) void k_kv_attend(KvAttend a)
+__global__ __launch_bounds__(NW * 64, (WAVES<D, ROWS>)) void k_kv_attend(KvAttend a)
 {
     using M = Mma<ROWS>;
     using S = State<D, ROWS>;
     using H = Shape<D, ROWS>;
-    constexpr bool FINE = std::is_same<T, _Float16>::value;
     __shared__ __align__(16) float so[NW * H::WIDE * H::ROWF];
     __shared__ float sl[NW * H::WIDE], sm[NW * H::WIDE];     // by wavefront and column
     h8 *sq = reinterpret_cast<h8 *>(so);                     // the loop's; so is the end's
@@ -467,14 +466,14 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, ROWS, std::is_same<T, _Float16>:
             else if (t0 < all_lo || t0 + STEP > all_hi || t.rows < ROWS)
                 hide<D, ROWS>(s, v, t0, seen, lane);
             fit<D, ROWS>(st, s, v);
-            probabilities<D, ROWS, FINE>(hi, lo, st, s, v);
+            probabilities<D, ROWS>(hi, lo, st, s, v, mk);
             // the values are unpacked here, not above the branch in fit()
 #pragma unroll
             for (int n = 0; n < H::VG; n++)
 #pragma unroll
                 for (int r = 0; r < H::REPS; r++)
                     asm volatile("" : "+v"(v.w[n][r].x), "+v"(v.w[n][r].y), "+v"(v.w[n][r].z), "+v"(v.w[n][r].w));
-            gather<D, ROWS, FINE>(st, hi, lo, v, mk, lane);
+            gather<D, ROWS>(st, hi, lo, v, mk, lane);
             load_values<D, ROWS>(v, block, P, tn, lane);
             asm volatile("" ::: "memory");                   // (or they are moved to the next step's start)
             t0 += HOP;

@@ -31,6 +31,7 @@ __device__ __forceinline__ h2 halves(uint32_t w) { return __builtin_bit_cast(h2,
 // two of them are one instruction, with two literals they are two.
 struct Masks {
     uint32_t low, high, exp;     // codes at bits 0..3 and 4..7 of each half, fp16's exponent of 1024
+    float one;                   // a product with it and a subtraction of an fp16 number are one instruction
 };
 
 __device__ __forceinline__ Masks masks()
@@ -39,6 +40,7 @@ __device__ __forceinline__ Masks masks()
     asm("s_mov_b32 %0, 0x000f000f" : "=s"(k.low));
     asm("s_mov_b32 %0, 0x00f000f0" : "=s"(k.high));
     asm("v_mov_b32 %0, 0x64006400" : "=v"(k.exp));
+    asm("s_mov_b32 %0, 1.0" : "=s"(k.one));
     return k;
 }
 
@@ -50,6 +52,20 @@ __device__ __forceinline__ h2 centred(uint32_t w, Masks k)
 {
     return SHIFTED ? halves((w & k.high) | k.exp) - h2{(_Float16)1152.0f, (_Float16)1152.0f}
                    : halves((w & k.low) | k.exp) - h2{(_Float16)1032.0f, (_Float16)1032.0f};
+}
+
+// x and y as fp16, and what their rounding leaves of them, as fp16 too
+// (2^-21 of them is lost).  The two are held as they are: of a product the
+// compiler may else make the rounded value from the product in 32 bits and the
+// rest from one rounding of the product itself, and where the two round apart,
+// once in some 2^13 times, the rest is off by a last place of the first.
+__device__ __forceinline__ void split2(float x, float y, Masks k, h2 &hi, h2 &rest)
+{
+    asm("" : "+v"(x), "+v"(y));
+    uint32_t w = __builtin_bit_cast(uint32_t, h2{(_Float16)x, (_Float16)y});
+    asm("" : "+v"(w));                                       // (both from one conversion)
+    hi = halves(w);
+    rest = h2{(_Float16)fmaf(x, k.one, -(float)hi[0]), (_Float16)fmaf(y, k.one, -(float)hi[1])};
 }
 
 // Eight codes of a word in the order 0 4 1 5 2 6 3 7, those of odd dimensions

@@ -32,10 +32,11 @@
 // 849 TFLOP/s (tiles of 32 rows of kv_attend.hip: 633), 2048 on 16384 778
 // (638), 2048 on themselves 389 (354).
 //
-// Rounding: as in kv_attend.hip, but p dv is rounded to fp16 once for fp16
-// outputs too.  Its error, at random 2^-12 of a part of the output, comes to
-// about that of rounding the output; the second operand that would remove it
-// costs a quarter of the rate (623 TFLOP/s and not 790, 4096 on 16384).
+// Rounding: as in kv_attend.hip.  The second operand of p dv, what its rounding
+// to fp16 leaves, costs 18 % (chunks of 511 to 1024 new tokens on 9000 to 16384,
+// 64 heads on 8 of 128 in fp16: 1734 us and not 1448); without it fp16 results
+// lie 3.0e-4 of their size from 64 bits, with it 2.1e-4, which is their own
+// rounding.
 #include <stddef.h>
 
 #include <algorithm>
@@ -147,10 +148,16 @@ struct Rows {
     float l, z;
 };
 
+__device__ __forceinline__ f16v product(uint4 v, const h2 (&p)[4], f16v o)
+{
+    const h8 x = {p[0][0], p[0][1], p[1][0], p[1][1], p[2][0], p[2][1], p[3][0], p[3][1]};
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, v), x, o, 0, 0, 0);
+}
+
 // 32 tokens of a tile, the first being t0.  masked: some of them may be hidden
 // from some rows; a hidden token's score is -infinity.
 template <int D>
-__device__ __forceinline__ void step(Rows<D> &st, const Tile<D> &tile, int sub, int t0, bool masked, Span seen, int lane)
+__device__ __forceinline__ void step(Rows<D> &st, const Tile<D> &tile, int sub, int t0, bool masked, Span seen, Masks mk, int lane)
 {
     using L = Tile<D>;
     constexpr int PIECES = 32 / L::TPW;
@@ -235,18 +242,17 @@ __device__ __forceinline__ void step(Rows<D> &st, const Tile<D> &tile, int sub, 
     }
 #pragma unroll
     for (int kk = 0; kk < 2; kk++) {
-        h8 e;
+        h2 e[4], rest[4];                                    // p dv, and what its rounding leaves
 #pragma unroll
         for (int c = 0; c < 4; c++) {
             const int a = 2 * kk + c / 2;
             const float4 x = vf[4 * a + c % 2];              // (dv, 8 dv - mv) of two tokens
-#pragma unroll
-            for (int b = 0; b < 2; b++) {
-                const float p = __builtin_amdgcn_exp2f(fmaf(s[a][c % 2 * 2 + b], st.qs, -st.mo));
-                st.l += p;
-                st.z = fmaf(p, b ? x.w : x.y, st.z);
-                e[2 * c + b] = (_Float16)(p * (b ? x.z : x.x));
-            }
+            const float p = __builtin_amdgcn_exp2f(fmaf(s[a][c % 2 * 2], st.qs, -st.mo));
+            const float r = __builtin_amdgcn_exp2f(fmaf(s[a][c % 2 * 2 + 1], st.qs, -st.mo));
+            st.l += p;
+            st.l += r;
+            st.z = fmaf(r, x.w, fmaf(p, x.y, st.z));
+            split2(p * x.x, r * x.z, mk, e[c], rest[c]);
         }
         if (EARLYV && kk == 0) {
 #pragma unroll
@@ -255,9 +261,11 @@ __device__ __forceinline__ void step(Rows<D> &st, const Tile<D> &tile, int sub, 
         }
 #pragma unroll
         for (int n = 0; n < L::NT; n++) {
-            const h8 v = __builtin_bit_cast(h8, EARLYV ? vw[kk][n] : values(kk, n));
-            st.o[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, e, st.o[n], 0, 0, 0);
+            if (!EARLYV) vw[kk][n] = values(kk, n);
+            st.o[n] = product(vw[kk][n], e, st.o[n]);
         }
+#pragma unroll
+        for (int n = 0; n < L::NT; n++) st.o[n] = product(vw[kk][n], rest, st.o[n]);
     }
 }
 
@@ -325,7 +333,8 @@ __global__ __launch_bounds__(WV * 64, (D > 64 ? 2 : 3)) void k_kv_prompt(KvAtten
     };
 
     Rows<D> st;
-    const Masks mk = masks();
+    Masks mk = masks();
+    asm("v_mov_b32 %0, 1.0" : "=v"(mk.one));                 // (scalar registers are short here)
     const Put<D> put(threadIdx.x);
     const bool any = mine.lo < mine.hi;
     uint32_t now = 0, next = 0;                              // the parts with a page of the tile in use, and of the one loaded;
@@ -372,7 +381,7 @@ __global__ __launch_bounds__(WV * 64, (D > 64 ? 2 : 3)) void k_kv_prompt(KvAtten
                 const int ts = t0 + sub * 32;
                 if (rows <= 0 || ts >= last.hi || ts + 32 <= first.lo || ts >= mine.hi) continue;
                 if (!(now >> sub & 1u)) continue;                      // (32 absent tokens)
-                step<D>(st, tile, sub, ts, rows < WIDE || ts < last.lo || ts + 32 > first.hi, seen, lane);
+                step<D>(st, tile, sub, ts, rows < WIDE || ts < last.lo || ts + 32 > first.hi, seen, mk, lane);
             }
             now = next;
             next = behind;

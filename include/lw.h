@@ -492,8 +492,9 @@ lw_status lw_kv_read(const lw_kv_cache *cache, const lw_kv_batch *batch, int64_t
  *             smaller one lowers the number of chunks that a sequence is cut
  *             into, and LW_E_ARG is given only for a misaligned one
  * Scores, sums and the output's accumulation are fp32; p times a value's d
- * is rounded to fp16 (for fp16 results of calls that are not large, with what
- * that leaves as a second term); sums run in a fixed order: results are
+ * is held to 2^-21 of itself, and to 2^-30 of p's largest times the largest d
+ * that the row sees (a row whose weight lies on values 2^20 below its largest
+ * ones loses bits of them); sums run in a fixed order: results are
  * deterministic (a batch is cut into chunks of one size, so what else is in it
  * may move a sequence's last bits).  At most 2^30 query rows per kv head, and
  * large calls 65535 tiles of 128 rows.
