@@ -296,7 +296,9 @@ struct Query {
         // the largest element goes to [2^14, 2^15); an infinity stays one and
         // makes the row NaN, as its scores are
         const int e = top > 0.0f ? (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127 : 0;
-        qs = scale * 1.44269504088896341f * ldexpf(1.0f, e - 14);
+        // (at least a normal number: a hidden token's score is -infinity times
+        // this; scores that small are zero either way)
+        qs = fmaxf(scale * 1.44269504088896341f * ldexpf(1.0f, e - 14), 0x1p-126f);
         qsum = ldexpf(sum, 14 - e);
 #pragma unroll
         for (int j = 0; j < PER; j++) {
