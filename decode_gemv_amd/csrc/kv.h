@@ -8,6 +8,10 @@
 
 #include "lw.h"
 
+// Tokens of a sequence that are looked at, at most: positions and what lies a
+// few steps past them fit 32 bits, chunks and pages divide it.
+constexpr int32_t KV_MOST_TOKENS = 0x7FFF0000;
+
 // A cache and a batch as the kernels see them: passed by value, so every
 // field is uniform.
 struct KvGeom {

@@ -559,7 +559,7 @@ KvPlan lw_kv_plan(int head_dim, int kv_heads, int group, int64_t n_seqs, int64_t
     KvPlan p = {};
     const int64_t rows = n_tokens * group;
     // tokens a row tile may see
-    int64_t span = max_len;
+    int64_t span = std::min<int64_t>(max_len, KV_MOST_TOKENS);
     if (window) span = std::min<int64_t>(span, (int64_t)window + 128 + STEP);
     // Query rows of a tile.  Up to 8, 16 or 32 a sequence on average: all of
     // them (8 sequences of 20 rows on 4000 tokens, heads of 128: 28.8 us with

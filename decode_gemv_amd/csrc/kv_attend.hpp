@@ -109,7 +109,7 @@ __device__ __forceinline__ Span span_of(const KvAttend &a, const RowTile &t, int
 // Tokens that the table can name.
 __device__ __forceinline__ int cap_of(const KvGeom &g)
 {
-    return (int)min(g.stride << g.page_shift, (int64_t)0x7FFF0000);
+    return (int)min(g.stride << g.page_shift, (int64_t)KV_MOST_TOKENS);
 }
 
 // Row tile `local` of a sequence.

@@ -92,3 +92,15 @@ def test_scores_far_below_one(torch, dg, D, group, planned):
         out, lse = run(s, q, dtype, scale=scale)
         _, fine = compare(s, q, out, lse, dtype, scale=scale)
         assert fine.all()
+
+
+@pytest.mark.parametrize("work", [True, 0])
+@pytest.mark.parametrize("group", [8, 128])
+def test_a_table_of_2_to_26_pages(torch, dg, group, work):
+    s = Setup(torch, dg, 1, 64, 256, [1], [300], 35).fill()
+    wide = torch.full((1, 1 << 26), -1, dtype=torch.int32, device="cuda")
+    wide[:, :2] = torch.from_numpy(s.table).cuda()
+    s.batch = dg.KvBatch(s.batch.start, s.batch.lens, wide)
+    q = s.tensor(group, "bf16")
+    out, lse = run(s, q, "bf16", work=work)
+    compare(s, q, out, lse, "bf16")

@@ -1,0 +1,37 @@
+"""How lw_kv_attend cuts a call up (lw_kv_plan), on the host: the library's own function, called by its C++ name."""
+import ctypes as C
+
+import pytest
+
+import decode_gemv_amd as dg
+
+ANY = (1 << 64) - 1                                           # bytes of work without a limit
+TOKENS = 0x7FFF0000                                           # of a sequence, at most, for the kernels
+
+
+class Plan(C.Structure):
+    _fields_ = [("tile", C.c_int), ("tiles", C.c_int64), ("target", C.c_int), ("splits", C.c_int), ("chunk", C.c_int),
+                ("pieces", C.c_int64), ("first_at", C.c_size_t), ("work_bytes", C.c_size_t)]
+
+
+def plan(D, kv, group, seqs, tokens, longest, window=0, room=ANY):
+    f = dg.lib()._Z10lw_kv_planiiilllim                      # (int, int, int, long, long, long, int, unsigned long)
+    f.restype, f.argtypes = Plan, [C.c_int] * 3 + [C.c_int64] * 3 + [C.c_int, C.c_size_t]
+    return f(D, kv, group, seqs, tokens, longest, window, room)
+
+
+def result(p, D, kv):
+    return kv * p.tile * (D + 2) * 4
+
+
+@pytest.mark.parametrize("shift", range(23, 27))
+@pytest.mark.parametrize("kv,seqs,rows", [(1, 1, 128), (8, 1, 4096), (64, 1, 128), (1, 64, 8192), (8, 600, 76800)])
+@pytest.mark.parametrize("room", [0, ANY], ids=["no_room", "room"])
+def test_tables_of_more_tokens_than_the_kernels_count(shift, kv, seqs, rows, room):
+    """2^23 to 2^26 pages of 256 tokens a sequence: sizes of chunks and their number stay what they are taken for."""
+    p = plan(128, kv, 1, seqs, rows, (1 << shift) * 256, 0, room)
+    assert p.tile == 128
+    assert 1 <= p.splits <= 512 and (p.splits == 1 or room)
+    assert p.chunk > 0 and p.chunk % 128 == 0
+    assert (p.splits - 1) * p.chunk < TOKENS <= p.splits * p.chunk
+    assert p.work_bytes == (p.tiles * p.splits * result(p, 128, kv) if p.splits > 1 else 0)
