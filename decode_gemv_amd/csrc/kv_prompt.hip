@@ -60,7 +60,8 @@ struct Tile {
     uint4 k[SUBS][PER][64];                                  // operands of K Q^T
     uint2 v[SUBS][2][NT][64][2];                             // operands of V^T P^T
     float2 kf[TT], vf[TT];                                   // dk, 8 dk - mk; dv, 8 dv - mv
-    float dmax[WV];                                          // largest dv of the tokens that a wavefront unpacked
+    float dmax[WV];                                          // largest dv of the tokens that a wavefront unpacked,
+    uint32_t odd[WV];                                        // infinity where the pairs of some (these bits) are not finite
 };
 
 // What a wavefront has loaded of a tile.
@@ -117,13 +118,13 @@ __device__ __forceinline__ void unpack(Tile<D> &o, const Raw<D> &r, const Put<D>
                 make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
         }
     }
-    // A value's pair that is not finite makes its token's score NaN instead
-    // (so that it reaches the rows that see it, and only zeros the others)
+    // A value's pair that is not finite counts as (0, 0), so that it is nothing
+    // to the rows that do not see it; step() makes the others' outputs NaN
     float d = half_lo(r.dm), c = fmaf(d, 8.0f, -half_hi(r.dm));
     const bool odd = !(fabsf(c) < __builtin_inff());
-    const bool bad = __ballot(odd) >> (lane + L::TPW) & 1;   // (for the lanes of keys)
+    const uint32_t odds = (uint32_t)(__ballot(odd) >> L::TPW) & ((1u << L::TPW) - 1);       // the values'
     if (lane < L::TPW) {
-        o.kf[wave * L::TPW + lane] = make_float2(d, bad ? __builtin_nanf("") : c);
+        o.kf[wave * L::TPW + lane] = make_float2(d, c);
     } else if (lane < 2 * L::TPW) {
         o.vf[wave * L::TPW + lane % L::TPW] = make_float2(odd ? 0.0f : d, odd ? 0.0f : c);
     }
@@ -135,7 +136,10 @@ __device__ __forceinline__ void unpack(Tile<D> &o, const Raw<D> &r, const Put<D>
     most(std::integral_constant<int, 0x4E>{});               // lane ^ 2
     most(std::integral_constant<int, 0x141>{});              // 7 - lane of eight
     most(std::integral_constant<int, 0x140>{});              // 15 - lane of sixteen
-    if (lane == L::TPW) o.dmax[wave] = d;
+    if (lane == L::TPW) {
+        o.dmax[wave] = odds ? __builtin_inff() : d;
+        o.odd[wave] = odds;
+    }
 }
 
 template <int D>
@@ -209,6 +213,11 @@ __device__ __forceinline__ void step(Rows<D> &st, const Tile<D> &tile, int sub, 
                 dtop = fmaxf(dtop, out ? 0.0f : dv[b]);
             }
         }
+        uint32_t bits = 0;                                   // tokens that count as (0, 0), and that the row sees
+#pragma unroll
+        for (int i = 0; i < PIECES; i++) bits |= tile.odd[sub * PIECES + i] << i * L::TPW;
+        bits &= (uint32_t)((1ull << min(max(seen.hi - t0, 0), 32)) - 1) & ~(uint32_t)((1ull << min(max(seen.lo - t0, 0), 32)) - 1);
+        dtop = bits ? __builtin_inff() : dtop;
     }
     uint4 vw[2][L::NT];
     if (EARLYV) {
@@ -234,7 +243,7 @@ __device__ __forceinline__ void step(Rows<D> &st, const Tile<D> &tile, int sub, 
         }
         const float f = __builtin_amdgcn_exp2f(old - st.mo);
         st.l *= f;
-        st.z *= f;
+        st.z = dtop > 65504.0f ? __builtin_nanf("") : st.z * f;
 #pragma unroll
         for (int n = 0; n < L::NT; n++)
 #pragma unroll
@@ -335,6 +344,7 @@ __global__ __launch_bounds__(WV * 64, (D > 64 ? 2 : 3)) void k_kv_prompt(KvAtten
     Rows<D> st;
     Masks mk = masks();
     asm("v_mov_b32 %0, 1.0" : "=v"(mk.one));                 // (scalar registers are short here)
+    asm("v_mov_b32 %0, 0x000f000f" : "=v"(mk.low));
     const Put<D> put(threadIdx.x);
     const bool any = mine.lo < mine.hi;
     uint32_t now = 0, next = 0;                              // the parts with a page of the tile in use, and of the one loaded;

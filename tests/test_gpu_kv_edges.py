@@ -104,3 +104,26 @@ def test_a_table_of_2_to_26_pages(torch, dg, group, work):
     q = s.tensor(group, "bf16")
     out, lse = run(s, q, "bf16", work=work)
     compare(s, q, out, lse, "bf16")
+
+
+@pytest.mark.parametrize("D,group,planned", [(D, g, p) for D in (64, 128, 256) for g, p in ((2, 0), (5, 0), (10, 0), (48, 1 << 19))])
+def test_values_that_are_not_numbers(torch, dg, D, group, planned):
+    """A value pair of NaN, its key as it was: the outputs of the rows that see it are NaN, and no log sum is."""
+    s = Setup(torch, dg, 1, D, 32, [3], [100], 501 + D).fill()
+    if planned:
+        planned_for(s, planned)
+    q = s.tensor(group, "fp16")
+    clean = s.image.copy()
+    ref, rl, by = R.attend(R.Cache(clean, 1, D, 32), s.table, s.start, s.lens, host(q).astype(np.float64), D ** -0.5)
+    tol, tl = tight(ref, rl, by, D, False)
+    for pos, sees in ((99, 2), (98, 1), (97, 0), (70, 0), (5, 0)):            # the first row that sees it
+        say("not numbers", D, group, pos)
+        s.image[:] = clean
+        page, t = R.Cache(clean, 1, D, 32).at(s.table[0], pos)
+        at = R.places(D, 32, t)[1][2]
+        s.image.reshape(s.n_pages, -1)[page, at:at + 4] = np.array([np.nan, np.nan], np.float16).view(np.uint8)
+        s.pages.copy_(torch.from_numpy(s.image))
+        out, lse = run(s, q, "fp16")
+        assert np.isnan(host(out)[sees:]).all()
+        assert np.all(np.abs(host(out)[:sees] - ref[:sees]) <= tol[:sees])
+        assert np.all(np.abs(host(lse) - rl) <= tl)
