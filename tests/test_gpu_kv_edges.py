@@ -4,6 +4,7 @@ import pytest
 
 import kv_ref as R
 from test_gpu_kv import Setup, dg, host, planned_for, run, say, torch  # noqa: F401  (dg and torch are fixtures)
+from test_kv_plan import plan
 
 pytestmark = pytest.mark.gpu
 
@@ -127,3 +128,127 @@ def test_values_that_are_not_numbers(torch, dg, D, group, planned):
         assert np.isnan(host(out)[sees:]).all()
         assert np.all(np.abs(host(out)[:sees] - ref[:sees]) <= tol[:sees])
         assert np.all(np.abs(host(lse) - rl) <= tl)
+
+
+def tile(s, heads, window=0):
+    """Rows of a tile that the call takes."""
+    longest = min(s.batch.desc.max_len or 1 << 62, s.batch.desc.table_stride * s.P)
+    return plan(s.D, s.kv, heads // s.kv, len(s.lens), s.rows, longest, window).tile
+
+
+# ------------------------------------------------------------------ tiles of 32 rows
+
+TALL = [
+    # kv, group, P, new, lens: 17 to 32 rows a sequence on average; tiles in part, in full and several of a sequence; pages
+    # that end inside a step; first tokens; sequences without new tokens
+    (1, 1, 32, [20], [20]), (2, 5, 32, [5, 4], [70, 40]), (1, 17, 64, [1], [257]), (1, 32, 32, [1], [1]),
+    (2, 3, 128, [9, 1, 20], [200, 64, 20]), (1, 4, 32, [8], [33]), (1, 8, 64, [0, 6], [40, 300]), (1, 2, 256, [40, 0, 3], [97, 30, 3]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("case", TALL, ids=lambda c: f"kv{c[0]}x{c[1]}_P{c[2]}_n{'_'.join(map(str, c[3]))}")
+def test_tall_tiles(torch, dg, case, D, dtype):
+    kv, group, P, new, lens = case
+    say("tall", case, D, dtype)
+    s = Setup(torch, dg, kv, D, P, new, lens, 600 + sum(lens)).fill()
+    q = s.tensor(kv * group, dtype, "fused")
+    for kw in (dict(), dict(window=17), dict(causal=False), dict(causal=False, window=40)):
+        assert tile(s, kv * group, kw.get("window", 0)) == 32
+        out, lse = run(s, q, dtype, **kw)
+        compare(s, q, out, lse, dtype, **kw)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows", [33, 64])
+def test_tall_tiles_of_more_rows_and_much_work(torch, dg, rows, D, dtype):
+    s = planned_for(Setup(torch, dg, 1, D, 64, [rows], [150], 610 + D + rows).fill(), 1 << 19)
+    q = s.tensor(1, dtype)
+    assert tile(s, 1) == 32
+    for work in (True, 0):
+        out, lse = run(s, q, dtype, work=work)
+        compare(s, q, out, lse, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_tall_tiles_in_chunks(torch, dg, D, dtype):
+    """Long sequences beside short ones, cut into many chunks, few, or one."""
+    s = Setup(torch, dg, 1, D, 64, [6, 1, 5], [3000, 33, 1027], 620 + D).fill()
+    q = s.tensor(7, dtype)
+    assert tile(s, 7) == 32
+    whole = dg.lw_kv_attend_scratch_bytes(s.cache, s.batch, s.rows, 7)
+    assert whole > 0
+    for nb in (whole, whole // 3, 64, 0):
+        for kw in (dict(), dict(window=1500)):
+            say("tall chunks", D, nb, kw)
+            out, lse = run(s, q, dtype, work=nb, **kw)
+            compare(s, q, out, lse, dtype, **kw)
+            again, lse2 = run(s, q, dtype, work=nb, **kw)
+            assert torch.equal(out, again) and torch.equal(lse, lse2), "not deterministic"
+
+
+@pytest.mark.parametrize("how", ["heads first", "misaligned"])
+def test_tall_tiles_strides(torch, dg, how):
+    s = Setup(torch, dg, 2, 128, 32, [5, 3], [80, 40], 631).fill()
+    q = s.tensor(10, "bf16", how)
+    assert tile(s, 10) == 32
+    out, lse = run(s, q, "bf16", how=how)
+    want, want_lse = run(s, s.tensor(10, "bf16", "dense", host(q)), "bf16")
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    compare(s, q, out, lse, "bf16")
+
+
+def test_tall_tiles_that_see_nothing(torch, dg):
+    """More new tokens than the sequence has, windows over pages given up, and whole sequences without pages."""
+    table = [[0, -1, -1, 1], [2, 2, 2, 2], [-1, 99, -5, -1]]
+    for D in (64, 128):
+        for dtype in ("fp16", "bf16"):
+            s = Setup(torch, dg, 1, D, 32, [2, 5, 3], [90, 2, 128], 641, table=table, n_pages=3).fill()
+            q = s.tensor(8, dtype)
+            assert tile(s, 8) == 32
+            for kw in (dict(), dict(window=20), dict(causal=False)):
+                say("tall, nothing", D, dtype, kw)
+                out, lse = run(s, q, dtype, **kw)
+                compare(s, q, out, lse, dtype, **kw)
+                assert torch.isneginf(lse[-3:]).all()
+            out, lse = run(s, q, dtype, window=20)
+            assert torch.isneginf(lse[:2]).all() and torch.isneginf(lse[2:5]).all()
+
+
+def test_tall_tiles_special_values(torch, dg):
+    """NaN and infinite pairs past the length, before the window and after a row's position, a visible NaN, queries with a
+    NaN and an infinity, and value pairs of very different sizes."""
+    for D in (64, 128):
+        s = Setup(torch, dg, 1, D, 32, [3], [50], 651).fill()
+        def pair(pos, side, d, m):
+            page, t = R.Cache(s.image, 1, D, 32).at(s.table[0], pos)
+            at = R.places(D, 32, t)[side][2]
+            s.image.reshape(s.n_pages, -1)[page, at:at + 4] = np.array([d, m], np.float16).view(np.uint8)
+        for pos in range(50):
+            d = np.float16(2.0 ** (-20 + 30 * pos / 50))
+            pair(pos, 1, d, np.float16(7.5) * d)
+        for pos in list(range(50, 64)) + list(range(20)):
+            for side in (0, 1):
+                pair(pos, side, np.nan if pos % 2 else np.inf, np.nan)
+        s.pages.copy_(torch.from_numpy(s.image))
+        x = s.rng.standard_normal((3, 10, D)).astype(np.float32)
+        q = s.tensor(10, "fp16", "dense", x)
+        assert tile(s, 10, 25) == 32
+        out, lse = run(s, q, "fp16", window=25)
+        compare(s, q, out, lse, "fp16", window=25)
+        clean = s.image.copy()
+        pair(49, 0, np.nan, np.nan)                           # only the last rows see it
+        s.pages.copy_(torch.from_numpy(s.image))
+        bad, bad_lse = run(s, q, "fp16", window=25)
+        assert torch.equal(bad[:2], out[:2]) and torch.equal(bad_lse[:2], lse[:2])
+        assert torch.isnan(bad[2]).all() and torch.isnan(bad_lse[2]).all()
+        s.pages.copy_(torch.from_numpy(clean))
+        x[0, 7, 5], x[1, 3, 6] = np.nan, np.inf
+        bad, bad_lse = run(s, s.tensor(10, "fp16", "dense", x), "fp16", window=25)
+        spoiled = torch.zeros((3, 10), dtype=torch.bool, device="cuda")
+        spoiled[0, 7] = spoiled[1, 3] = True
+        assert torch.isnan(bad[spoiled]).all() and torch.isnan(bad_lse[spoiled]).all()
+        assert torch.equal(bad[~spoiled], out[~spoiled]) and torch.equal(bad_lse[~spoiled], lse[~spoiled])

@@ -35,3 +35,19 @@ def test_tables_of_more_tokens_than_the_kernels_count(shift, kv, seqs, rows, roo
     assert p.chunk > 0 and p.chunk % 128 == 0
     assert (p.splits - 1) * p.chunk < TOKENS <= p.splits * p.chunk
     assert p.work_bytes == (p.tiles * p.splits * result(p, 128, kv) if p.splits > 1 else 0)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_rows_of_a_tile(D):
+    """Which kernel takes how many rows: 8, 16 and 32 a sequence on average, 16 up to the work at which 128 rows are worth it,
+    and 32 from there on for sequences of not more than 64.  Heads of 256 have no tiles of more than 16."""
+    wide = lambda tile: min(tile, 16) if D == 256 else tile
+    work = 1 << 19                                            # tokens at which one tile of 128 rows is work enough
+    for seqs in (1, 3, 150):
+        for rows, tile in ((1, 8), (8, 8), (9, 16), (16, 16), (17, 32), (32, 32), (33, 16), (64, 16), (400, 16)):
+            assert plan(D, 1, 1, seqs, seqs * rows, 500).tile == wide(tile), (seqs, rows)
+    for rows, tile in ((32, 32), (33, 32), (64, 32), (65, 128), (400, 128)):
+        assert plan(D, 1, 1, 1, rows, work).tile == wide(tile), rows
+    for rows in (33, 64, 65, 128):
+        assert plan(D, 1, 1, 1, rows, work - 1).tile == 16
+        assert plan(D, 4, 1, 1, rows, work // 4).tile == plan(D, 1, 1, 1, rows, work).tile
