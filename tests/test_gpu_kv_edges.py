@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 
 import kv_ref as R
-from test_gpu_kv import Setup, dg, host, planned_for, run, say, torch  # noqa: F401  (dg and torch are fixtures)
+from test_gpu_kv import ATTENDS, MANY, Setup, dg, host, planned_for, run, say, torch  # noqa: F401  (dg and torch are fixtures)
 from test_kv_plan import plan
 
 pytestmark = pytest.mark.gpu
@@ -134,6 +134,23 @@ def tile(s, heads, window=0):
     """Rows of a tile that the call takes."""
     longest = min(s.batch.desc.max_len or 1 << 62, s.batch.desc.table_stride * s.P)
     return plan(s.D, s.kv, heads // s.kv, len(s.lens), s.rows, longest, window).tile
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("case,planned", [(c, 0) for c in ATTENDS] + [(c, 1 << 19) for c in MANY])
+def test_p_dv_in_two_parts(torch, dg, case, planned, D, dtype):
+    """The calls of the other tests' tiles of 8, 16 and 128 rows within the bounds of a p dv that is held to 2^-21."""
+    kv, group, P, new, lens = case
+    s = Setup(torch, dg, kv, D, P, new, lens, 700 + sum(lens)).fill()
+    if planned:
+        planned_for(s, planned)
+    q = s.tensor(kv * group, dtype)
+    say("two parts", case, D, dtype, tile(s, kv * group))
+    assert tile(s, kv * group) in ((32, 128) if planned and D < 256 else (8, 16))
+    for kw in (dict(), dict(causal=False)):
+        out, lse = run(s, q, dtype, **kw)
+        compare(s, q, out, lse, dtype, **kw)
 
 
 # ------------------------------------------------------------------ tiles of 32 rows
