@@ -553,6 +553,29 @@ hipError_t launch_dim(const KvAttend &a, int dtype, const KvPlan &p, hipStream_t
 
 }  // namespace
 
+namespace {
+
+// Whether sequences are cut into chunks.  Not up to 1024 tokens; from there on
+// where there are fewer workgroups than the chip has places for: heads of 128,
+// 32 on 8, 8 sequences of 1000 tokens 17.2 us cut and 15.9 not, one of 1500
+// 16.6 and 18.7, 48 of 500 to 8190 63 and 79.  And where one sequence may be
+// far longer than the others, whose workgroups would leave it alone on the
+// chip: 128 sequences of 500 tokens and one of 131071, 57 us and not 786 (256:
+// 76 and 893, 512: 128 and 934).  That has a price, as each workgroup looks at
+// all sequences (n^2 kv looks): 128, 256, 512 and 1024 of 500 tokens and none
+// longer, 27, 44, 100 and 232 us and not 26, 42, 75 and 143.  So it is done
+// where the looks, 12 ps n^2 kv, come to a fifteenth at most of the time that a
+// sequence of `span` tokens would be left alone, 5.8 ns a token.  (Sequences of
+// more than one row tile have workgroups enough.)
+bool cut(int64_t kv_heads, int64_t n_seqs, int64_t rows, int tile, int64_t span)
+{
+    if (span <= 1024) return false;
+    if (std::max(n_seqs, (rows + tile - 1) / tile) * kv_heads < 1024) return true;
+    return rows <= tile * n_seqs && n_seqs * n_seqs * kv_heads <= 32 * span;
+}
+
+}  // namespace
+
 KvPlan lw_kv_plan(int head_dim, int kv_heads, int group, int64_t n_seqs, int64_t n_tokens, int64_t max_len, int window,
                   size_t room)
 {
@@ -595,11 +618,7 @@ KvPlan lw_kv_plan(int head_dim, int kv_heads, int group, int64_t n_seqs, int64_t
         p.work_bytes = p.splits > 1 ? p.tiles * p.splits * result : 0;
         return p;
     }
-    // Cut or not, heads of 128, 32 on 8: 8 sequences of 1000 tokens 17.2 us cut
-    // and 15.9 not, one of 1500 16.6 and 18.7; 48 sequences of 500 to 8190
-    // tokens 63 and 79, 256 of 100 to 4000 139 and 132 (workgroups enough, of
-    // which the chip takes the next as it is done with one).
-    if (span <= 1024 || std::max(n_seqs, (rows + p.tile - 1) / p.tile) * kv_heads >= 1024) return p;
+    if (!cut(kv_heads, n_seqs, rows, p.tile, span)) return p;
     // Into about 768 pieces, three for a CU: 16 sequences of 501 to 8190 tokens
     // take 26.8 us, with 1024 28.1 and with 1536 30.3; one of 131071 43.5,
     // 43.3 and 47; 32 of 16384 116, 119 and 120.

@@ -188,50 +188,71 @@ struct Piece {
 // same for all, for which the batch makes about a.target (at most that and
 // one more per row tile): then workgroups have the same work however
 // different the sequences are, and none has nothing to do.  The wavefront's
-// lanes look at 64 sequences at a time.
-template <int ROWS>
-__device__ __forceinline__ RowTile piece_of(const KvAttend &a, int y, Piece &o)
+// lanes look at 64 sequences at a time, B times at once (what a look takes is
+// its loads' latency: 512 sequences of 500 tokens in chunks take 100 us with
+// four looks at once and 110 with one).
+template <int ROWS, int B>
+__device__ __forceinline__ KvSeq find_piece(const KvAttend &a, int y, Piece &o, int &local)
 {
     const KvGeom &g = a.g;
     const int lane = threadIdx.x & 63, cap = cap_of(g);
-    int row0, n_new, len, tiles, span;
+    int row0[B], n_new[B], len[B], tiles[B], span[B];
     auto look = [&](int s) {
-        const int mine = min(s + lane, g.n_seqs - 1);
-        const int b = g.start[mine], e = g.start[mine + 1];
-        len = max(g.lens[mine], 0);
-        row0 = min(max(b, 0), g.n_tokens);
-        n_new = min(max(e, row0), g.n_tokens) - row0;
-        tiles = s + lane < g.n_seqs ? (n_new * a.group + ROWS - 1) / ROWS : 0;
-        const int pos = len - n_new;                         // the first row's
-        const int lo = a.window && pos >= a.window ? pos - a.window + 1 : 0;
-        span = max(min(len, cap) - (lo & ~(STEP - 1)), 0);
+        int b[B], e[B], l[B];
+#pragma unroll
+        for (int i = 0; i < B; i++) {
+            const int mine = min(s + 64 * i + lane, g.n_seqs - 1);
+            b[i] = g.start[mine];
+            e[i] = g.start[mine + 1];
+            l[i] = g.lens[mine];
+        }
+#pragma unroll
+        for (int i = 0; i < B; i++) {
+            len[i] = max(l[i], 0);
+            row0[i] = min(max(b[i], 0), g.n_tokens);
+            n_new[i] = min(max(e[i], row0[i]), g.n_tokens) - row0[i];
+            tiles[i] = s + 64 * i + lane < g.n_seqs ? (n_new[i] * a.group + ROWS - 1) / ROWS : 0;
+            const int pos = len[i] - n_new[i];               // the first row's
+            const int lo = a.window && pos >= a.window ? pos - a.window + 1 : 0;
+            span[i] = max(min(len[i], cap) - (lo & ~(STEP - 1)), 0);
+        }
     };
     float all = 0.0f;
-    for (int s = 0; s < g.n_seqs; s += 64) {
+    for (int s = 0; s < g.n_seqs; s += 64 * B) {
         look(s);
-        all += (float)tiles * (float)span;
+#pragma unroll
+        for (int i = 0; i < B; i++) all += (float)tiles[i] * (float)span[i];
     }
     all = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, prefix(all)), 63));
     const float part = fminf(all / (float)a.target, 0x1p30f);
     o.chunk = max((__builtin_amdgcn_readfirstlane((int)ceilf(part)) + CHUNK - 1) / CHUNK * CHUNK, LEAST);
-    KvSeq q = {-1, 0, 0, 0};
-    int local = 0, before = 0;
-    for (int s = 0; s < g.n_seqs; s += 64) {
-        if (g.n_seqs > 64) look(s);
-        const int chunks = max((int)(((unsigned)span + o.chunk - 1) / (unsigned)o.chunk), 1);
-        const int sum = prefix(tiles * chunks);
-        const int c = __popcll(__ballot(before + sum <= y));
-        if (c == 64) {
+    int before = 0;
+    for (int s = 0; s < g.n_seqs; s += 64 * B) {
+        if (g.n_seqs > 64 * B) look(s);
+#pragma unroll
+        for (int i = 0; i < B; i++) {
+            const int chunks = max((int)(((unsigned)span[i] + o.chunk - 1) / (unsigned)o.chunk), 1);
+            const int sum = prefix(tiles[i] * chunks);
+            const int c = __popcll(__ballot(before + sum <= y));
+            if (c < 64) {
+                const int each = __builtin_amdgcn_readlane(chunks, c);
+                const int in = y - before - (c ? __builtin_amdgcn_readlane(sum, c - 1) : 0);
+                local = in / each;
+                o.split = in - local * each;
+                return {s + 64 * i + c, __builtin_amdgcn_readlane(row0[i], c), __builtin_amdgcn_readlane(n_new[i], c),
+                        __builtin_amdgcn_readlane(len[i], c)};
+            }
             before += __builtin_amdgcn_readlane(sum, 63);
-            continue;
         }
-        const int each = __builtin_amdgcn_readlane(chunks, c);
-        const int in = y - before - (c ? __builtin_amdgcn_readlane(sum, c - 1) : 0);
-        q = {s + c, __builtin_amdgcn_readlane(row0, c), __builtin_amdgcn_readlane(n_new, c), __builtin_amdgcn_readlane(len, c)};
-        local = in / each;
-        o.split = in - local * each;
-        break;
     }
+    return {-1, 0, 0, 0};
+}
+
+template <int ROWS>
+__device__ __forceinline__ RowTile piece_of(const KvAttend &a, int y, Piece &o)
+{
+    int local = 0;
+    const KvSeq q = a.g.n_seqs > 64 ? find_piece<ROWS, 4>(a, y, o, local) : find_piece<ROWS, 1>(a, y, o, local);
     o.n = y;
     const RowTile t = tile_of<ROWS>(a, q, local);
     if (t.rows && o.split == 0 && blockIdx.x == 0 && threadIdx.x == 0)

@@ -269,3 +269,18 @@ def test_tall_tiles_special_values(torch, dg):
         spoiled[0, 7] = spoiled[1, 3] = True
         assert torch.isnan(bad[spoiled]).all() and torch.isnan(bad_lse[spoiled]).all()
         assert torch.equal(bad[~spoiled], out[~spoiled]) and torch.equal(bad_lse[~spoiled], lse[~spoiled])
+
+
+# ------------------------------------------------------------------ batches of many workgroups
+
+@pytest.mark.parametrize("kv,group,seqs,long_", [(8, 2, 130, 4400), (16, 1, 70, 2500), (4, 9, 300, 12000)])
+def test_one_long_sequence_among_many(torch, dg, kv, group, seqs, long_):
+    """More workgroups than the chip has places for, cut into chunks for the sake of one sequence."""
+    lens = [1 + i * 7 % 40 for i in range(seqs)]
+    lens[seqs // 3] = long_
+    s = Setup(torch, dg, kv, 64, 256, [1] * seqs, lens, 800 + seqs).fill()
+    assert plan(64, kv, group, seqs, seqs, long_).target > 0 and seqs * kv >= 1024
+    q = s.tensor(kv * group, "bf16")
+    for kw in (dict(), dict(window=1200)):
+        out, lse = run(s, q, "bf16", **kw)
+        compare(s, q, out, lse, "bf16", **kw)

@@ -51,3 +51,17 @@ def test_rows_of_a_tile(D):
     for rows in (33, 64, 65, 128):
         assert plan(D, 1, 1, 1, rows, work - 1).tile == 16
         assert plan(D, 4, 1, 1, rows, work // 4).tile == plan(D, 1, 1, 1, rows, work).tile
+
+
+def test_one_long_sequence_among_many_is_cut():
+    """However many sequences there are, up to where looking at all of them costs a fifteenth of walking the long one; not where
+    the longest is short, and not prompts, which have workgroups enough."""
+    for seqs in (127, 128, 129, 256, 500):
+        assert plan(128, 8, 4, seqs, seqs, 131072).target > 0, seqs
+    assert plan(128, 8, 4, 256, 256, 16384).target and not plan(128, 8, 4, 256, 256, 8000).target
+    assert not plan(128, 8, 4, 4096, 4096, 131072).target
+    assert not plan(128, 8, 4, 128, 128, 1024).target
+    assert not plan(256, 4, 4, 1, 1024, 4096).target and plan(256, 4, 4, 1, 1024, 4096).tile == 16
+    for seqs in (128, 256):                                   # and if only because there is no room for it
+        p = plan(128, 8, 4, seqs, seqs, 131072, 0, 1 << 20)
+        assert not p.target and p.pieces == p.tiles and not p.work_bytes
