@@ -64,6 +64,10 @@ struct KvPlan {
 KvPlan lw_kv_plan(int head_dim, int kv_heads, int group, int64_t n_seqs, int64_t n_tokens, int64_t max_len,
                   int window, size_t room);
 
+// Bytes that no plan of up to that many sequences, new tokens and max_len wants
+// more of, with any window.
+size_t lw_kv_most_work(int head_dim, int kv_heads, int group, int64_t n_seqs, int64_t n_tokens, int64_t max_len);
+
 hipError_t lw_launch_kv_append(const KvGeom &g, int head_dim, const KvTensor &k, const KvTensor &v, int dtype,
                                hipStream_t s);
 hipError_t lw_launch_kv_read(const KvGeom &g, int head_dim, const KvTensor &k, const KvTensor &v, int dtype,

@@ -37,6 +37,7 @@
 // is scaled to lie high in fp16's range and held in two fp16 operands, rounded
 // and what that left (2^-21 in all).  Scores, maxima, sums and outputs are fp32.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "kv_attend.hpp"
@@ -631,6 +632,32 @@ KvPlan lw_kv_plan(int head_dim, int kv_heads, int group, int64_t n_seqs, int64_t
     p.first_at = pieces * result;
     p.work_bytes = p.first_at + notes;
     return p;
+}
+
+size_t lw_kv_most_work(int head_dim, int kv_heads, int group, int64_t n_seqs, int64_t n_tokens, int64_t max_len)
+{
+    const int64_t rows = n_tokens * group, span = std::min<int64_t>(max_len, KV_MOST_TOKENS);
+    auto result = [&](int tile) { return (size_t)kv_heads * tile * (head_dim + 2) * sizeof(float); };
+    size_t most = 0;
+    // cut(): sequences that are cut whatever their rows, and those that are for
+    // the sake of a long one (the root as n (n kv) <= 32 span has it, or one more)
+    const int64_t few = (1023 / kv_heads), many = (int64_t)std::sqrt(32.0 * (double)span / kv_heads) + 1;
+    for (int tile = 8; span > 1024 && tile <= (head_dim > 128 ? 16 : 32); tile *= 2) {
+        if (rows <= (tile == 8 ? 0 : tile / 2)) break;       // (one sequence of that many takes smaller tiles)
+        const int64_t full = rows / tile;
+        const int64_t tiles = std::max(few ? std::min(full, few) + std::min(n_seqs, few) : 0,
+                                       std::min(full, std::min(n_seqs, many)) + std::min(n_seqs, many));
+        most = std::max(most, (std::max(768 / kv_heads, 1) + tiles) * result(tile) + tiles * sizeof(int2));
+    }
+    // tiles of 128: by the larger of sequences and full tiles, x, as the plan
+    // counts workgroups
+    const KvPlan all = lw_kv_plan(head_dim, kv_heads, group, 1, n_tokens, max_len, 0, 0);
+    if (all.tile == 128)
+        for (int64_t x = 1; x * kv_heads < 512 && x <= std::max(n_seqs, (rows + 127) / 128); x++) {
+            const int64_t splits = std::min((512 + x * kv_heads - 1) / (x * kv_heads), (span + LEAST - 1) / LEAST);
+            if (splits > 1) most = std::max(most, (std::min(x, rows / 128) + std::min(x, n_seqs)) * splits * result(128));
+        }
+    return most;
 }
 
 hipError_t lw_launch_kv_attend(const KvAttend &a, int head_dim, int dtype, const KvPlan &p, hipStream_t s)

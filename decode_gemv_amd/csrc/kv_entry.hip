@@ -76,13 +76,11 @@ lw_status device(hipError_t e, const char *what)
     return lw_fail(LW_E_DEVICE, std::string(what) + ": " + hipGetErrorString(e));
 }
 
-// `room`: bytes of work.
-KvPlan plan_of(const lw_kv_cache *c, const lw_kv_batch *b, int64_t n_tokens, int q_heads, int window, size_t room)
+// Tokens of the longest sequence, as far as the host knows.
+int64_t longest(const lw_kv_cache *c, const lw_kv_batch *b)
 {
     const int64_t cap = b->table_stride * c->page_tokens;
-    const int64_t longest = b->max_len ? (b->max_len < cap ? b->max_len : cap) : cap;
-    return lw_kv_plan(c->head_dim, c->kv_heads, q_heads / c->kv_heads, b->n_seqs, n_tokens, longest, window,
-                      room);
+    return b->max_len ? std::min(b->max_len, cap) : cap;
 }
 
 }  // namespace
@@ -127,7 +125,8 @@ extern "C" size_t lw_kv_attend_scratch_bytes(const lw_kv_cache *cache, const lw_
     if (q_heads < 1 || q_heads % cache->kv_heads || q_heads / cache->kv_heads > 1024 ||
         n_tokens * (q_heads / cache->kv_heads) > (1 << 30))
         return 0;
-    return plan_of(cache, batch, n_tokens, q_heads, 0, SIZE_MAX).work_bytes;
+    return lw_kv_most_work(cache->head_dim, cache->kv_heads, q_heads / cache->kv_heads, batch->n_seqs, n_tokens,
+                           longest(cache, batch));
 }
 
 extern "C" lw_status lw_kv_attend(const lw_kv_cache *cache, const lw_kv_batch *batch, int64_t n_tokens,
@@ -149,7 +148,8 @@ extern "C" lw_status lw_kv_attend(const lw_kv_cache *cache, const lw_kv_batch *b
     if ((st = tensor(q, "q", dtype, a.q)) || (st = tensor(out, "out", dtype, a.out))) return st;
     if (!aligned(lse, 4)) return lw_fail(LW_E_ARG, "lse must be 4-byte aligned");
     if (!aligned(work, 16)) return lw_fail(LW_E_ARG, "work must be 16-byte aligned");
-    const KvPlan p = plan_of(cache, batch, n_tokens, q_heads, window, work ? work_bytes : 0);
+    const KvPlan p = lw_kv_plan(cache->head_dim, cache->kv_heads, q_heads / cache->kv_heads, batch->n_seqs, n_tokens,
+                                longest(cache, batch), window, work ? work_bytes : 0);
     if (p.tile == 128 && p.tiles > 65535)
         return lw_fail(LW_E_UNSUPPORTED, "more than 65535 tiles of query rows (n_seqs + n_tokens * q_heads / kv_heads / 128)");
     a.lse = lse;

@@ -505,8 +505,9 @@ lw_status lw_kv_attend(const lw_kv_cache *cache, const lw_kv_batch *batch, int64
                        float *lse, void *work, size_t work_bytes, void *stream);
 
 /* Bytes of work with which lw_kv_attend cuts long sequences as finely as it
- * would like to, for batches of up to that many sequences, rows and max_len
- * (0 where one chunk a sequence does, or for arguments that it refuses). */
+ * would like to, for all batches of up to that many sequences, rows and
+ * max_len and with any window: it does not fall as these grow (0 where one
+ * chunk a sequence does for all of them, or for arguments that it refuses). */
 size_t lw_kv_attend_scratch_bytes(const lw_kv_cache *cache, const lw_kv_batch *batch, int64_t n_tokens, int q_heads);
 
 /* ---------------------------------------------------------------- pipelines */

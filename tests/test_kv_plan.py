@@ -1,9 +1,11 @@
 """How lw_kv_attend cuts a call up (lw_kv_plan), on the host: the library's own function, called by its C++ name."""
 import ctypes as C
 
+import numpy as np
 import pytest
 
 import decode_gemv_amd as dg
+from decode_gemv_amd import lw
 
 ANY = (1 << 64) - 1                                           # bytes of work without a limit
 TOKENS = 0x7FFF0000                                           # of a sequence, at most, for the kernels
@@ -65,3 +67,42 @@ def test_one_long_sequence_among_many_is_cut():
     for seqs in (128, 256):                                   # and if only because there is no room for it
         p = plan(128, 8, 4, seqs, seqs, 131072, 0, 1 << 20)
         assert not p.target and p.pieces == p.tiles and not p.work_bytes
+
+
+def scratch(D, kv, group, seqs, tokens, longest):
+    cache = lw.lw_kv_cache(1 << 20, 4, kv, D, 32)
+    batch = lw.lw_kv_batch(seqs, 1 << 20, 1 << 20, 1 << 20, 1 << 26, longest)
+    return dg.lib().lw_kv_attend_scratch_bytes(C.byref(cache), C.byref(batch), tokens, kv * group)
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_work_for_the_largest_batch_does_for_smaller_ones(seed):
+    """lw_kv_attend_scratch_bytes of a shape is what no smaller one (sequences, rows, longest sequence, with any window)
+    wants more of, and does not fall as the shape grows; nor is it far more than the largest of them wants."""
+    rng = np.random.default_rng(seed)
+    log = lambda lo, hi: int(round(np.exp(rng.uniform(np.log(lo), np.log(hi)))))
+    D, kv, group = int(rng.choice([64, 128, 256])), log(1, 1024), log(1, 64)
+    seqs, longest = log(1, 4000), log(1, 200000)
+    tokens = log(1, 20000)
+    have, want = scratch(D, kv, group, seqs, tokens, longest), 0
+    for _ in range(3000):
+        n, t, l = log(1, seqs), log(1, tokens), log(1, longest)
+        want = max(want, plan(D, kv, group, n, t, l, int(rng.choice([0, log(1, 100000)]))).work_bytes)
+        if rng.random() < 0.02:
+            assert scratch(D, kv, group, n, t, l) <= have
+    edges = [n for n in (seqs, 1023 // kv, 1024 // kv, 511 // kv, 1) if 1 <= n <= seqs]
+    rows = [r * n for n in edges for r in (8, 9, 16, 17, 32, 33, 64, 65, 128)] + [128 * n for n in edges]
+    for n in edges:
+        for t in {min(tokens, max(1, r // group)) for r in rows} | {tokens}:
+            want = max(want, plan(D, kv, group, n, t, longest).work_bytes)
+    assert want <= have <= 2.5 * want + (1 << 12), (D, kv, group, seqs, tokens, longest, want, have)
+
+
+def test_work_across_the_thresholds():
+    for seqs in range(1, 400):
+        assert scratch(128, 8, 4, seqs, seqs, 131072) <= scratch(128, 8, 4, seqs + 1, seqs + 1, 131072)
+    assert scratch(128, 8, 4, 4096, 4096, 131072) > 0
+    for tokens in range(1, 300):
+        assert scratch(128, 2, 4, 3, tokens, 16384) <= scratch(128, 2, 4, 3, tokens + 1, 16384)
+    for longest in range(900, 1100):
+        assert scratch(64, 4, 4, 9, 9, longest) <= scratch(64, 4, 4, 9, 9, longest + 1)
