@@ -593,7 +593,7 @@ def lw_kv_attend(cache: KvCache, batch: KvBatch, q, out, scale: float | None = N
     pl, wp, wn = None, None, 0
     if lse is not None:
         pl = _dptr(lse, "lse")
-        if lse.numel() != n * heads or lse.element_size() != 4:
+        if lse.shape != q.shape[:2] or (_KV_TYPES or _kv_types()).get(lse.dtype) != LW_F32:
             raise LwError(LW_E_ARG, "lse must be fp32 [tokens][q_heads]")
     if work is not None and work.numel():
         wp, wn = _wbuf(work)

@@ -284,3 +284,20 @@ def test_one_long_sequence_among_many(torch, dg, kv, group, seqs, long_):
     for kw in (dict(), dict(window=1200)):
         out, lse = run(s, q, "bf16", **kw)
         compare(s, q, out, lse, "bf16", **kw)
+
+
+def test_log_sums_are_fp32_by_token_and_head(torch, dg):
+    from decode_gemv_amd import lw
+    s = Setup(torch, dg, 2, 64, 32, [3], [40], 95).fill()
+    q = s.tensor(8, "fp16")
+    out = torch.empty_like(q)
+    for bad in (torch.zeros((3, 8), dtype=torch.int32, device="cuda"), torch.zeros((8, 3), device="cuda"),
+                torch.zeros(24, device="cuda"), torch.zeros((3, 8), dtype=torch.float64, device="cuda"),
+                torch.zeros((3, 8), dtype=torch.float16, device="cuda"), torch.zeros((8, 3), device="cuda").T):
+        with pytest.raises(dg.LwError):
+            dg.lw_kv_attend(s.cache, s.batch, q, out, lse=bad)
+        assert not bad.any()
+    lw._KV_TYPES.clear()                                      # as in a process's first call
+    lse = torch.zeros((3, 8), device="cuda")
+    dg.lw_kv_attend(s.cache, s.batch, q, out, lse=lse)
+    compare(s, q, out, lse, "fp16")
