@@ -238,6 +238,8 @@ __device__ __forceinline__ KvSeq find_piece(const KvAttend &a, int y, Piece &o, 
                 const int each = __builtin_amdgcn_readlane(chunks, c);
                 const int in = y - before - (c ? __builtin_amdgcn_readlane(sum, c - 1) : 0);
                 local = in / each;
+                // (else a start that decreases has taken the sums past 2^31)
+                if (in < 0 || local >= __builtin_amdgcn_readlane(tiles[i], c)) return {-1, 0, 0, 0};
                 o.split = in - local * each;
                 return {s + 64 * i + c, __builtin_amdgcn_readlane(row0[i], c), __builtin_amdgcn_readlane(n_new[i], c),
                         __builtin_amdgcn_readlane(len[i], c)};
@@ -381,8 +383,11 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttend a)
     const int2 at = a.target ? a.first[x] : make_int2((int)x * a.splits, a.chunk);
     const RowTile t = row_tile<ROWS>(a, (int)x);
     if (t.rows == 0) return;                                 // (and the first chunk's number is nobody's)
+    // (where start decreases, a tile's chunks may not all have had a workgroup,
+    // and what its first one's number would be is anything)
+    if (a.target && at.y < LEAST) return;
     const int used = chunks_of(t, at.y, a.target ? INT_MAX : a.splits);
-    if (used == 1) return;
+    if (used == 1 || (a.target && (at.x < 0 || at.x > a.pieces - used))) return;
     const int d0 = threadIdx.x % C * 8;
     float y[8], top = NONE, l = 0.0f;
 #pragma unroll

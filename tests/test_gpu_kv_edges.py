@@ -301,3 +301,33 @@ def test_log_sums_are_fp32_by_token_and_head(torch, dg):
     lse = torch.zeros((3, 8), device="cuda")
     dg.lw_kv_attend(s.cache, s.batch, q, out, lse=lse)
     compare(s, q, out, lse, "fp16")
+
+
+@pytest.mark.parametrize("how", [0, 1, 2])
+def test_starts_that_decrease(torch, dg, how):
+    """An error of the caller's, in device memory, that no host check sees: results are anything, but nothing outside of
+    the call's tensors is touched, whatever the workspace held."""
+    starts = [[0, 9, 2, 12, 1, 20, 3], [30, 20, 10, 5, 0, -7, 40], [0, 1 << 30, -(1 << 31), 17, 40, 2, (1 << 31) - 1]]
+    s = Setup(torch, dg, 2, 64, 64, [6] * 6, [3000, 700, 1500, 64, 2000, 900], 97 + how).fill()
+    rows, heads, pad = 36, 6, 4096
+    start = torch.tensor(starts[how], dtype=torch.int32, device="cuda")
+    batch = dg.KvBatch(start, s.batch.lens, s.batch.table, max_len=3000)
+    need = dg.lw_kv_attend_scratch_bytes(s.cache, batch, rows, heads)
+    assert need and plan(64, 2, 3, 6, rows, 3000).target
+    q = s.tensor(heads, "fp16")
+    for fill in (0, 0xFF, 0x7F, None):
+        say("decreasing", how, fill)
+        mem = torch.full((need + 2 * pad,), fill or 0, dtype=torch.uint8, device="cuda")
+        if fill is None:
+            mem.copy_(torch.from_numpy(s.rng.integers(0, 256, need + 2 * pad, dtype=np.uint8)))
+        before = mem.clone()
+        big = torch.full((rows * heads * 64 + 2 * pad,), 7.0, dtype=torch.float16, device="cuda")
+        out = big[pad:-pad].view(rows, heads, 64)
+        sums = torch.full((rows * heads + 2 * pad,), 7.0, device="cuda")
+        dg.lw_kv_attend(s.cache, batch, q, out, lse=sums[pad:-pad].view(rows, heads), work=mem[pad:-pad])
+        k, v = s.tensor(2, "fp16"), s.tensor(2, "fp16")
+        dg.lw_kv_read(s.cache, batch, k, v)
+        torch.cuda.synchronize()
+        for x, y in ((mem, before), (big, torch.full_like(big, 7.0)), (sums, torch.full_like(sums, 7.0))):
+            assert torch.equal(x[:pad], y[:pad]) and torch.equal(x[-pad:], y[-pad:])
+    assert np.array_equal(s.pages.cpu().numpy(), s.image)
