@@ -307,31 +307,30 @@ struct Query {
 #pragma unroll
         for (int j = 0; j < PER; j++)
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-                top = fmaxf(top, fabsf((float)x[j][i]));
-                sum += (float)x[j][i];
-            }
+            for (int i = 0; i < 8; i++) top = fmaxf(top, fabsf((float)x[j][i]));
 #pragma unroll
-        for (int o = WIDE; o < 64; o *= 2) {
-            top = fmaxf(top, __shfl_xor(top, o));
-            sum += __shfl_xor(sum, o);
-        }
-        // the largest element goes to [2^14, 2^15); an infinity stays one and
-        // makes the row NaN, as its scores are
+        for (int o = WIDE; o < 64; o *= 2) top = fmaxf(top, __shfl_xor(top, o));
+        // the largest element goes to [2^14, 2^15), also before they are summed;
+        // an infinity stays one and makes the row NaN, as its scores are
         const int e = top > 0.0f ? (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127 : 0;
         // (at least a normal number: a hidden token's score is -infinity times
         // this; scores that small are zero either way)
         qs = fmaxf(scale * 1.44269504088896341f * ldexpf(1.0f, e - 14), 0x1p-126f);
-        qsum = ldexpf(sum, 14 - e);
 #pragma unroll
         for (int j = 0; j < PER; j++) {
             constexpr int order[8] = {0, 4, 1, 5, 2, 6, 3, 7};
             h8 y;
 #pragma unroll
-            for (int i = 0; i < 8; i++)
-                y[i] = (_Float16)ldexpf((float)x[j][order[i]], 14 - e - (order[i] % 2 ? 4 : 0));
+            for (int i = 0; i < 8; i++) {
+                const float v = ldexpf((float)x[j][order[i]], 14 - e);
+                sum += v;
+                y[i] = (_Float16)(order[i] % 2 ? v * 0x1p-4f : v);
+            }
             put(j, y);
         }
+#pragma unroll
+        for (int o = WIDE; o < 64; o *= 2) sum += __shfl_xor(sum, o);
+        qsum = sum;
     }
 };
 

@@ -331,3 +331,17 @@ def test_starts_that_decrease(torch, dg, how):
         for x, y in ((mem, before), (big, torch.full_like(big, 7.0)), (sums, torch.full_like(sums, 7.0))):
             assert torch.equal(x[:pad], y[:pad]) and torch.equal(x[-pad:], y[-pad:])
     assert np.array_equal(s.pages.cpu().numpy(), s.image)
+
+
+@pytest.mark.parametrize("group,planned", TILES)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_queries_near_the_largest_number(torch, dg, D, group, planned):
+    """bf16 queries whose elements' sum has no fp32 number, under a scale that brings the scores back."""
+    s = Setup(torch, dg, 1, D, 32, [1], [70], 403 + D).fill()
+    if planned:
+        planned_for(s, planned)
+    x = s.rng.uniform(0.6, 1, (1, group, D)) * np.where(np.arange(group) % 3, 1, -1)[:, None]
+    q = s.tensor(group, "bf16", "dense", (x * 3e38).astype(np.float32))
+    out, lse = run(s, q, "bf16", scale=1e-39)
+    _, fine = compare(s, q, out, lse, "bf16", scale=1e-39)
+    assert fine.all()
