@@ -191,10 +191,12 @@ struct State {
     h8 q[Shape<D, ROWS>::QREG ? Shape<D, ROWS>::PER : 1];    // query operands, where registers hold them
     typename Mma<ROWS>::Acc o[TILES];
     float qs, qsum;              // score = qs * (acc dk + (8 dk - mk) qsum), log2 units
-    float mo, mrow;              // the offset, and the row's largest score when it was set
+    float mo, ref;               // the offset, and the row's largest raw score when it was set (kv_attend.hpp)
     float thr;                   // the raw score that calls for a new offset,
     uint32_t dlim;               // and the dv (fp16 bits) that does
     float l, z;                  // sum p, sum p (8 dv - mv)
+
+    __device__ __forceinline__ Offset offset() const { return offset_of(ref, qs, mo, (float)(6 + 15 - (int)(dlim >> 10))); }
 };
 
 // Raw scores of 32 tokens.
@@ -249,7 +251,7 @@ __device__ __forceinline__ void hide(Scores<D, ROWS> &s, Values<D, ROWS> &v, int
 // Scores may then exceed the reference 2^7 times before the next.  A row's
 // offset depends on what the row sees and on nothing else.
 template <int D, int ROWS>
-__device__ __forceinline__ void fit(State<D, ROWS> &st, const Scores<D, ROWS> &s, const Values<D, ROWS> &v)
+__device__ __forceinline__ void fit(State<D, ROWS> &st, Scores<D, ROWS> &s, const Values<D, ROWS> &v)
 {
     using H = Shape<D, ROWS>;
     float top = -__builtin_inff();
@@ -271,14 +273,18 @@ __device__ __forceinline__ void fit(State<D, ROWS> &st, const Scores<D, ROWS> &s
         dtop = max(dtop, (uint32_t)__shfl_xor((int)dtop, o));
     }
     const bool need = top > st.thr || dtop > st.dlim;
-    const float old = st.mo;
+    const Offset old = st.offset();
     if (need) {
         st.dlim = max(st.dlim, min(dtop, 0x7BFFu) | 0x03FFu);       // up to the next power of two
-        st.mrow = fmaxf(st.mrow, top * st.qs);
-        st.mo = st.mrow - (float)(6 + 15 - (int)(st.dlim >> 10));
-        st.thr = (st.mrow + 7.0f) / st.qs;
+        st.ref = fmaxf(st.ref, top);
+        set_offset(st.ref, st.qs, (float)(6 + 15 - (int)(st.dlim >> 10)), st.mo, st.thr);
     }
-    const float f = __builtin_amdgcn_exp2f(old - st.mo);
+    const Offset now = st.offset();
+#pragma unroll
+    for (int i = 0; i < H::TG; i++)
+#pragma unroll
+        for (int b = 0; b < 4; b++) s[i][b] -= now.shift;
+    const float f = between(old, now);
     st.l *= f;
     st.z *= f;
 #pragma unroll
@@ -392,7 +398,14 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, ROWS>)) void k_kv_attend(KvAtten
     const Span mine = chunk_of(t, piece.chunk, INT_MAX, piece.split);
     if (piece.split > 0 && mine.lo >= mine.hi) return;       // (chunk 0 always leaves a result)
 
-    const Span seen = span_of(a, t, m % ROWS);
+    // (what the loop seldom or never needs is worked out anew from the thread's
+    // number where it is needed: registers)
+    auto thread = [&]() {
+        unsigned i = threadIdx.x;
+        asm volatile("" : "+v"(i));
+        return i;
+    };
+    auto seen = [&]() { return span_of(a, t, (int)(thread() % ROWS)); };
     const Span head_row = span_of(a, t, 0), last_row = span_of(a, t, t.rows - 1);
     const int all_lo = last_row.lo, all_hi = head_row.hi;     // tokens every row sees
     const int P = 1 << a.g.page_shift;
@@ -438,8 +451,8 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, ROWS>)) void k_kv_attend(KvAtten
         });
     }
     if (!H::QREG) __syncthreads();
-    st.mrow = st.mo = NONE;
-    st.thr = NONE / fmaxf(st.qs, 1.0f);
+    st.mo = NONE;
+    st.ref = st.thr = UNSEEN;
     st.dlim = 0;
     st.l = st.z = 0.0f;
 #pragma unroll
@@ -465,7 +478,7 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, ROWS>)) void k_kv_attend(KvAtten
             if (!present(page))
                 hide<D, ROWS>(s, v, t0, Span{0, 0}, lane);
             else if (t0 < all_lo || t0 + STEP > all_hi || t.rows < ROWS)
-                hide<D, ROWS>(s, v, t0, seen, lane);
+                hide<D, ROWS>(s, v, t0, seen(), lane);
             fit<D, ROWS>(st, s, v);
             probabilities<D, ROWS>(hi, lo, st, s, v, mk);
             // the values are unpacked here, not above the branch in fit()
@@ -483,33 +496,39 @@ __global__ __launch_bounds__(NW * 64, (WAVES<D, ROWS>)) void k_kv_attend(KvAtten
     }
 
     // the lanes that share a row, then the wavefronts
+    const unsigned last = thread();
+    const int m_ = last % H::WIDE, g_ = last % 64 / H::WIDE;
+    const Offset offset = st.offset();
+    const float own = __builtin_amdgcn_exp2f(-offset.part);  // (1, or a power of two)
+    st.l *= own;
+    st.z *= own;
 #pragma unroll
     for (int o = Mma<ROWS>::WIDE; o < 64; o *= 2) {
         st.l += __shfl_xor(st.l, o);
         st.z += __shfl_xor(st.z, o);
     }
-    if (g == 0) {
-        sl[wave * H::WIDE + m] = st.l;
-        sm[wave * H::WIDE + m] = st.mo;
+    if (g_ == 0) {
+        sl[wave * H::WIDE + m_] = st.l;
+        sm[wave * H::WIDE + m_] = offset.whole;
     }
     __syncthreads();
     constexpr int MEET = NW * H::COPIES;                     // results of a row, at every ROWS entries
-    float mo = sm[m % ROWS];
+    float mo = sm[m_ % ROWS];
 #pragma unroll
-    for (int w = 1; w < MEET; w++) mo = fmaxf(mo, sm[w * ROWS + m % ROWS]);
+    for (int w = 1; w < MEET; w++) mo = fmaxf(mo, sm[w * ROWS + m_ % ROWS]);
     float *part = chunks_of(t, piece.chunk, INT_MAX) > 1 ? part_of<D, ROWS>(a, piece.n, head) : nullptr;
-    const float f = __builtin_amdgcn_exp2f(st.mo - mo), fixed = st.z * f;
+    const float meet = __builtin_amdgcn_exp2f(offset.whole - mo), f = own * meet, fixed = st.z * meet;
 #pragma unroll
     for (int i = 0; i < S::TILES; i++)
 #pragma unroll
         for (int j = 0; j < M::ACC; j++) {
             const int r = i / H::NT, n = i % H::NT;
-            const int row = H::WIDE == 16 ? 4 * g + j : 8 * (j / 4) + 4 * g + j % 4;  // along the head
+            const int row = H::WIDE == 16 ? 4 * g_ + j : 8 * (j / 4) + 4 * g_ + j % 4;  // along the head
             const int d = 8 * (row % H::DW + r * H::WIDE) + (row / H::DW) * H::NT + n;
-            so[(wave * H::WIDE + m) * H::ROWF + d] = fmaf(st.o[i][j], n % 2 ? 0x1p-4f * f : f, fixed);
+            so[(wave * H::WIDE + m_) * H::ROWF + d] = fmaf(st.o[i][j], n % 2 ? 0x1p-4f * f : f, fixed);
         }
     __syncthreads();
-    for (int i = threadIdx.x; i < t.rows * (D / 8); i += NW * 64) {
+    for (int i = last; i < t.rows * (D / 8); i += NW * 64) {
         const int r = i / (D / 8), d = i % (D / 8) * 8;
         float y[8], top = sm[r], l = 0.0f;
 #pragma unroll

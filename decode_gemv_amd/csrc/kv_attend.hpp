@@ -19,7 +19,8 @@ typedef float f4 __attribute__((ext_vector_type(4)));
 typedef float f16v __attribute__((ext_vector_type(16)));
 
 constexpr int STEP = 32;               // tokens of a wavefront's step
-constexpr float NONE = -1e30f;         // log2 of "nothing seen yet"
+constexpr float NONE = -0x1.fffffep127f;  // log2 of "nothing seen yet"
+constexpr float UNSEEN = -0x1p60f;     // and the raw score of it (what there is lies within 2^44)
 constexpr int CHUNK = 128, LEAST = 512;  // chunks are multiples of the first, and from the second on
 
 __device__ __forceinline__ float half_lo(uint32_t w) { return (float)__builtin_bit_cast(h2, w)[0]; }
@@ -75,6 +76,40 @@ __device__ __forceinline__ h8 spread8(uint32_t w, Masks k)
     const h2 a = centred<false>(w, k), b = centred<true>(w, k);
     const h2 c = centred<false>(w >> 8, k), d = centred<true>(w >> 8, k);
     return h8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// A row's sums are relative to 2^o, o = ref qs - k for a raw score ref and a
+// small number k: p = exp2(s qs - mo), mo = o.  Where ref qs is large, o has no
+// place for k, and the product of s and qs before the subtraction, which is
+// exact in a fused one, differs from ref qs by more than p can bear: there
+// (FAR) ref is taken from the raw scores, which is exact for those near it, and
+// mo is -k.  For a step's scores: a row that is so asks for a look each step.
+constexpr float FAR = 0x1p20f;
+
+struct Offset {
+    float whole, part;           // o = whole - part
+    float shift;                 // to be taken from raw scores
+};
+
+__device__ __forceinline__ Offset offset_of(float ref, float qs, float mo, float k)
+{
+    const bool far = fabsf(ref * qs) >= FAR && ref > 0.5f * UNSEEN;
+    return {far ? ref * qs : mo, far ? k : 0.0f, far ? ref : 0.0f};
+}
+
+__device__ __forceinline__ void set_offset(float ref, float qs, float k, float &mo, float &thr)
+{
+    const float x = ref * qs;
+    const bool far = fabsf(x) >= FAR;
+    asm volatile("" : "+v"(qs));                             // (the division is done here, not ahead of the loop)
+    mo = far ? -k : x - k;
+    thr = far ? -__builtin_inff() : ref + 7.0f / qs;
+}
+
+// What brings sums from one offset to another.
+__device__ __forceinline__ float between(const Offset &old, const Offset &now)
+{
+    return __builtin_amdgcn_exp2f((old.whole - now.whole) - (old.part - now.part));
 }
 
 // The visible tokens of a packed row: first and one past the last.

@@ -148,8 +148,11 @@ struct Rows {
     h8 q[Tile<D>::PER];
     f16v o[NT];
     float qs, qsum;
-    float mo, mrow, thr, dlim;   // offset, its reference, and what calls for a new one (kv_attend.hip)
+    float mo, ref, thr, dlim;    // offset, its reference, and what calls for a new one (kv_attend.hip)
     float l, z;
+
+    __device__ __forceinline__ float k() const { return (float)(7 + 127 - (int)(__builtin_bit_cast(uint32_t, dlim) >> 23)); }
+    __device__ __forceinline__ Offset offset() const { return offset_of(ref, qs, mo, k()); }
 };
 
 __device__ __forceinline__ f16v product(uint4 v, const h2 (&p)[4], f16v o)
@@ -233,15 +236,19 @@ __device__ __forceinline__ void step(Rows<D> &st, const Tile<D> &tile, int sub, 
         top = fmaxf(top, __shfl_xor(top, 32));
         dtop = fmaxf(dtop, __shfl_xor(dtop, 32));
         const bool need = top > st.thr || dtop > st.dlim;
-        const float old = st.mo;
+        const Offset old = st.offset();
         if (need) {
             const uint32_t up = __builtin_bit_cast(uint32_t, fminf(fmaxf(dtop, 0x1p-24f), 65504.0f)) + 0x7FFFFFu;
             st.dlim = fmaxf(st.dlim, __builtin_bit_cast(float, up & 0xFF800000u));          // up to a power of two
-            st.mrow = fmaxf(st.mrow, top * st.qs);
-            st.mo = st.mrow - (float)(7 + 127 - (int)(__builtin_bit_cast(uint32_t, st.dlim) >> 23));
-            st.thr = (st.mrow + 7.0f) / st.qs;
+            st.ref = fmaxf(st.ref, top);
+            set_offset(st.ref, st.qs, st.k(), st.mo, st.thr);
         }
-        const float f = __builtin_amdgcn_exp2f(old - st.mo);
+        const Offset now = st.offset();
+#pragma unroll
+        for (int a = 0; a < 4; a++)
+#pragma unroll
+            for (int b = 0; b < 4; b++) s[a][b] -= now.shift;
+        const float f = between(old, now);
         st.l *= f;
         st.z = dtop > 65504.0f ? __builtin_nanf("") : st.z * f;
 #pragma unroll
@@ -345,6 +352,7 @@ __global__ __launch_bounds__(WV * 64, (D > 64 ? 2 : 3)) void k_kv_prompt(KvAtten
     Masks mk = masks();
     asm("v_mov_b32 %0, 1.0" : "=v"(mk.one));                 // (scalar registers are short here)
     asm("v_mov_b32 %0, 0x000f000f" : "=v"(mk.low));
+    asm("v_mov_b32 %0, 0x00f000f0" : "=v"(mk.high));
     const Put<D> put(threadIdx.x);
     const bool any = mine.lo < mine.hi;
     uint32_t now = 0, next = 0;                              // the parts with a page of the tile in use, and of the one loaded;
@@ -361,8 +369,8 @@ __global__ __launch_bounds__(WV * 64, (D > 64 ? 2 : 3)) void k_kv_prompt(KvAtten
         }
         q.make(st.qs, st.qsum, a.scale, [&](int j, h8 y) { st.q[j] = y; });
     }
-    st.mrow = st.mo = NONE;
-    st.thr = NONE / fmaxf(st.qs, 1.0f);
+    st.mo = NONE;
+    st.ref = st.thr = UNSEEN;
     st.l = st.z = st.dlim = 0.0f;
 #pragma unroll
     for (int n = 0; n < L::NT; n++)
@@ -372,6 +380,7 @@ __global__ __launch_bounds__(WV * 64, (D > 64 ? 2 : 3)) void k_kv_prompt(KvAtten
     const Span seen = span_of(a, t, wave * WIDE + m);
     const int rows = min(t.rows - wave * WIDE, WIDE);
     const Span first = span_of(a, t, wave * WIDE), last = span_of(a, t, wave * WIDE + max(rows, 1) - 1);
+    const int some_hi = rows > 0 ? last.hi : 0, all_hi = rows < WIDE ? 0 : first.hi;
     if (any) {
         unpack<D>(tiles[0], raw, put, mk, wave, lane);
         load(mine.lo + L::TT, after);
@@ -389,9 +398,9 @@ __global__ __launch_bounds__(WV * 64, (D > 64 ? 2 : 3)) void k_kv_prompt(KvAtten
 #pragma unroll
             for (int sub = 0; sub < L::SUBS; sub++) {
                 const int ts = t0 + sub * 32;
-                if (rows <= 0 || ts >= last.hi || ts + 32 <= first.lo || ts >= mine.hi) continue;
+                if (ts >= some_hi || ts + 32 <= first.lo || ts >= mine.hi) continue;
                 if (!(now >> sub & 1u)) continue;                      // (32 absent tokens)
-                step<D>(st, tile, sub, ts, rows < WIDE || ts < last.lo || ts + 32 > first.hi, seen, mk, lane);
+                step<D>(st, tile, sub, ts, ts < last.lo || ts + 32 > all_hi, seen, mk, lane);
             }
             now = next;
             next = behind;
@@ -400,11 +409,15 @@ __global__ __launch_bounds__(WV * 64, (D > 64 ? 2 : 3)) void k_kv_prompt(KvAtten
         }
     }
 
+    const Offset offset = st.offset();
+    const float own = __builtin_amdgcn_exp2f(-offset.part);  // (1, or a power of two)
+    st.l *= own;
+    st.z *= own;
     st.l += __shfl_xor(st.l, 32);
     st.z += __shfl_xor(st.z, 32);
     if (g == 0) {
         sl[wave * WIDE + m] = st.l;
-        sm[wave * WIDE + m] = st.mo;
+        sm[wave * WIDE + m] = offset.whole;
     }
     float *part = chunks_of(t, a.chunk, a.splits) > 1 ? part_of<D, ROWS>(a, (int64_t)x * a.splits + split, head) : nullptr;
     float *so = reinterpret_cast<float *>(mem) + wave * (WIDE * ROWF);
@@ -417,7 +430,7 @@ __global__ __launch_bounds__(WV * 64, (D > 64 ? 2 : 3)) void k_kv_prompt(KvAtten
             for (int j = 0; j < 16; j++) {
                 const int r = 8 * (j / 4) + 4 * g + j % 4, d = 8 * (r % L::DW) + r / L::DW * L::NT + n;
                 if (D > 64 && j / 4 % (D / PD) != pass) continue;             // (d / 64 is that)
-                so[m * ROWF + d % PD] = fmaf(st.o[n][j], n % 2 ? 0x1p-4f : 1.0f, st.z);
+                so[m * ROWF + d % PD] = fmaf(st.o[n][j], n % 2 ? 0x1p-4f * own : own, st.z);
             }
         __syncthreads();
 #pragma unroll

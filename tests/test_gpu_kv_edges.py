@@ -345,3 +345,31 @@ def test_queries_near_the_largest_number(torch, dg, D, group, planned):
     out, lse = run(s, q, "bf16", scale=1e-39)
     _, fine = compare(s, q, out, lse, "bf16", scale=1e-39)
     assert fine.all()
+
+
+@pytest.mark.parametrize("group,planned", TILES)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_scores_far_from_zero(torch, dg, D, group, planned):
+    """Scores so large that fp32 tells them apart by more than an exponential can bear: the largest takes all the weight, also
+    where it is far below zero.  Rows whose two largest are closer than what fp32 scores are off by are left out."""
+    for dtype, size, gain, n in (("fp16", 3e4, 1, 40), ("fp16", 6e4, 300, 40), ("bf16", 1e8, 1, 70), ("bf16", 1e20, 1, 33),
+                                 ("bf16", 1e33, 1, 40), ("bf16", 1e33, 1, 1), ("bf16", 1e31, 1, 2), ("fp16", 6e4, 300, 1),
+                                 ("bf16", 1e12, 1, 1500)):
+        say("large scores", D, group, dtype, size, gain, n)
+        s = Setup(torch, dg, 1, D, 64, [1], [n], 404 + D).fill(gain)
+        if planned:
+            planned_for(s, planned)
+        q = s.tensor(group, dtype, "dense", np.clip(s.rng.standard_normal((1, group, D)) * size, -3e38 if dtype == "bf16" else -65504,
+                                                     3e38 if dtype == "bf16" else 65504).astype(np.float32))
+        out, lse = run(s, q, dtype)
+        cache = R.Cache(s.pages.cpu().numpy(), 1, D, 64)
+        ref, rl, by = R.attend(cache, s.table, s.start, s.lens, host(q).astype(np.float64), D ** -0.5)
+        k, v, _, dv, _ = cache.tokens(s.table[0], n)
+        x = np.sort(host(q)[0].astype(np.float64) @ k[:, 0].T * D ** -0.5, -1)
+        delta = (D + 8) * 2.0 ** -23 * by["size"][0]
+        clear = np.ones(group, bool) if n == 1 else x[:, -1] - x[:, -2] > 2 * delta + 40
+        assert clear.sum() >= group // 4
+        top = np.abs(dv[:, 0, 0]).max() * 8
+        tol = 2.0 ** (-8 if dtype == "bf16" else -11) * np.abs(ref[0]) + 2.0 ** -20 * top + 2.0 ** -25
+        assert np.all(np.abs(host(out)[0] - ref[0])[clear] <= tol[clear])
+        assert np.all(np.abs(host(lse)[0] - rl[0]) <= delta + 2.0 ** -21 * (1 + np.abs(rl[0])))
