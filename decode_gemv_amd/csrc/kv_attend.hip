@@ -45,8 +45,9 @@
 namespace {
 
 // Wavefronts of a workgroup.  16 sequences of 501 to 8190 tokens (replays of a
-// graph, with the join) take 26.5 us with 4, 28.8 with 2 and 31.0 with 8, one of
-// 131071 42.9, 47.8 and 45.2, 96 in a window of 1024 33.3, 37.3 and 39.2.
+// graph, with the join; a call among others takes some 6 us less) take 28.5 us
+// with 4, 31.6 with 2 and 32.3 with 8, one of 131071 42.7, 46.0 and 44.1, 96 in
+// a window of 1024 35.5, 40.4 and 41.4.
 constexpr int NW = 4;
 
 // A row tile has 8, 16 or 32 rows.  16 and 32 are the columns of a matrix
@@ -71,8 +72,9 @@ template <> struct Mma<32> {           // 32 x 32 x 16: lane = row/column l % 32
 };
 
 // Wavefronts a SIMD is to hold (the registers that leaves).  Six of 8 rows of
-// 64 dimensions take 34.4 us for 96 sequences of 16 heads in a window of 1024
-// tokens (bf16, replays of a graph), five 37.4.
+// 64 dimensions take 36.5 us in bf16 and 35.5 in fp16 for 96 sequences of 16
+// heads in a window of 1024 tokens (replays of a graph), five 39.2 and 38.6;
+// 200 sequences of 600 tokens 29.0 and 29.8.
 template <int D, int ROWS>
 constexpr int WAVES = D * ROWS <= 512 ? 6 : D * ROWS <= 1024 ? 4 : D * ROWS <= 2048 ? 3 : 2;
 
@@ -577,8 +579,9 @@ namespace {
 
 // Whether sequences are cut into chunks.  Not up to 1024 tokens; from there on
 // where there are fewer workgroups than the chip has places for: heads of 128,
-// 32 on 8, 8 sequences of 1000 tokens 17.2 us cut and 15.9 not, one of 1500
-// 16.6 and 18.7, 48 of 500 to 8190 63 and 79.  And where one sequence may be
+// 32 on 8 (replays of a graph), 8 sequences of 1000 tokens 18.0 us cut and 17.8
+// not, 8 of 1300 18.8 and 20.3, one of 1500 17.3 and 20.3, 48 of 500 to 8190 65
+// and 87, 100 of 100 to 4000 70 and 68.  And where one sequence may be
 // far longer than the others, whose workgroups would leave it alone on the
 // chip: 128 sequences of 500 tokens and one of 131071, 57 us and not 786 (256:
 // 76 and 893, 512: 128 and 934).  That has a price, as each workgroup looks at
@@ -605,17 +608,25 @@ KvPlan lw_kv_plan(int head_dim, int kv_heads, int group, int64_t n_seqs, int64_t
     int64_t span = std::min<int64_t>(max_len, KV_MOST_TOKENS);
     if (window) span = std::min<int64_t>(span, (int64_t)window + 128 + STEP);
     // Query rows of a tile.  Up to 8, 16 or 32 a sequence on average: all of
-    // them (8 sequences of 20 rows on 4000 tokens, heads of 128: 28.8 us with
-    // 32 and 30.5 with 16; 32 sequences 62 and 72).  More: 128 (kv_prompt.hip)
-    // where there is work enough, by the products of 128 rows with a token,
-    // as that kernel needs many workgroups to be fast and others to follow
-    // them: 4096 tokens on 8192, 32 heads on 8 of 128, 534 us with 128, 700
-    // with 32 and 813 with 16; 1024 on 4096 (2^20) 120, 128 and 143; 1024 on
-    // themselves (2^18) 50, 43 and 41; 300 on 8000, 8 heads on 2, 48, 46 and
-    // 43.  32 to 64 rows: 16 or 32 alike (8 sequences of 64 on 4000: 39 and
-    // 46).  Heads of 256 have registers for 16 rows and a second wavefront,
-    // but not for more: 1024 on 4096, 16 heads on 4, 136 us, 219 with 32 and
-    // 164 with 128.
+    // them (8 sequences of 20 rows on 4000 tokens, heads of 128: 28.0 us with
+    // 32 and 30.2 with 16, heads of 64 23.9 and 25.0; 32 sequences 63 and 75,
+    // 45 and 57).  More: 128 (kv_prompt.hip) where there is work enough, by the
+    // products of 128 rows with a token, as that kernel needs many workgroups
+    // to be fast and others to follow them.  With tiles of 16, 32 and 128 rows,
+    // 32 heads on 8, heads of 128 and (heads of 64), us:
+    //   1024 on themselves, 2^18   41, 43, 51        (31, 28, 40)
+    //   1024 on 2048, 2^19         76, 71, 83        (56, 54, 63)
+    //   512 on 4096, 2^19          87, 108, 78       (63, 80, 63)
+    //   256 on 8192, 2^19          121, 88, 77       (88, 63, 72)
+    //   2048 on themselves, 2^20   100, 97, 89       (73, 68, 78)
+    //   512 on 8192, 2^20          162, 182, 130     (116, 135, 112)
+    //   4096 on 8192, 2^23         875, 770, 639     (601, 523, 487)
+    // 33 to 64 rows with that work: 32, of which 128 would be half empty (8
+    // sequences of 64 on 16384: 101, 94, 185 and 73, 66, 99); with less, 16 (8
+    // of 64 on 4000: 39, 44, 63 and 31, 32, 39).  Heads of 256 have registers
+    // for 16 rows and a second wavefront, but not for more: 1024 on 4096, 16
+    // heads on 4, 131 us (32 rows and 128 rows took half as long again and a
+    // fifth more).
     const bool much = (rows + 127) / 128 * kv_heads * std::min<int64_t>(span, 1 << 20) >= 1 << 19;
     p.tile = rows <= 8 * n_seqs                       ? 8
              : rows <= 16 * n_seqs || head_dim > 128 ? 16
@@ -628,8 +639,8 @@ KvPlan lw_kv_plan(int head_dim, int kv_heads, int group, int64_t n_seqs, int64_t
     const size_t result = (size_t)kv_heads * p.tile * (head_dim + 2) * sizeof(float);
     if (p.tile == 128) {
         // Chunks for two workgroups a CU: more cost their results' way through
-        // memory (2048 new tokens on themselves: 101 us with twice as many,
-        // 93 so)
+        // memory (2048 new tokens on themselves: 101 us with twice as many, 89
+        // so), fewer leave CUs idle (512 on 16384: 385 us with half, 235 so)
         const int64_t base = std::max(n_seqs, (rows + p.tile - 1) / p.tile) * kv_heads;
         int64_t splits = std::min((512 + base - 1) / base, (span + LEAST - 1) / LEAST);
         splits = std::max<int64_t>(std::min(splits, (int64_t)(room / result) / p.tiles), 1);
@@ -639,9 +650,10 @@ KvPlan lw_kv_plan(int head_dim, int kv_heads, int group, int64_t n_seqs, int64_t
         return p;
     }
     if (!cut(kv_heads, n_seqs, rows, p.tile, span)) return p;
-    // Into about 768 pieces, three for a CU: 16 sequences of 501 to 8190 tokens
-    // take 26.8 us, with 1024 28.1 and with 1536 30.3; one of 131071 43.5,
-    // 43.3 and 47; 32 of 16384 116, 119 and 120.
+    // Into about 768 pieces, three for a CU (replays of a graph): 16 sequences
+    // of 501 to 8190 tokens take 28.5 us, with 512 32.7, with 1024 30.1 and with
+    // 1536 31.7; one of 131071 42.7, 41.7, 42.9 and 45.8; 32 of 16384 119, 118,
+    // 120 and 124.
     const size_t notes = p.tiles * sizeof(int2);
     int64_t pieces = std::max(768 / kv_heads, 1) + p.tiles;
     if (room < notes || (room - notes) / result < (size_t)pieces) pieces = room < notes ? 0 : (room - notes) / result;

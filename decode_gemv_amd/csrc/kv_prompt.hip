@@ -2,41 +2,40 @@
 // for heads of 64 and 128 (lw_kv_plan in kv_attend.hip says when).
 //
 // The mathematics is kv_attend.hip's.  There each wavefront unpacks the codes
-// that it uses, which for many query rows is most of its work: 152 of some 400
+// that it uses, which for many query rows is most of its work: 152 of some 440
 // instructions for 32 tokens and 32 rows.  Here a workgroup has 128 rows of a
-// sequence, 32 for each wavefront, and goes through the tokens in tiles of 64
-// each wavefront unpacks a quarter of a tile's keys and
-// values into LDS, laid out as the matrix operands that all four then read in
-// whole 16-byte lanes, and turns their pairs into the factors of scores and
-// values, once per token instead of once per lane.  Two buffers: a tile is
-// unpacked, and the one after it loaded, while the one before is used, with
-// one barrier a tile.  No tokens are shared out between wavefronts, so nothing
-// has to be joined at the end, and two workgroups stand on a CU whose phases
-// (unpacking, products, exponentials) fill each other's gaps.
+// sequence, 32 for each wavefront, and goes through the tokens in tiles of 64:
+// each wavefront unpacks a quarter of a tile's keys and values into LDS, laid
+// out as the matrix operands that all four then read in whole 16-byte lanes,
+// and turns their pairs into the factors of scores and values, once per token
+// instead of once per lane.  Two buffers: a tile is unpacked, and the one after
+// it loaded, while the one before is used, with one barrier a tile.  No tokens
+// are shared out between wavefronts, so nothing has to be joined at the end,
+// and two workgroups stand on a CU whose phases (unpacking, products,
+// exponentials) fill each other's gaps.
 //
 // What bounds it: issue.  For 32 tokens and 32 rows of 128 dimensions a
-// wavefront has 512 cycles of matrix instructions and some 830 of others, at
+// wavefront has 768 cycles of matrix instructions and some 900 of others, at
 // what they were measured to take (4 to 4.6 a multiply-add, a conversion or an
 // operation on packed halves, 2.6 a multiplication or addition, 8.5 an
-// exponential: 16 elements a lane with 9 of them, and 43 operations of
-// unpacking), and a SIMD does one such part in 1430: with two wavefronts the
-// two kinds hardly overlap, and the times of the parts add up (of 1208 us,
-// 4096 tokens on 16384, unpacking takes 320, the values' products 250, the
-// keys' 200, the factors' reads 200, the exponentials 130).  A wavefront alone
-// on its SIMD issues one instruction in 5.4 cycles and takes as long for a
-// part as two side by side, so the calls that leave the longest rows'
-// workgroups alone at the end (prompts of up to 2048 tokens, where all are
-// there from the start) are bound by those.
+// exponential), and a SIMD does one such part in some 1800: with two wavefronts
+// the two kinds hardly overlap, and the times of the parts add up (4096 tokens
+// on 16384, 1467 us: unpacking takes 320, the values' products 250 for p dv and
+// 250 for what its rounding leaves, the keys' 200, the factors' reads 200, the
+// exponentials 130).  A wavefront alone on its SIMD issues one instruction in
+// 5.4 cycles and takes as long for a part as two side by side, so the calls
+// that leave the longest rows' workgroups alone at the end (prompts of up to
+// 2048 tokens, where all are there from the start) are bound by those.
 //
-// Measured, heads of 128 in bf16, 32 of them on 8: 16384 tokens on themselves
-// 849 TFLOP/s (tiles of 32 rows of kv_attend.hip: 633), 2048 on 16384 778
-// (638), 2048 on themselves 389 (354).
+// Measured, bf16, 32 heads on 8 (replays of a graph; in brackets tiles of 32
+// rows of kv_attend.hip): heads of 128, 16384 tokens on themselves 3.28 ms, 670
+// TFLOP/s (4.03 ms), 2048 on 16384 814 us, 633 (943), 2048 on themselves 89 us,
+// 386 (97); heads of 64, 2.15 ms, 511 (2.73), 614 us, 420 (645), and 78 us (68).
 //
-// Rounding: as in kv_attend.hip.  The second operand of p dv, what its rounding
-// to fp16 leaves, costs 18 % (chunks of 511 to 1024 new tokens on 9000 to 16384,
-// 64 heads on 8 of 128 in fp16: 1734 us and not 1448); without it fp16 results
-// lie 3.0e-4 of their size from 64 bits, with it 2.1e-4, which is their own
-// rounding.
+// Rounding: as in kv_attend.hip.  The second operand of p dv costs 24 % of the
+// longest calls (3.28 ms and not 2.65) and 11 % of 2048 on themselves; without
+// it fp16 results lie 3.0e-4 of their size from 64 bits, with it 2.1e-4, which
+// is their own rounding.
 #include <stddef.h>
 
 #include <algorithm>
@@ -172,10 +171,6 @@ __device__ __forceinline__ void step(Rows<D> &st, const Tile<D> &tile, int sub, 
     f16v acc;
 #pragma unroll
     for (int i = 0; i < 16; i++) acc[i] = 0.0f;
-    // Operands are read ahead of their use, held there by the fences: the keys'
-    // before the products, and where there are registers, the values' before
-    // the exponentials (823 TFLOP/s and not 811)
-    constexpr bool EARLYV = D > 64;
     auto values = [&](int kk, int n) { return *reinterpret_cast<const uint4 *>(&tile.v[sub][kk][n][lane][0]); };
     const float4 *kf = reinterpret_cast<const float4 *>(&tile.kf[sub * 32 + 4 * g]);
     const float4 *vf = reinterpret_cast<const float4 *>(&tile.vf[sub * 32 + 4 * g]);
@@ -185,7 +180,6 @@ __device__ __forceinline__ void step(Rows<D> &st, const Tile<D> &tile, int sub, 
     float dm[PIECES];
 #pragma unroll
     for (int i = 0; i < PIECES; i++) dm[i] = tile.dmax[sub * PIECES + i];
-    asm volatile("" ::: "memory");
 #pragma unroll
     for (int j = 0; j < L::PER; j++)
         acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, kw[j]), st.q[j], acc, 0, 0, 0);
@@ -222,12 +216,6 @@ __device__ __forceinline__ void step(Rows<D> &st, const Tile<D> &tile, int sub, 
         bits &= (uint32_t)((1ull << min(max(seen.hi - t0, 0), 32)) - 1) & ~(uint32_t)((1ull << min(max(seen.lo - t0, 0), 32)) - 1);
         dtop = bits ? __builtin_inff() : dtop;
     }
-    uint4 vw[2][L::NT];
-    if (EARLYV) {
-#pragma unroll
-        for (int n = 0; n < L::NT; n++) vw[0][n] = values(0, n);
-    }
-    if (EARLYV) asm volatile("" ::: "memory");
 #pragma unroll
     for (int a = 0; a < 4; a++)
 #pragma unroll
@@ -270,18 +258,14 @@ __device__ __forceinline__ void step(Rows<D> &st, const Tile<D> &tile, int sub, 
             st.z = fmaf(r, x.w, fmaf(p, x.y, st.z));
             split2(p * x.x, r * x.z, mk, e[c], rest[c]);
         }
-        if (EARLYV && kk == 0) {
-#pragma unroll
-            for (int n = 0; n < L::NT; n++) vw[1][n] = values(1, n);
-            asm volatile("" ::: "memory");
-        }
+        uint4 vw[L::NT];
 #pragma unroll
         for (int n = 0; n < L::NT; n++) {
-            if (!EARLYV) vw[kk][n] = values(kk, n);
-            st.o[n] = product(vw[kk][n], e, st.o[n]);
+            vw[n] = values(kk, n);
+            st.o[n] = product(vw[n], e, st.o[n]);
         }
 #pragma unroll
-        for (int n = 0; n < L::NT; n++) st.o[n] = product(vw[kk][n], rest, st.o[n]);
+        for (int n = 0; n < L::NT; n++) st.o[n] = product(vw[n], rest, st.o[n]);
     }
 }
 
@@ -289,8 +273,8 @@ __device__ __forceinline__ void step(Rows<D> &st, const Tile<D> &tile, int sub, 
 // every second four the other way round, as consecutive workgroups of an XCD
 // go round its four shader engines and would give the first of them the
 // longest of each four.  (Chunks come last in the grid for the same reason:
-// with a tile's two chunks side by side, half of the engines got the short
-// ones, and 2048 tokens on themselves took 112 us and not 93.)
+// with a tile's two chunks side by side, half of the engines get the short
+// ones, which cost 2048 tokens on themselves a fifth.)
 __device__ __forceinline__ int order_of(int tiles, int y)
 {
     if ((y | 3) < tiles && y & 4) y ^= 3;
