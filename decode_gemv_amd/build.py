@@ -21,8 +21,9 @@ LIB = os.path.join(PKG, "liblw.so")
 ARCH = "gfx950"
 
 HIP_SOURCES = ["runtime.hip", "fused_q.hip", "bf16.hip", "mfma.hip", "twin.hip", "mlp.hip", "skip.hip", "probe.hip", "rans.hip", "recon.hip",
-               "kv_cache.hip", "kv_attend.hip", "kv_prompt.hip", "kv_entry.hip"]
-CXX_SOURCES = ["bundle.cpp"]
+               "kv_cache.hip", "kv_attend.hip", "kv_prompt.hip", "kv_selected.hip", "kv_select.hip", "kv_weigh.hip", "rope.hip",
+               "kv_entry.hip"]
+CXX_SOURCES = ["bundle.cpp", "rope.cpp"]
 
 
 def hipcc() -> str:

@@ -38,7 +38,7 @@ struct KvAttend {
     KvGeom g;
     KvTensor q, out;
     float *lse;                  // [n_tokens][q_heads], or null
-    float *part;                 // split partials (see kv_attend.hip), or null
+    float *part;                 // split partials (see kv_attend.hpp), or null
     int32_t group;               // query heads per kv head
     uint32_t group_inv;          // ceil(2^21 / group): (x * group_inv) >> 21 = x / group for x < 2048
     int32_t causal, window;      // window 0: none
@@ -74,6 +74,48 @@ hipError_t lw_launch_kv_read(const KvGeom &g, int head_dim, const KvTensor &k, c
                              hipStream_t s);
 hipError_t lw_launch_kv_attend(const KvAttend &a, int head_dim, int dtype, const KvPlan &p, hipStream_t s);
 hipError_t lw_launch_kv_prompt(const KvAttend &a, int head_dim, int dtype, const KvPlan &p, hipStream_t s);
+
+// A selection of pages (kv_select.hip): what chooses it, and where it goes.
+struct KvSelect {
+    KvGeom g;
+    KvTensor q;
+    const uint8_t *bounds;
+    int64_t bounds_bytes;        // of a page
+    int32_t group;
+    int32_t first, last, take;   // first + last < take
+    int32_t *start, *lens, *table;
+    uint32_t *work;              // keys [n_tokens][kv_heads][g.stride], or null
+};
+
+struct KvWeigh {
+    KvAttend a;                  // no outputs
+    const float *lse, *before;   // before: may be null
+    float *weights;
+    int64_t stride;              // pages of a head in before and weights, at most 2^24
+    float decay;
+};
+
+struct KvEvict {
+    KvGeom g;
+    const float *weights;
+    int64_t stride, keep;
+    int32_t first, last;
+    int32_t *table, *gone, *count;
+};
+
+constexpr int64_t KV_PICK_MOST = 32768;                      // pages that are chosen from (LDS)
+
+hipError_t lw_launch_rope(const lw_rope_plan &plan, const KvGeom &g, const int32_t *pos, int heads, int head_dim,
+                          const KvTensor &x, int x_dtype, const KvTensor &y, int y_dtype, hipStream_t s);
+hipError_t lw_launch_kv_bounds(const KvGeom &g, int head_dim, uint8_t *bounds, int64_t bounds_bytes, hipStream_t s);
+// `pages`: of the longest sequence, as far as the host knows.
+hipError_t lw_launch_kv_select(const KvSelect &a, int head_dim, int dtype, int64_t pages, hipStream_t s);
+// Whether a row's scores are shared out over workgroups.
+bool lw_kv_select_shared(int kv_heads, int64_t n_tokens, int64_t pages);
+// a.splits and a.chunk say how rows are cut; a.g's start, lens and table are the selection's.
+hipError_t lw_launch_kv_selected(const KvAttend &a, int head_dim, int dtype, int tile, hipStream_t s);
+hipError_t lw_launch_kv_weigh(const KvWeigh &b, int head_dim, int dtype, int64_t pages, hipStream_t s);
+hipError_t lw_launch_kv_evict(const KvEvict &a, hipStream_t s);
 
 #ifdef __HIPCC__
 // ------------------------------------------------------------ device helpers

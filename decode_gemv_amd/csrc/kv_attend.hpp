@@ -184,6 +184,24 @@ __device__ __forceinline__ RowTile row_tile(const KvAttend &a, int x)
     return tile_of<ROWS>(a, q, x - first_tile<ROWS>(a, q.row0, q.seq));
 }
 
+// Row tile x of selected pages (kv_selected.hip): a new token is a sequence by
+// itself, whose heads fill ceil(group / ROWS) tiles, and all of its tokens are
+// seen.
+template <int ROWS>
+__device__ __forceinline__ RowTile selected_tile(const KvAttend &a, int x)
+{
+    const int per = (a.group + ROWS - 1) / ROWS, row = x / per, h0 = (x - row * per) * ROWS;
+    RowTile t = {};
+    t.seq = t.row0 = row;
+    t.n_new = 1;
+    if (row >= a.g.n_tokens || a.g.start[row] != row || a.g.start[row + 1] != row + 1) return t;
+    t.len = max(a.g.lens[row], 0);
+    t.rows = min(ROWS, a.group - h0);
+    t.rem0 = h0;
+    t.hi = min(t.len, cap_of(a.g));
+    return t;
+}
+
 // The row tile that workgroups of number z take: the last first, as later rows
 // see more tokens, and those of one parity before the others.  Row tiles with
 // nothing to do come at regular distances (every second where sequences fill
@@ -405,7 +423,7 @@ __device__ __forceinline__ void write_row(const KvAttend &a, const RowTile &t, i
 // Joins the chunks of rows: D/8 threads take eight dimensions each of a row,
 // in a.slices slices (a power of two) that take the chunks in turn and meet
 // in LDS.
-template <int D, int ROWS, class T>
+template <int D, int ROWS, class T, bool SELECTED = false>
 __global__ __launch_bounds__(256) void k_kv_join(KvAttend a)
 {
     constexpr int C = D / 8;
@@ -415,7 +433,7 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttend a)
     const int head = blockIdx.y, part = threadIdx.x / C, slice = part % a.slices;
     const int r = blockIdx.z * (256 / C / a.slices) + part / a.slices;
     const int2 at = a.target ? a.first[x] : make_int2((int)x * a.splits, a.chunk);
-    const RowTile t = row_tile<ROWS>(a, (int)x);
+    const RowTile t = SELECTED ? selected_tile<ROWS>(a, (int)x) : row_tile<ROWS>(a, (int)x);
     if (t.rows == 0) return;                                 // (and the first chunk's number is nobody's)
     // (where start decreases, a tile's chunks may not all have had a workgroup,
     // and what its first one's number would be is anything)
@@ -473,17 +491,23 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttend a)
     write_row<D, T>(a, t, head, r, d0, y, l, most);
 }
 
-template <int D, int ROWS, class T>
-hipError_t launch_join(const KvAttend &a, const KvPlan &p, hipStream_t s)
+template <int D, int ROWS, class T, bool SELECTED = false>
+hipError_t launch_join(const KvAttend &a, int64_t tiles, int64_t chunks, hipStream_t s)
 {
     constexpr int PARTS = 2048 / D;                          // rows times slices of a workgroup
     KvAttend b = a;
     b.slices = 1;
-    const int64_t chunks = p.target ? 2 * p.pieces / p.tiles : p.splits;      // a row tile's, about
     while (8 * b.slices < chunks && b.slices < PARTS) b.slices *= 2;
     const unsigned z = (ROWS + PARTS / b.slices - 1) / (PARTS / b.slices);
-    hipLaunchKernelGGL((k_kv_join<D, ROWS, T>), dim3((unsigned)p.tiles, b.g.kv_heads, z), dim3(256), 0, s, b);
+    hipLaunchKernelGGL((k_kv_join<D, ROWS, T, SELECTED>), dim3((unsigned)tiles, b.g.kv_heads, z), dim3(256), 0, s, b);
     return hipGetLastError();
+}
+
+// Of a plan: a row tile's chunks, about.
+template <int D, int ROWS, class T>
+hipError_t launch_join(const KvAttend &a, const KvPlan &p, hipStream_t s)
+{
+    return launch_join<D, ROWS, T>(a, p.tiles, p.target ? 2 * p.pieces / p.tiles : p.splits, s);
 }
 
 }  // namespace

@@ -1,7 +1,7 @@
 // kv_prompt.hip -- attention of many new tokens over the 4-bit key/value cache,
 // for heads of 64 and 128 (lw_kv_plan in kv_attend.hip says when).
 //
-// The mathematics is kv_attend.hip's.  There each wavefront unpacks the codes
+// The mathematics is kv_rows.hpp's.  There each wavefront unpacks the codes
 // that it uses, which for many query rows is most of its work: 152 of some 440
 // instructions for 32 tokens and 32 rows.  Here a workgroup has 128 rows of a
 // sequence, 32 for each wavefront, and goes through the tokens in tiles of 64:
@@ -28,11 +28,11 @@
 // 2048 tokens, where all are there from the start) are bound by those.
 //
 // Measured, bf16, 32 heads on 8 (replays of a graph; in brackets tiles of 32
-// rows of kv_attend.hip): heads of 128, 16384 tokens on themselves 3.28 ms, 670
+// rows of kv_rows.hpp): heads of 128, 16384 tokens on themselves 3.28 ms, 670
 // TFLOP/s (4.03 ms), 2048 on 16384 814 us, 633 (943), 2048 on themselves 89 us,
 // 386 (97); heads of 64, 2.15 ms, 511 (2.73), 614 us, 420 (645), and 78 us (68).
 //
-// Rounding: as in kv_attend.hip.  The second operand of p dv costs 24 % of the
+// Rounding: as in kv_rows.hpp.  The second operand of p dv costs 24 % of the
 // longest calls (3.28 ms and not 2.65) and 11 % of 2048 on themselves; without
 // it fp16 results lie 3.0e-4 of their size from 64 bits, with it 2.1e-4, which
 // is their own rounding.
@@ -147,7 +147,7 @@ struct Rows {
     h8 q[Tile<D>::PER];
     f16v o[NT];
     float qs, qsum;
-    float mo, ref, thr, dlim;    // offset, its reference, and what calls for a new one (kv_attend.hip)
+    float mo, ref, thr, dlim;    // offset, its reference, and what calls for a new one (kv_rows.hpp)
     float l, z;
 
     __device__ __forceinline__ float k() const { return (float)(7 + 127 - (int)(__builtin_bit_cast(uint32_t, dlim) >> 23)); }
@@ -220,7 +220,7 @@ __device__ __forceinline__ void step(Rows<D> &st, const Tile<D> &tile, int sub, 
     for (int a = 0; a < 4; a++)
 #pragma unroll
         for (int b = 0; b < 4; b++) top = fmaxf(top, s[a][b]);
-    if (__any(top > st.thr || dtop > st.dlim)) {             // rare: a new offset, as in kv_attend.hip
+    if (__any(top > st.thr || dtop > st.dlim)) {             // rare: a new offset, as in kv_rows.hpp
         top = fmaxf(top, __shfl_xor(top, 32));
         dtop = fmaxf(dtop, __shfl_xor(dtop, 32));
         const bool need = top > st.thr || dtop > st.dlim;

@@ -25,6 +25,9 @@ LW_FORM_PALETTE, LW_FORM_EXPONENT = 0, 1
 LW_CODE_HUFFMAN, LW_CODE_COMPACT, LW_CODE_LENS = 0, 1, 2
 LW_RECON_VARIANTS = 5
 LW_F16, LW_BF16, LW_F32 = range(3)
+LW_ROPE_HALVES, LW_ROPE_PAIRS = range(2)
+LW_ROPE_PLAIN, LW_ROPE_LINEAR, LW_ROPE_BASE, LW_ROPE_INDEX, LW_ROPE_TURNS = range(5)
+LW_ROPE_MOST = 256
 (LW_REG_TABLE, LW_REG_GPUTAB, LW_REG_TILE_OFF, LW_REG_WORDS, LW_REG_DM, LW_REG_PALETTE, LW_REG_SM,
  LW_REG_VB_BITS, LW_REG_VB_START, LW_REG_VERBATIM, LW_REG_SPLIT, LW_REG_WORK, LW_REG_COUNT) = range(13)
 
@@ -62,6 +65,22 @@ class lw_kv_batch(C.Structure):
 
 class lw_kv_tensor(C.Structure):
     _fields_ = [("data", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
+class lw_rope_opts(C.Structure):
+    _fields_ = [("pairs", C.c_int32), ("layout", C.c_int32), ("scaling", C.c_int32), ("amplitude", C.c_float),
+                ("base", C.c_double), ("factor", C.c_double), ("original", C.c_double), ("low", C.c_double),
+                ("high", C.c_double)]
+
+
+class lw_rope_plan(C.Structure):
+    _fields_ = [("step", C.c_uint64 * LW_ROPE_MOST), ("amplitude", C.c_float), ("pairs", C.c_int32),
+                ("layout", C.c_int32)]
+
+
+class lw_kv_selection(C.Structure):
+    _fields_ = [("n_tokens", C.c_int64), ("start", C.c_void_p), ("lens", C.c_void_p), ("table", C.c_void_p),
+                ("pages", C.c_int64)]
 
 
 def _load():
@@ -114,6 +133,16 @@ def _load():
         "lw_kv_read": (st, [P, P, i64, P, P, i32, P]),
         "lw_kv_attend": (st, [P, P, i64, P, P, i32, i32, C.c_float, i32, i32, P, P, C.c_size_t, P]),
         "lw_kv_attend_scratch_bytes": (C.c_size_t, [P, P, i64, i32]),
+        "lw_rope_make": (st, [P, P]),
+        "lw_rope": (st, [P, P, P, i64, i32, i32, P, i32, P, i32, P]),
+        "lw_kv_bounds_bytes": (C.c_size_t, [i32, i32]),
+        "lw_kv_bounds": (st, [P, P, i64, P, P]),
+        "lw_kv_select": (st, [P, P, P, i32, i32, P, i32, i32, P, P, C.c_size_t, P]),
+        "lw_kv_select_scratch_bytes": (C.c_size_t, [P, P, i64, i32]),
+        "lw_kv_attend_selected": (st, [P, P, P, P, i32, i32, C.c_float, P, P, C.c_size_t, P]),
+        "lw_kv_attend_selected_scratch_bytes": (C.c_size_t, [P, P, i32]),
+        "lw_kv_weigh": (st, [P, P, i64, P, i32, i32, C.c_float, i32, i32, P, P, C.c_float, P, i64, P]),
+        "lw_kv_evict": (st, [P, P, P, i64, i64, i32, i32, P, P, P, P]),
         "lw_status_str": (C.c_char_p, [st]),
         "lw_last_error": (C.c_char_p, []),
     }
@@ -600,6 +629,179 @@ def lw_kv_attend(cache: KvCache, batch: KvBatch, q, out, scale: float | None = N
     st = _L.lw_kv_attend(cache.ref, batch.ref, n, C.byref(tq), C.byref(to), _kv_type(q), heads,
                          cache.head_dim ** -0.5 if scale is None else scale, causal, window, pl, wp, wn,
                          _stream(stream))
+    if st:
+        _check(st)
+
+
+# ---------------------------------------------------------------- rotary positions
+
+class RopePlan:
+    """A worked out lw_rope_plan."""
+
+    def __init__(self, desc: lw_rope_plan):
+        self.desc = desc
+        self.ref = C.byref(desc)
+
+
+def lw_rope_make(pairs: int, layout: int = LW_ROPE_HALVES, base: float = 10000.0, scaling: int = LW_ROPE_PLAIN,
+                 factor: float = 1.0, original: float = 0.0, low: float = 1.0, high: float = 32.0,
+                 amplitude: float = 1.0) -> RopePlan:
+    opts = lw_rope_opts(pairs, layout, scaling, amplitude, base, factor, original, low, high)
+    plan = lw_rope_plan()
+    _check(_L.lw_rope_make(C.byref(opts), C.byref(plan)))
+    return RopePlan(plan)
+
+
+def _rope_tensor(t, what: str, like=None):
+    try:
+        shape, (s0, s1, s2), ok = t.shape, t.stride(), t.is_cuda
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok or (s2 != 1 and shape[2] != 1):
+        raise LwError(LW_E_ARG, f"{what} must be a device tensor [tokens][heads][head_dim] with contiguous head vectors")
+    if like is not None and shape != like.shape:
+        raise LwError(LW_E_ARG, f"{what} must have the shape of the tensor before it")
+    return lw_kv_tensor(t.data_ptr(), s0, s1)
+
+
+def lw_rope(plan: RopePlan, x, y, batch: KvBatch | None = None, pos=None, stream=None) -> None:
+    """y = x [n][heads][head_dim] turned by the rows' positions: those of the batch's tokens, or pos (int32 [n])."""
+    import torch
+    tx = _rope_tensor(x, "x")
+    ty = _rope_tensor(y, "y", x)
+    pp = None
+    if pos is not None:
+        pp = _dptr(pos, "pos")
+        if pos.dtype != torch.int32 or pos.numel() != x.shape[0]:
+            raise LwError(LW_E_ARG, "pos must be int32 [tokens]")
+    st = _L.lw_rope(plan.ref, batch.ref if batch is not None else None, pp, x.shape[0], x.shape[1], x.shape[2],
+                    C.byref(tx), _kv_type(x), C.byref(ty), _kv_type(y), _stream(stream))
+    if st:
+        _check(st)
+
+
+# ---------------------------------------------------------------- a few pages of a long cache
+
+def lw_kv_bounds_bytes(kv_heads: int, head_dim: int) -> int:
+    """Bytes of one page's bounds (0: not supported)."""
+    return int(_L.lw_kv_bounds_bytes(kv_heads, head_dim))
+
+
+def _bounds(bounds, cache):
+    p = _dptr(bounds, "bounds")
+    if bounds.numel() * bounds.element_size() < cache.n_pages * lw_kv_bounds_bytes(cache.kv_heads, cache.head_dim):
+        raise LwError(LW_E_ARG, "bounds must hold lw_kv_bounds_bytes for each page of the cache")
+    return p
+
+
+class KvSelection:
+    """The pages that n new tokens attend over: device int32 tensors start [n + 1], lens [n] and
+    table [n][kv_heads][pages], which lw_kv_select fills."""
+
+    def __init__(self, start, lens, table):
+        import torch
+        ps, pl, pt = _dptr(start, "start"), _dptr(lens, "lens"), _dptr(table, "table")
+        if any(t.dtype != torch.int32 for t in (start, lens, table)):
+            raise LwError(LW_E_ARG, "start, lens and table must be int32")
+        n = lens.numel()
+        if start.numel() != n + 1 or table.dim() != 3 or table.shape[0] != n:
+            raise LwError(LW_E_ARG, "start must hold one entry more than lens, table [kv_heads][pages] for each")
+        self.start, self.lens, self.table = start, lens, table
+        self.n, self.kv_heads = n, table.shape[1]
+        self.desc = lw_kv_selection(n, ps, pl, pt, table.shape[2])
+        self.ref = C.byref(self.desc)
+
+
+def _rows(t, what, sel, cache):
+    tensor = _kv_tensor(t, what, cache)
+    if t.shape[0] != sel.n or sel.kv_heads != cache.kv_heads:
+        raise LwError(LW_E_ARG, f"the selection must have {what}'s rows and the cache's heads")
+    return tensor
+
+
+def lw_kv_bounds(cache: KvCache, batch: KvBatch, n_tokens: int, bounds, stream=None) -> None:
+    """Bounds of the pages that the batch's n_tokens new tokens have filled."""
+    st = _L.lw_kv_bounds(cache.ref, batch.ref, n_tokens, _bounds(bounds, cache), _stream(stream))
+    if st:
+        _check(st)
+
+
+def lw_kv_select_scratch_bytes(cache: KvCache, batch: KvBatch, n_tokens: int, q_heads: int) -> int:
+    return int(_L.lw_kv_select_scratch_bytes(cache.ref, batch.ref, n_tokens, q_heads))
+
+
+def lw_kv_select(cache: KvCache, batch: KvBatch, q, bounds, sel: KvSelection, first: int = 1, last: int = 1, work=None,
+                 stream=None) -> None:
+    """Choose sel's pages for the rows of q [n][q_heads][head_dim]."""
+    tq = _rows(q, "q", sel, cache)
+    wp, wn = _wbuf(work if work is not None and work.numel() else None)
+    st = _L.lw_kv_select(cache.ref, batch.ref, C.byref(tq), _kv_type(q), q.shape[1], _bounds(bounds, cache), first, last,
+                         sel.ref, wp, wn, _stream(stream))
+    if st:
+        _check(st)
+
+
+def lw_kv_attend_selected_scratch_bytes(cache: KvCache, sel: KvSelection, q_heads: int) -> int:
+    return int(_L.lw_kv_attend_selected_scratch_bytes(cache.ref, sel.ref, q_heads))
+
+
+def _lse(lse, q):
+    p = _dptr(lse, "lse")
+    if lse.shape != q.shape[:2] or (_KV_TYPES or _kv_types()).get(lse.dtype) != LW_F32:
+        raise LwError(LW_E_ARG, "lse must be fp32 [tokens][q_heads]")
+    return p
+
+
+def lw_kv_attend_selected(cache: KvCache, sel: KvSelection, q, out, scale: float | None = None, lse=None, work=None,
+                          stream=None) -> None:
+    """out = attention of q [n][q_heads][head_dim] over the selected pages; scale None: head_dim ** -0.5."""
+    tq = _rows(q, "q", sel, cache)
+    to = _kv_tensor(out, "out", cache, q)
+    pl = _lse(lse, q) if lse is not None else None
+    wp, wn = _wbuf(work if work is not None and work.numel() else None)
+    st = _L.lw_kv_attend_selected(cache.ref, sel.ref, C.byref(tq), C.byref(to), _kv_type(q), q.shape[1],
+                                  cache.head_dim ** -0.5 if scale is None else scale, pl, wp, wn, _stream(stream))
+    if st:
+        _check(st)
+
+
+# ---------------------------------------------------------------- pages given up
+
+def _weights(t, what, cache, batch):
+    p = _dptr(t, what)
+    if (t.dim() != 3 or t.shape[:2] != (batch.lens.numel(), cache.kv_heads)
+            or (_KV_TYPES or _kv_types()).get(t.dtype) != LW_F32):
+        raise LwError(LW_E_ARG, f"{what} must be fp32 [sequences][kv_heads][pages]")
+    return p
+
+
+def lw_kv_weigh(cache: KvCache, batch: KvBatch, q, lse, weights, before=None, decay: float = 1.0,
+                scale: float | None = None, causal: bool = True, window: int = 0, stream=None) -> None:
+    """weights [sequences][kv_heads][pages] = decay * before + what the rows of q gave to the pages' tokens."""
+    tq = _kv_tensor(q, "q", cache)
+    pw, pb = _weights(weights, "weights", cache, batch), None
+    if before is not None:
+        pb = _weights(before, "before", cache, batch)
+        if before.shape != weights.shape:
+            raise LwError(LW_E_ARG, "before must have the shape of weights")
+    st = _L.lw_kv_weigh(cache.ref, batch.ref, q.shape[0], C.byref(tq), _kv_type(q), q.shape[1],
+                        cache.head_dim ** -0.5 if scale is None else scale, causal, window, _lse(lse, q), pb, decay, pw,
+                        weights.shape[2], _stream(stream))
+    if st:
+        _check(st)
+
+
+def lw_kv_evict(cache: KvCache, batch: KvBatch, weights, keep: int, table, gone, count, first: int = 1, last: int = 1,
+                stream=None) -> None:
+    """Give up each sequence's pages of least weight until keep are left: table (batch's shape; may be its own) gets
+    -1 for them, gone their numbers, count how many."""
+    import torch
+    pw = _weights(weights, "weights", cache, batch)
+    ps = [_dptr(t, what) for t, what in ((table, "table"), (gone, "gone"), (count, "count"))]
+    if (any(t.dtype != torch.int32 for t in (table, gone, count)) or table.shape != batch.table.shape
+            or gone.shape != batch.table.shape or count.numel() != batch.lens.numel()):
+        raise LwError(LW_E_ARG, "table and gone must be int32 of the batch's table's shape, count int32 [sequences]")
+    st = _L.lw_kv_evict(cache.ref, batch.ref, pw, weights.shape[2], keep, first, last, *ps, _stream(stream))
     if st:
         _check(st)
 

@@ -510,6 +510,191 @@ lw_status lw_kv_attend(const lw_kv_cache *cache, const lw_kv_batch *batch, int64
  * chunk a sequence does for all of them, or for arguments that it refuses). */
 size_t lw_kv_attend_scratch_bytes(const lw_kv_cache *cache, const lw_kv_batch *batch, int64_t n_tokens, int q_heads);
 
+/* ---------------------------------------------------------------- rotary positions */
+/* Queries and keys turned by their position before the cache takes them: pair
+ * i of `pairs` by the angle pos * f_i,
+ *   (a, b) -> g (a cos - b sin, a sin + b cos),  g the amplitude
+ * and the dimensions past 2 pairs stay as they are.  f_i = base^(-i / pairs),
+ * and for contexts longer than the `original` one: */
+typedef enum { LW_ROPE_HALVES = 0,     /* pair i: dimensions i and i + pairs */
+               LW_ROPE_PAIRS = 1       /* pair i: dimensions 2i and 2i + 1 */
+} lw_rope_layout;
+
+typedef enum {
+    LW_ROPE_PLAIN = 0,         /* f */
+    LW_ROPE_LINEAR = 1,        /* f / factor */
+    LW_ROPE_BASE = 2,          /* base factor^(pairs / (pairs - 1)) in the base's place (pairs >= 2) */
+    LW_ROPE_INDEX = 3,         /* f (1 - r + r / factor), r = (i - lo) / (hi - lo) within 0..1, lo = floor(at(high)) and
+                                  hi = ceil(at(low)) within 0..2 pairs - 1 (hi 0.001 more where they are equal), at(t) =
+                                  pairs ln(original / (2 pi t)) / ln(base): the pairs that turn `high` times over the
+                                  original context keep their pace, those that turn `low` times take factor's */
+    LW_ROPE_TURNS = 4          /* f (s + (1 - s) / factor), s = (original f / (2 pi) - low) / (high - low) within 0..1 */
+} lw_rope_scaling;
+
+enum { LW_ROPE_MOST = 256 };           /* pairs, at most */
+
+typedef struct {
+    int32_t pairs;             /* 1..LW_ROPE_MOST */
+    int32_t layout;            /* lw_rope_layout */
+    int32_t scaling;           /* lw_rope_scaling */
+    float amplitude;           /* g, finite (1: rotation alone) */
+    double base;               /* 1..2^64 (INDEX: above 1) */
+    double factor;             /* 2^-64..2^64 (PLAIN: not looked at) */
+    double original;           /* INDEX, TURNS: positive, at most 2^64 */
+    double low, high;          /* INDEX: positive; TURNS: low < high, low not negative; both at most 2^64 */
+} lw_rope_opts;
+
+/* What lw_rope needs to know: plain data, to be kept and copied as one likes.
+ * step[i] is f_i / (2 pi), in units of 2^-64 turns. */
+typedef struct {
+    uint64_t step[LW_ROPE_MOST];
+    float amplitude;
+    int32_t pairs, layout;
+} lw_rope_plan;
+
+/* Work out a plan.  Errors: LW_E_ARG. */
+lw_status lw_rope_make(const lw_rope_opts *opts, lw_rope_plan *plan);
+
+/* y = x turned, for n_tokens rows of `heads` head vectors of head_dim elements
+ * (lw_kv_tensor's strides; LW_F16, LW_BF16 or LW_F32 each), in fp32, rounded
+ * once to y's type.  Row i is at position pos[i], or where pos is NULL at its
+ * place in the batch (lens[s] - n + i, as the cache has it; table is not
+ * looked at, and rows that belong to no sequence are left as they are).
+ * Positions are any int32; negative ones turn back.  Angles are worked out in
+ * whole 2^-64 turns: far positions are as exact as near ones.
+ *   head_dim : 2 * pairs..1024
+ *   heads    : 1..65536
+ *   batch    : NULL where pos is given
+ *   y        : may be x (the same data, strides and type); may not overlap it
+ *              otherwise, nor itself (a stride of 0 for more than one)
+ * Errors: LW_E_ARG, LW_E_DEVICE. */
+lw_status lw_rope(const lw_rope_plan *plan, const lw_kv_batch *batch, const int32_t *pos, int64_t n_tokens, int heads,
+                  int head_dim, const lw_kv_tensor *x, int x_dtype, const lw_kv_tensor *y, int y_dtype, void *stream);
+
+/* ---------------------------------------------------------------- a few pages of a long cache */
+/* Attention over a few of a sequence's pages, chosen for each new token and kv
+ * head by a score that costs a fraction of reading the keys.
+ *
+ * Bounds: of a full page's P keys of a head (as lw_kv_read gives them in fp32)
+ * each channel's largest hi and smallest lo, and e, the smallest whole number
+ * with all |hi|, |lo| <= 127 * 2^e (0 where they are 0).  A page's bounds are
+ * lw_kv_bounds_bytes at page * lw_kv_bounds_bytes: for each head D bytes
+ * ceil(hi 2^-e) and D bytes floor(lo 2^-e), signed, then the heads' e (int32),
+ * padded to 16 bytes.  A page with a key that is not finite has zeros and
+ * e = 127 there.
+ *
+ * Scores: a query head vector x counts as the whole numbers rint(x 2^-e), e as
+ * above (as zeros where it has a NaN or an infinity); its score for a page is
+ *   sum_d max(x_d hi_d, x_d lo_d) * 2^max(e - top, -64) * 2^(the page's e),
+ * top the largest e of the kv head's query heads (that are not zero): a bound of
+ * q.k over the page's keys, but for the rounding of q.  A page's score is the
+ * largest of the query heads', +infinity where its e is 127.  Whole numbers below
+ * 2^22 times powers of two: exact, so that what is selected is defined to the bit. */
+
+/* Bytes of one page's bounds, or 0 where the cache kind is not supported. */
+size_t lw_kv_bounds_bytes(int kv_heads, int head_dim);
+
+/* Bounds of the pages that the batch's new tokens have filled: those whose
+ * last token is one of the sequence's lens[s] and which hold a new one.  To be
+ * called after lw_kv_append with the same batch (pages of a sequence that has
+ * been cut back and goes on are bounded anew when they are full again).
+ *   bounds : device, 16-byte aligned, n_pages * lw_kv_bounds_bytes
+ * Errors: LW_E_ARG, LW_E_UNSUPPORTED (head_dim, page_tokens), LW_E_DEVICE. */
+lw_status lw_kv_bounds(const lw_kv_cache *cache, const lw_kv_batch *batch, int64_t n_tokens, void *bounds,
+                       void *stream);
+
+/* The pages that n_tokens new tokens attend over.  A row of a sequence has
+ * start[i] = i, start[i+1] = i + 1, one that belongs to none has them equal;
+ * its tokens are numbered along its pages, lens[i] of them in all, and
+ * table[i][g] are kv head g's pages in the order of their positions, `pages`
+ * entries, -1 past the last. */
+typedef struct {
+    int64_t n_tokens;
+    int32_t *start;            /* device [n_tokens + 1] */
+    int32_t *lens;             /* device [n_tokens] */
+    int32_t *table;            /* device [n_tokens][kv_heads][pages] */
+    int64_t pages;             /* 1..32768 */
+} lw_kv_selection;
+
+/* Choose the pages of sel->n_tokens new tokens (rows of q, [n][q_heads][D],
+ * LW_F16 or LW_BF16).  A row at position p takes the page of p (last, absent
+ * or not), and of its sequence's pages before that which are present: the
+ * first `first`, the last `last`, and of the others those of the highest
+ * scores, of equal ones that of the lowest position, until it has sel->pages.
+ * Pages before p's count as full: their bounds have to be there.
+ *   first, last : not negative, first + last < sel->pages
+ *   work        : device, 4-byte aligned, lw_kv_select_scratch_bytes bytes
+ *                 (NULL/0 where that is 0), contents not kept between calls;
+ *                 with less, scores of long sequences take longer
+ * A sequence may have up to 32768 pages (batch->table_stride).
+ * Errors: LW_E_ARG, LW_E_UNSUPPORTED (head_dim, page_tokens, dtype,
+ * table_stride), LW_E_DEVICE. */
+lw_status lw_kv_select(const lw_kv_cache *cache, const lw_kv_batch *batch, const lw_kv_tensor *q, int dtype, int q_heads,
+                       const void *bounds, int first, int last, const lw_kv_selection *sel, void *work,
+                       size_t work_bytes, void *stream);
+
+/* Bytes of work that lw_kv_select wants for these (0 where it needs none, or
+ * for arguments that it refuses). */
+size_t lw_kv_select_scratch_bytes(const lw_kv_cache *cache, const lw_kv_batch *batch, int64_t n_tokens, int q_heads);
+
+/* lw_kv_attend of sel->n_tokens rows over the pages that lw_kv_select chose:
+ * each sees all tokens of its kv head's pages up to its own.  q, out, dtype,
+ * q_heads, scale, lse, and what a row that sees nothing gets, as there; rows
+ * that belong to no sequence are left as they are.
+ *   work : device, 16-byte aligned, lw_kv_attend_selected_scratch_bytes bytes
+ *          (NULL/0 where that is 0), contents not kept between calls; with
+ *          less, rows are cut into fewer chunks
+ * Errors: LW_E_ARG, LW_E_UNSUPPORTED (head_dim, page_tokens, dtype),
+ * LW_E_DEVICE. */
+lw_status lw_kv_attend_selected(const lw_kv_cache *cache, const lw_kv_selection *sel, const lw_kv_tensor *q,
+                                const lw_kv_tensor *out, int dtype, int q_heads, float scale, float *lse, void *work,
+                                size_t work_bytes, void *stream);
+size_t lw_kv_attend_selected_scratch_bytes(const lw_kv_cache *cache, const lw_kv_selection *sel, int q_heads);
+
+/* ---------------------------------------------------------------- pages given up */
+/* Which of a sequence's pages the attention of its tokens needs least, and
+ * giving those up: an absent page costs nothing and is not seen.
+ *
+ * lw_kv_weigh: the attention weight that the batch's rows gave to each page,
+ *   weights[s][g][j] = decay * before[s][g][j] + sum exp(scale q.k - lse)
+ * over the rows of sequence s, the query heads of kv head g and the tokens of
+ * page j that a row sees (causal and window as in lw_kv_attend, whose log sums
+ * lse are; a row whose log sum is not finite adds nothing).
+ *   q       : [n_tokens][q_heads][D], LW_F16 or LW_BF16
+ *   lse     : fp32 [n_tokens][q_heads]
+ *   before  : fp32 [n_seqs][kv_heads][stride], may be weights itself, or NULL
+ *             (nothing before)
+ *   weights : the same shape; written for the sequences with new tokens, pages
+ *             j < stride that hold one of their lens[s] tokens (0 where the
+ *             page is absent); the others keep what they have
+ *   decay   : 0..1 (with 0 before is not read)
+ * Weights are fp32 sums in a fixed order: results are deterministic.
+ * Errors: LW_E_ARG, LW_E_UNSUPPORTED (head_dim, page_tokens, dtype),
+ * LW_E_DEVICE. */
+lw_status lw_kv_weigh(const lw_kv_cache *cache, const lw_kv_batch *batch, int64_t n_tokens, const lw_kv_tensor *q,
+                      int dtype, int q_heads, float scale, int causal, int window, const float *lse,
+                      const float *before, float decay, float *weights, int64_t stride, void *stream);
+
+/* Give up pages of every sequence (start is not looked at) until `keep` are
+ * left: of those present that hold one of its lens[s] tokens, without the
+ * first `first` and the last `last`, the ones of the lowest weight, of equal
+ * ones that of the lowest position.  A page's weight is the sum of its heads',
+ * in 64 bits and in order, rounded to 32; NaN counts as the largest, and pages
+ * j >= stride as the largest, too.  What cannot be spared stays, so that more
+ * than keep may be left.
+ *   keep, first : not negative; last : at least 1 (the page being filled)
+ *   weights     : fp32 [n_seqs][kv_heads][stride]
+ *   table       : device int32 [n_seqs][batch->table_stride], overwritten with
+ *                 batch's, -1 where a page is given up; may be batch's itself
+ *   gone        : device int32 [n_seqs][batch->table_stride]: the pages given
+ *                 up, in the order of their positions, then -1
+ *   count       : device int32 [n_seqs]: how many
+ * A sequence may have up to 32768 pages (batch->table_stride).
+ * Errors: LW_E_ARG, LW_E_UNSUPPORTED (head_dim, page_tokens, table_stride),
+ * LW_E_DEVICE. */
+lw_status lw_kv_evict(const lw_kv_cache *cache, const lw_kv_batch *batch, const float *weights, int64_t stride,
+                      int64_t keep, int first, int last, int32_t *table, int32_t *gone, int32_t *count, void *stream);
+
 /* ---------------------------------------------------------------- pipelines */
 /* "Unweight", sections "Four approaches to using compressed weights" and
  * "Why no single pipeline wins": full decode rebuilds every bf16 weight in
