@@ -2,10 +2,12 @@
 // first, and the places of those taken in ascending order.  Internal to the
 // library.
 //
-// The key that divides them is found from its highest byte on: a histogram of
-// the keys that share the bytes found so far, and the byte in which the count
-// from above passes m.  Sums and counts are whole numbers, so that the order in
-// which the counters are reached does not matter.
+// The key that divides them is found from its highest 11 bits on: a histogram of
+// the keys that share the bits found so far, and the counter in which the count
+// from above passes m.  Keys count from the smallest on and are moved up as far
+// as the largest allows: they then spread over the counters (64 lanes that reach
+// for one of them take turns), and the first 11 bits mostly do.  Counts are whole
+// numbers, so that the order in which lanes add does not matter.
 #ifndef LW_KV_PICK_HPP
 #define LW_KV_PICK_HPP
 
@@ -15,11 +17,22 @@ namespace {
 
 constexpr int PICK_MOST = 32768;       // keys (their counts fit 16 bits)
 
-// Taken are keys with (key & mask) > value, and of those where it is value the
-// first `ties`.
+// Keys are 0 (never taken), MUST (always) or between.  They come in fours, with
+// zeros after the last one.
+constexpr uint32_t MUST = ~0u;
+
+// What a workgroup's keys are, of the last two those between.
+struct Keys {
+    uint32_t there, must, least, most;
+};
+
+// Taken are those between whose place y = (key - least) << up has
+// (y & mask) > value, and of those where it is value the first `ties`.
 struct Cut {
-    uint32_t mask, value;
+    uint32_t least, up, mask, value;
     int ties;
+
+    __device__ __forceinline__ uint32_t place(uint32_t key) const { return (key - least) << up & mask; }
 };
 
 // fp32 numbers as whole numbers in the same order; above 0 for all but NaN with
@@ -30,58 +43,147 @@ __device__ __forceinline__ uint32_t ordered(float x)
     return u >> 31 ? ~u : u | 0x80000000u;
 }
 
-// The cut that takes m of n keys, 1 <= m <= n.  hist: 512 counters in LDS.
-// Begins with a barrier: the keys are then there.
+template <class F>
+__device__ __forceinline__ void each_of(uint4 x, F f)
+{
+    const uint32_t k[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int j = 0; j < 4; j++) f(j, k[j]);
+}
+
+// The largest of x over the lanes up to this one (prefix() has the steps).
+__device__ __forceinline__ uint32_t prefix_max(uint32_t x)
+{
+    auto with = [&](auto ctrl, auto rows) {
+        x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, ctrl.value, rows.value, 0xF, true));
+    };
+    using std::integral_constant;
+    with(integral_constant<int, 0x111>{}, integral_constant<int, 0xF>{});
+    with(integral_constant<int, 0x112>{}, integral_constant<int, 0xF>{});
+    with(integral_constant<int, 0x114>{}, integral_constant<int, 0xF>{});
+    with(integral_constant<int, 0x118>{}, integral_constant<int, 0xF>{});
+    with(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});
+    with(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});
+    return x;
+}
+
+// A number of each thread's, summed over the workgroup.  sums: T / 64 words of
+// LDS.
 template <int T>
-__device__ __forceinline__ Cut pick_cut(const uint32_t *key, int n, int m, uint32_t *hist)
+__device__ __forceinline__ uint32_t sum_of(uint32_t x, uint32_t *sums)
+{
+    x = prefix(x);
+    if ((threadIdx.x & 63) == 63) sums[threadIdx.x >> 6] = x;
+    __syncthreads();
+    uint32_t all = 0;
+#pragma unroll
+    for (int w = 0; w < T / 64; w++) all += sums[w];
+    return all;
+}
+
+// Of `quads` times four keys in LDS.  sums: 4 * T / 64 words of LDS.  The keys are
+// there after a barrier.
+template <int T>
+__device__ __forceinline__ Keys look_at(const uint32_t *key, int quads, uint32_t *sums)
 {
     const int lane = threadIdx.x & 63;
-    Cut c = {0, 0, m};
-    if (threadIdx.x < 256) hist[threadIdx.x] = 0;
+    uint32_t counts = 0, least = ~0u, most = 0;              // there, and << 16 those that must (at most 2^15)
+#pragma unroll 2
+    for (int i = threadIdx.x; i < quads; i += T)
+        each_of(reinterpret_cast<const uint4 *>(key)[i], [&](int, uint32_t k) {
+            counts += k == 0 ? 0u : k == MUST ? 0x10001u : 1u;
+            least = k == 0 ? least : min(least, k);
+            most = k == MUST ? most : max(most, k);
+        });
+    counts = prefix(counts);
+    least = ~prefix_max(~least);
+    most = prefix_max(most);
+    if (lane == 63) *reinterpret_cast<uint4 *>(sums + 4 * (threadIdx.x >> 6)) = make_uint4(counts, least, most, 0);
+    __syncthreads();
+    Keys r = {0, 0, ~0u, 0};
 #pragma unroll
-    for (int pass = 0; pass < 4; pass++) {
-        const int shift = 24 - 8 * pass;
-        uint32_t *h = hist + pass % 2 * 256, *next = hist + (pass + 1) % 2 * 256;
+    for (int w = 0; w < T / 64; w++) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(sums + 4 * w);
+        r.there += x.x & 0xFFFFu;
+        r.must += x.x >> 16;
+        r.least = min(r.least, x.y);
+        r.most = max(r.most, x.z);
+    }
+    return r;
+}
+
+// Histograms have 2048 counters, 32 and four words of padding in a row (64 lanes
+// that read a row each then meet no bank twice).  There are two, used in turn,
+// and two numbers that a wavefront leaves for the others.
+constexpr int PICK_ROW = 36, PICK_HIST = 64 * PICK_ROW, PICK_WORDS = 2 * PICK_HIST + 4;
+
+// The cut that takes all that must be and so many of the others that they are m
+// (fewer than there are).  hist: PICK_WORDS of LDS; it and the keys are 16-byte
+// aligned.  One wavefront looks for the counter (all of a large workgroup doing
+// so took longer than the barrier after it).
+template <int T>
+__device__ __forceinline__ Cut pick_cut(const uint32_t *key, int quads, Keys all, int m, uint32_t *hist)
+{
+    constexpr int BITS[3] = {11, 11, 10}, SHIFT[3] = {21, 10, 0};
+    const int lane = threadIdx.x & 63;
+    Cut c = {all.least, 0, 0, 0, m - (int)all.must};
+    if (c.ties <= 0) return {0, 0, ~0u, ~0u, 0};             // (none of them)
+    c.up = __builtin_clz(max(all.most - all.least, 1u));
+    for (int i = threadIdx.x; i < PICK_HIST; i += T) hist[i] = 0;
+#pragma unroll
+    for (int pass = 0; pass < 3; pass++) {
+        uint32_t *h = hist + pass % 2 * PICK_HIST, *next = hist + (pass + 1) % 2 * PICK_HIST;
+        uint2 *found = reinterpret_cast<uint2 *>(hist + 2 * PICK_HIST);
         __syncthreads();
-        for (int i = threadIdx.x; i < n; i += T) {
-            const uint32_t k = key[i];
-            if ((k & c.mask) == c.value) atomicAdd(&h[k >> shift & 255u], 1u);
+#pragma unroll 2
+        for (int i = threadIdx.x; i < quads; i += T)
+            each_of(reinterpret_cast<const uint4 *>(key)[i], [&](int, uint32_t k) {
+                const uint32_t x = (k - c.least) << c.up >> SHIFT[pass] & ((1u << BITS[pass]) - 1);
+                if (k - 1 < MUST - 1 && c.place(k) == c.value) atomicAdd(&h[x / 32 * PICK_ROW + x % 32], 1u);
+            });
+        __syncthreads();
+        if (threadIdx.x < 64) {
+            // rows from the last on, one a lane, then the counters of one row
+            const uint4 *row = reinterpret_cast<const uint4 *>(h + (63 - lane) * PICK_ROW);
+            int own = 0;
+#pragma unroll
+            for (int i = 0; i < 8; i++) own += (int)(row[i].x + row[i].y + row[i].z + row[i].w);
+            const int sum = prefix(own), r = __popcll(__ballot(sum < c.ties));
+            const int above = r ? __builtin_amdgcn_readlane(sum, r - 1) : 0;
+            const int in = lane < 32 ? (int)h[(63 - r) * PICK_ROW + 31 - lane] : 0, upto = above + prefix(in);
+            const int i = __popcll(__ballot(upto < c.ties));
+            // what the counter has, and what is taken of it; the counter
+            if (lane == i) *found = make_uint2((uint32_t)in << 16 | (uint32_t)(c.ties - (upto - in)), (63 - r) * 32 + 31 - i);
+        } else {
+            for (int i = threadIdx.x - 64; i < PICK_HIST; i += T - 64) next[i] = 0;       // (last read before the barrier above)
         }
         __syncthreads();
-        if (threadIdx.x < 256) next[threadIdx.x] = 0;        // (last read before the barrier above)
-        // bins 255 - 4 lane and the three below it
-        const uint4 b = *reinterpret_cast<const uint4 *>(h + 252 - 4 * lane);
-        const int own[4] = {(int)b.w, (int)b.z, (int)b.y, (int)b.x};
-        const int sum = prefix(own[0] + own[1] + own[2] + own[3]);
-        const int at = __popcll(__ballot(sum < c.ties));     // the lane whose bins the count passes in
-        int above = at ? __builtin_amdgcn_readlane(sum, at - 1) : 0, bin = 255 - 4 * at, in = 0;
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            in = __builtin_amdgcn_readlane(own[i], at);
-            if (above + in >= c.ties) break;
-            above += in;
-            bin--;
-        }
-        c.ties -= above;
-        c.mask |= 0xFFu << shift;
-        c.value |= (uint32_t)bin << shift;
-        if (in == c.ties) break;                             // all that share the bytes are taken
+        const uint2 f = *found;
+        c.ties = (int)(f.x & 0xFFFFu);
+        c.mask |= ((1u << BITS[pass]) - 1) << SHIFT[pass];
+        c.value |= f.y << SHIFT[pass];
+        if (f.x >> 16 == (uint32_t)c.ties) break;            // all that share the bits are taken
     }
     return c;
 }
 
-// put(place, rank) for each key taken, rank by rank; returns their number.
-// sums: T / 64 counters in LDS.
+// put(place, rank) for each key taken (all that are there where `every`), rank by
+// rank; returns their number.  sums: T / 64 words of LDS.
 template <int T, class F>
-__device__ __forceinline__ int pick_each(const uint32_t *key, int n, Cut c, uint32_t *sums, F put)
+__device__ __forceinline__ int pick_each(const uint32_t *key, int quads, bool every, Cut c, uint32_t *sums, F put)
 {
-    const int each = (n + T - 1) / T, i0 = min((int)threadIdx.x * each, n), i1 = min(i0 + each, n);
+    const int each = (quads + T - 1) / T, i0 = min((int)threadIdx.x * each, quads), i1 = min(i0 + each, quads);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint32_t mine = 0;                                       // above the cut, and on it << 16
-    for (int i = i0; i < i1; i++) {
-        const uint32_t k = key[i] & c.mask;
-        mine += k > c.value ? 1u : k == c.value ? 0x10000u : 0u;
-    }
+    uint32_t mine = 0;                                       // taken for sure, and on the cut << 16
+    auto four = [&](int i, auto f) {
+        each_of(reinterpret_cast<const uint4 *>(key)[i], [&](int j, uint32_t k) {
+            const uint32_t y = c.place(k);
+            const bool is = k != 0 && (every || k == MUST || y > c.value);
+            f(4 * i + j, is, k != 0 && !is && y == c.value);
+        });
+    };
+#pragma unroll 2
+    for (int i = i0; i < i1; i++) four(i, [&](int, bool is, bool tie) { mine += is ? 1u : tie ? 0x10000u : 0u; });
     const uint32_t upto = prefix(mine);
     if (lane == 63) sums[wave] = upto;
     __syncthreads();
@@ -91,13 +193,14 @@ __device__ __forceinline__ int pick_each(const uint32_t *key, int n, Cut c, uint
         if (w < wave) before += sums[w];
         all += sums[w];
     }
-    int above = before & 0xFFFFu, on = before >> 16;
-    for (int i = i0; i < i1; i++) {
-        const uint32_t k = key[i] & c.mask;
-        const bool is = k > c.value, tie = k == c.value;
-        if (is || (tie && on < c.ties)) put(i, above + min(on, c.ties));
-        above += is;
-        on += tie;
+    if (mine) {
+        int above = before & 0xFFFFu, on = before >> 16;
+        for (int i = i0; i < i1; i++)
+            four(i, [&](int place, bool is, bool tie) {
+                if (is || (tie && on < c.ties)) put(place, above + min(on, c.ties));
+                above += is;
+                on += tie;
+            });
     }
     return (int)(all & 0xFFFFu) + min((int)(all >> 16), c.ties);
 }

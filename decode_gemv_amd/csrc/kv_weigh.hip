@@ -229,7 +229,7 @@ __global__ __launch_bounds__(NW * 64) void k_kv_weigh(KvWeigh args)
 // LDS for all (two buffers, one barrier a time).
 template <int D>
 struct Many {
-    static constexpr int WAVES = D == 256 ? 8 : 4, TB = D == 256 ? 32 : 64, SUBS = TB / 16;
+    static constexpr int WAVES = 8, TB = 32, SUBS = TB / 16;
     static constexpr int TOKENS = WAVES * TB, ROWS = WAVES * 16;             // pages divide TOKENS
     struct Buffer {
         h8 q[WAVES][D / 32][64];
@@ -291,25 +291,28 @@ __global__ __launch_bounds__(Many<D>::WAVES * 64) void k_kv_weigh_rows(KvWeigh a
                 ck[u][i] = fmaf(dk[u][i], 8.0f, -half_hi(d[i]));
             }
         }
-        // 16 rows of the batch's tile (row tile i of the sequence) into a buffer
+        // 16 rows, row tile i of the sequence: loaded, and made into operands
         const int tiles = (q.n_new * a.group + 15) / 16;
-        auto put = [&](int i, typename M::Buffer &o) {
+        Query<D, 16, T> raw;
+        float log_sum = 0.0f;
+        auto load = [&](int i) {
+            if (i >= tiles) return;
             const KvWeigh &b = arguments();
             const KvAttend &a = b.a;
-            RowTile t = tile_of<16>(a, q, i);
-            if (t.rows == 0) {
-                if (lane < 16) o.row[wave * 16 + m] = make_float4(0.0f, 0.0f, 0.0f, 0.0f), o.seen[wave * 16 + m] = make_int2(0, 0);
-                return;
-            }
+            const RowTile t = tile_of<16>(a, q, i);
             const int2 at = token_of(a, t, min(m, t.rows - 1));
             const int64_t tok = t.row0 + at.x, h = (int64_t)head * a.group + at.y;
-            Query<D, 16, T> x;
-            x.load(a.q, tok, h, lane);
-            const float l = b.lse[tok * ((int64_t)a.g.kv_heads * a.group) + h];
+            raw.load(a.q, tok, h, lane);
+            log_sum = b.lse[tok * ((int64_t)a.g.kv_heads * a.group) + h];
+        };
+        auto put = [&](int i, typename M::Buffer &o) {
+            if (i >= tiles) return;
+            const KvAttend &a = arguments().a;
+            const RowTile t = tile_of<16>(a, q, i);
             float qs, qsum;
-            x.make(qs, qsum, a.scale, [&](int j, h8 y) { o.q[wave][j][lane] = y; });
-            const bool counts = m < t.rows && fabsf(l) < __builtin_inff();
-            const float2 lse = log2_of(l);
+            raw.make(qs, qsum, a.scale, [&](int j, h8 y) { o.q[wave][j][lane] = y; });
+            const bool counts = m < t.rows && fabsf(log_sum) < __builtin_inff();
+            const float2 lse = log2_of(log_sum);
             const Span seen = span_of(a, t, m);
             if (quarter == 0) {
                 o.row[wave * 16 + m] = make_float4(qs, qsum, lse.x, counts ? __builtin_amdgcn_exp2f(-lse.y) : 0.0f);
@@ -326,10 +329,13 @@ __global__ __launch_bounds__(Many<D>::WAVES * 64) void k_kv_weigh_rows(KvWeigh a
             if (before > 0) i0 = (int)min(before * a.group / 16, (int64_t)tiles) / M::WAVES * M::WAVES;
         }
         int turn = 0;
+        load(i0 + wave);
         put(i0 + wave, buf[0]);
+        load(i0 + M::WAVES + wave);
         for (int i = i0; i < tiles; i += M::WAVES, turn ^= 1) {
             __syncthreads();
-            if (i + M::WAVES < tiles) put(i + M::WAVES + wave, buf[turn ^ 1]);
+            put(i + M::WAVES + wave, buf[turn ^ 1]);
+            load(i + 2 * M::WAVES + wave);
             const typename M::Buffer &o = buf[turn];
             for (int n = 0; n < M::WAVES && i + n < tiles; n++) {
                 const float4 row = o.row[n * 16 + m];
