@@ -114,7 +114,7 @@ hipError_t lw_launch_kv_select(const KvSelect &a, int head_dim, int dtype, int64
 bool lw_kv_select_shared(int kv_heads, int64_t n_tokens, int64_t pages);
 // a.splits and a.chunk say how rows are cut; a.g's start, lens and table are the selection's.
 hipError_t lw_launch_kv_selected(const KvAttend &a, int head_dim, int dtype, int tile, hipStream_t s);
-hipError_t lw_launch_kv_weigh(const KvWeigh &b, int head_dim, int dtype, int64_t pages, hipStream_t s);
+hipError_t lw_launch_kv_weigh(const KvWeigh &b, int head_dim, int dtype, hipStream_t s);
 hipError_t lw_launch_kv_evict(const KvEvict &a, hipStream_t s);
 
 #ifdef __HIPCC__

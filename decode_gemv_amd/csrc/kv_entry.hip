@@ -405,7 +405,7 @@ extern "C" lw_status lw_kv_weigh(const lw_kv_cache *cache, const lw_kv_batch *ba
     if (window < 0) return lw_fail(LW_E_ARG, "negative window");
     if (!(decay >= 0.0f && decay <= 1.0f)) return lw_fail(LW_E_ARG, "decay must be in 0..1");
     if (stride < 0 || stride > (1 << 24)) return lw_fail(LW_E_ARG, "stride must be in 0..2^24");
-    if (batch->n_seqs * stride > (1 << 30)) return lw_fail(LW_E_ARG, "weights of more than 2^30 pages");
+    if (batch->n_seqs * stride > (1 << 27)) return lw_fail(LW_E_ARG, "weights of more than 2^27 pages");
     if (!batch->n_seqs || !n_tokens || !stride) return LW_OK;
     if ((st = tensor(q, "q", dtype, b.a.q))) return st;
     if (!lse || !weights || !aligned(lse, 4) || !aligned(before, 4) || !aligned(weights, 4))
@@ -419,7 +419,7 @@ extern "C" lw_status lw_kv_weigh(const lw_kv_cache *cache, const lw_kv_batch *ba
     b.decay = decay;
     b.weights = weights;
     b.stride = stride;
-    return device(lw_launch_kv_weigh(b, cache->head_dim, dtype, pages_of(cache, batch), (hipStream_t)stream), "kv weigh launch");
+    return device(lw_launch_kv_weigh(b, cache->head_dim, dtype, (hipStream_t)stream), "kv weigh launch");
 }
 
 extern "C" lw_status lw_kv_evict(const lw_kv_cache *cache, const lw_kv_batch *batch, const float *weights, int64_t stride,

@@ -666,7 +666,8 @@ size_t lw_kv_attend_selected_scratch_bytes(const lw_kv_cache *cache, const lw_kv
  *             (nothing before)
  *   weights : the same shape; written for the sequences with new tokens, pages
  *             j < stride that hold one of their lens[s] tokens (0 where the
- *             page is absent); the others keep what they have
+ *             page is absent); the others keep what they have.  n_seqs * stride
+ *             is at most 2^27
  *   decay   : 0..1 (with 0 before is not read)
  * Weights are fp32 sums in a fixed order: results are deterministic.
  * Errors: LW_E_ARG, LW_E_UNSUPPORTED (head_dim, page_tokens, dtype),
