@@ -67,50 +67,41 @@ __device__ __forceinline__ uint32_t prefix_max(uint32_t x)
     return x;
 }
 
-// A number of each thread's, summed over the workgroup.  sums: T / 64 words of
-// LDS.
-template <int T>
-__device__ __forceinline__ uint32_t sum_of(uint32_t x, uint32_t *sums)
-{
-    x = prefix(x);
-    if ((threadIdx.x & 63) == 63) sums[threadIdx.x >> 6] = x;
-    __syncthreads();
-    uint32_t all = 0;
-#pragma unroll
-    for (int w = 0; w < T / 64; w++) all += sums[w];
-    return all;
-}
+// What a thread has put: its keys' counts (there, and << 16 those that must be), and
+// the smallest and largest of the others.
+struct Tally {
+    uint32_t counts = 0, least = ~0u, most = 0;
 
-// Of `quads` times four keys in LDS.  sums: 4 * T / 64 words of LDS.  The keys are
-// there after a barrier.
-template <int T>
-__device__ __forceinline__ Keys look_at(const uint32_t *key, int quads, uint32_t *sums)
-{
-    const int lane = threadIdx.x & 63;
-    uint32_t counts = 0, least = ~0u, most = 0;              // there, and << 16 those that must (at most 2^15)
-#pragma unroll 2
-    for (int i = threadIdx.x; i < quads; i += T)
-        each_of(reinterpret_cast<const uint4 *>(key)[i], [&](int, uint32_t k) {
-            counts += k == 0 ? 0u : k == MUST ? 0x10001u : 1u;
-            least = k == 0 ? least : min(least, k);
-            most = k == MUST ? most : max(most, k);
-        });
-    counts = prefix(counts);
-    least = ~prefix_max(~least);
-    most = prefix_max(most);
-    if (lane == 63) *reinterpret_cast<uint4 *>(sums + 4 * (threadIdx.x >> 6)) = make_uint4(counts, least, most, 0);
-    __syncthreads();
-    Keys r = {0, 0, ~0u, 0};
-#pragma unroll
-    for (int w = 0; w < T / 64; w++) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(sums + 4 * w);
-        r.there += x.x & 0xFFFFu;
-        r.must += x.x >> 16;
-        r.least = min(r.least, x.y);
-        r.most = max(r.most, x.z);
+    __device__ __forceinline__ void add(uint32_t k)
+    {
+        counts += k == 0 ? 0u : k == MUST ? 0x10001u : 1u;
+        least = k == 0 ? least : min(least, k);
+        most = k == MUST ? most : max(most, k);
     }
-    return r;
-}
+
+    // The workgroup's, and the sum of x (at most 2^16).  sums: T / 16 words of LDS.
+    // Ends with a barrier: the keys are there.
+    template <int T>
+    __device__ __forceinline__ Keys meet(uint32_t *sums, uint32_t &x) const
+    {
+        const uint32_t n = prefix(counts), low = prefix_max(~least), high = prefix_max(most);
+        x = prefix(x);
+        if ((threadIdx.x & 63) == 63) *reinterpret_cast<uint4 *>(sums + 4 * (threadIdx.x >> 6)) = make_uint4(n, ~low, high, x);
+        __syncthreads();
+        Keys r = {0, 0, ~0u, 0};
+        x = 0;
+#pragma unroll
+        for (int w = 0; w < T / 64; w++) {
+            const uint4 y = *reinterpret_cast<const uint4 *>(sums + 4 * w);
+            r.there += y.x & 0xFFFFu;
+            r.must += y.x >> 16;
+            r.least = min(r.least, y.y);
+            r.most = max(r.most, y.z);
+            x += y.w;
+        }
+        return r;
+    }
+};
 
 // Histograms have 2048 counters, 32 and four words of padding in a row (64 lanes
 // that read a row each then meet no bank twice).  There are two, used in turn,

@@ -268,10 +268,10 @@ __device__ __forceinline__ Wanted wanted(const KvSelect &a, int row)
     return w;
 }
 
-// put(page, key, more) for the pages of tiles tile0, tile0 + hop, ... (of 16
+// put(page, key, part) for the pages of tiles tile0, tile0 + hop, ... (of 16
 // pages each) before `tiles`: a key's order is the pages', 0 means not to be
 // had.  Groups of more than 16 query heads come 16 at a time, and of what they
-// give the largest counts (more: not the first).  raw: the first 16 heads'.
+// give the largest counts (part of `parts`).  raw: the first 16 heads'.
 // N tiles' loads are under way at once, and the entries of the N after them:
 // their latency is what this takes.  Every wavefront of the workgroup comes here.
 template <int D, class T, int N, class F>
@@ -343,7 +343,7 @@ __device__ __forceinline__ void score_tiles(const KvSelect &a, const Wanted &w, 
                 if (col < 4 && k < w.n) {
                     const uint32_t key = ordered(e[n] == NOT_FINITE ? __builtin_inff() : ldexpf(x, e[n]));
                     const bool must = k < a.first || k >= w.own - a.last;
-                    put(k, !there[n] ? 0u : must ? MUST : key, part > 0);
+                    put(k, !there[n] ? 0u : must ? MUST : key, part);
                 }
             }
         }
@@ -364,7 +364,7 @@ __global__ __launch_bounds__(256) void k_kv_score(KvSelect a)
     if ((int)blockIdx.x * 4 >= tiles) return;
     uint32_t *to = a.work + ((int64_t)row * a.g.kv_heads + kv) * a.g.stride;
     score_tiles<D, T, TILES<D>>(a, w, row, kv, raw, mem, blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6),
-                               gridDim.x * 4, tiles, [&](int k, uint32_t x, bool more) { to[k] = more ? max(to[k], x) : x; });
+                               gridDim.x * 4, tiles, [&](int k, uint32_t x, int part) { to[k] = part ? max(to[k], x) : x; });
 }
 
 // The pages of a row and kv head.  THREADS a workgroup; the keys come from the
@@ -391,9 +391,13 @@ __global__ __launch_bounds__(THREADS) void k_kv_select(KvSelect a)
     const int n = w.q.seq < 0 ? 0 : w.n, quads = (n + 3) / 4;
     int got = 0;
     if (n > 0 && a.take > 1) {
+        Tally tally;
         if (threadIdx.x < (unsigned)(4 * quads - n)) key[n + threadIdx.x] = 0;
         if (n < a.take) {                                    // all of them that are present
-            for (int j = threadIdx.x; j < n; j += THREADS) key[j] = (uint32_t)w.pages[j] < a.g.n_pages;
+            for (int j = threadIdx.x; j < n; j += THREADS) {
+                key[j] = (uint32_t)w.pages[j] < a.g.n_pages;
+                tally.add(key[j]);
+            }
         } else if (a.work) {
             const uint32_t *from = a.work + ((int64_t)row * a.g.kv_heads + kv) * a.g.stride;
             for (int j0 = threadIdx.x; j0 < n; j0 += 8 * THREADS) {
@@ -402,15 +406,23 @@ __global__ __launch_bounds__(THREADS) void k_kv_select(KvSelect a)
                 for (int i = 0; i < 8; i++) x[i] = from[min(j0 + i * THREADS, n - 1)];
 #pragma unroll
                 for (int i = 0; i < 8; i++)
-                    if (j0 + i * THREADS < n) key[j0 + i * THREADS] = x[i];
+                    if (j0 + i * THREADS < n) {
+                        key[j0 + i * THREADS] = x[i];
+                        tally.add(x[i]);
+                    }
             }
         } else {
+            const int parts = (a.group + 15) / 16;
             score_tiles<D, T, TILES<D>>(a, w, row, kv, raw, reinterpret_cast<i4 (*)[2][64]>(hist),
-                                 __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), THREADS / 64, (n + 15) / 16,
-                                 [&](int k, uint32_t x, bool more) { key[k] = more ? max(key[k], x) : x; });
+                                        __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), THREADS / 64, (n + 15) / 16,
+                                        [&](int k, uint32_t x, int part) {
+                                            if (part) x = max(key[k], x);
+                                            key[k] = x;
+                                            if (part == parts - 1) tally.add(x);
+                                        });
         }
-        __syncthreads();
-        const Keys all = look_at<THREADS>(key, quads, sums + 4 * (THREADS / 64));
+        uint32_t nothing = 0;
+        const Keys all = tally.meet<THREADS>(sums + 4 * (THREADS / 64), nothing);
         const bool every = (int)all.there < a.take;
         Cut c = {};
         if (!every) c = pick_cut<THREADS>(key, quads, all, a.take - 1, hist);
@@ -445,6 +457,7 @@ __global__ __launch_bounds__(THREADS) void k_kv_evict(KvEvict a)
     const int known = (int)min((int64_t)n, a.stride);
     const int quads = (n + 3) / 4;
     uint32_t here = 0;
+    Tally tally;
     for (int j0 = threadIdx.x; j0 < (stride + 3) / 4 * 4; j0 += 2 * THREADS) {
         // (two pages and eight heads at once: their loads' latency is what this takes)
         double sum[2] = {0.0, 0.0};
@@ -468,15 +481,18 @@ __global__ __launch_bounds__(THREADS) void k_kv_evict(KvEvict a)
             const int j = j0 + i * THREADS;
             const bool present = j < n && (uint32_t)entry[i] < a.g.n_pages;
             const bool spare = present && j >= a.first && j < used - a.last;
-            const float x = (float)sum[i] + 0.0f;            // (-0 counts as 0)
+            const float total = (float)sum[i] + 0.0f;        // (-0 counts as 0)
             // the lowest weight has the largest key; at least 1
-            if (j < 4 * quads) key[j] = !spare ? 0u : j < known && x == x ? ~ordered(x) : 1u;
+            const uint32_t k = !spare ? 0u : j < known && total == total ? ~ordered(total) : 1u;
+            if (j < 4 * quads) {
+                key[j] = k;
+                tally.add(k);
+            }
             if (j < stride) to[j] = entry[i];
             here += present;
         }
     }
-    here = sum_of<THREADS>(here, sums);
-    const Keys all = look_at<THREADS>(key, quads, sums + 4 * (THREADS / 64));
+    const Keys all = tally.meet<THREADS>(sums + 4 * (THREADS / 64), here);
     const int drop = (int)min((int64_t)all.there, max((int64_t)here - a.keep, (int64_t)0));
     int got = 0;
     if (drop) {
