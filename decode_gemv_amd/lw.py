@@ -155,6 +155,8 @@ def _load():
 
 _L = _load()
 
+import torch as _torch  # noqa: E402  (after the library, whose loading maps its HIP runtime)
+
 
 def lib():
     return _L
@@ -536,6 +538,7 @@ class KvCache:
             raise LwError(LW_E_ARG, f"pages must hold whole pages of {size} bytes")
         self.pages, self.n_pages = pages, n // size
         self.kv_heads, self.head_dim, self.page_tokens = kv_heads, head_dim, page_tokens
+        self.bounds_bytes = self.n_pages * int(_L.lw_kv_bounds_bytes(kv_heads, head_dim))
         self.desc = lw_kv_cache(p, n // size, kv_heads, head_dim, page_tokens)
         self.ref = C.byref(self.desc)
 
@@ -553,6 +556,7 @@ class KvBatch:
         if start.numel() != n + 1 or table.dim() != 2 or table.shape[0] != n:
             raise LwError(LW_E_ARG, "start must hold one entry more than lens, table one row for each")
         self.start, self.lens, self.table = start, lens, table
+        self.n, self.shape = n, table.shape
         self.desc = lw_kv_batch(n, ps, pl, pt, table.shape[1], max_len)
         self.ref = C.byref(self.desc)
 
@@ -634,6 +638,41 @@ def lw_kv_attend(cache: KvCache, batch: KvBatch, q, out, scale: float | None = N
 
 
 # ---------------------------------------------------------------- rotary positions
+# (Small calls take as long as their way to the GPU: what is checked here is checked once, and addresses are passed as
+# numbers.)
+
+def _addr(t, what: str) -> int:
+    """Address of a contiguous device tensor."""
+    try:
+        if t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    raise LwError(LW_E_ARG, f"{what} must be a contiguous device tensor")
+
+
+def _typed(t, what: str, dtype, want: str) -> int:
+    p = _addr(t, what)
+    if t.dtype is not dtype:
+        raise LwError(LW_E_ARG, f"{what} must be {want}")
+    return p
+
+
+def _vectors(t, what: str, dim: int | None = None):
+    """Descriptor of a packed device tensor [n][heads][dim] with any row and head strides, and its shape."""
+    try:
+        shape, (s0, s1, s2), ok = t.shape, t.stride(), t.is_cuda
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok or (s2 != 1 and shape[2] != 1) or (dim is not None and shape[2] != dim):
+        raise LwError(LW_E_ARG, f"{what} must be a device tensor [tokens][heads][{dim or 'head_dim'}] with contiguous "
+                                "head vectors")
+    return lw_kv_tensor(t.data_ptr(), s0, s1), shape
+
+
+def _work(work):
+    return (_addr(work, "work"), work.numel() * work.element_size()) if work is not None and work.numel() else (None, 0)
+
 
 class RopePlan:
     """A worked out lw_rope_plan."""
@@ -652,30 +691,20 @@ def lw_rope_make(pairs: int, layout: int = LW_ROPE_HALVES, base: float = 10000.0
     return RopePlan(plan)
 
 
-def _rope_tensor(t, what: str, like=None):
-    try:
-        shape, (s0, s1, s2), ok = t.shape, t.stride(), t.is_cuda
-    except (AttributeError, ValueError):
-        ok = False
-    if not ok or (s2 != 1 and shape[2] != 1):
-        raise LwError(LW_E_ARG, f"{what} must be a device tensor [tokens][heads][head_dim] with contiguous head vectors")
-    if like is not None and shape != like.shape:
-        raise LwError(LW_E_ARG, f"{what} must have the shape of the tensor before it")
-    return lw_kv_tensor(t.data_ptr(), s0, s1)
-
-
 def lw_rope(plan: RopePlan, x, y, batch: KvBatch | None = None, pos=None, stream=None) -> None:
     """y = x [n][heads][head_dim] turned by the rows' positions: those of the batch's tokens, or pos (int32 [n])."""
-    import torch
-    tx = _rope_tensor(x, "x")
-    ty = _rope_tensor(y, "y", x)
+    tx, shape = _vectors(x, "x")
+    ty, out = _vectors(y, "y")
+    if shape != out:
+        raise LwError(LW_E_ARG, "y must have the shape of x")
+    n, heads, dim = shape
     pp = None
     if pos is not None:
-        pp = _dptr(pos, "pos")
-        if pos.dtype != torch.int32 or pos.numel() != x.shape[0]:
+        pp = _typed(pos, "pos", _torch.int32, "int32 [tokens]")
+        if pos.numel() != n:
             raise LwError(LW_E_ARG, "pos must be int32 [tokens]")
-    st = _L.lw_rope(plan.ref, batch.ref if batch is not None else None, pp, x.shape[0], x.shape[1], x.shape[2],
-                    C.byref(tx), _kv_type(x), C.byref(ty), _kv_type(y), _stream(stream))
+    st = _L.lw_rope(plan.ref, None if batch is None else batch.ref, pp, n, heads, dim, C.byref(tx), _kv_type(x), C.byref(ty),
+                    _kv_type(y), _stream(stream))
     if st:
         _check(st)
 
@@ -687,9 +716,9 @@ def lw_kv_bounds_bytes(kv_heads: int, head_dim: int) -> int:
     return int(_L.lw_kv_bounds_bytes(kv_heads, head_dim))
 
 
-def _bounds(bounds, cache):
-    p = _dptr(bounds, "bounds")
-    if bounds.numel() * bounds.element_size() < cache.n_pages * lw_kv_bounds_bytes(cache.kv_heads, cache.head_dim):
+def _bounds(bounds, cache) -> int:
+    p = _addr(bounds, "bounds")
+    if bounds.numel() * bounds.element_size() < cache.bounds_bytes:
         raise LwError(LW_E_ARG, "bounds must hold lw_kv_bounds_bytes for each page of the cache")
     return p
 
@@ -699,10 +728,7 @@ class KvSelection:
     table [n][kv_heads][pages], which lw_kv_select fills."""
 
     def __init__(self, start, lens, table):
-        import torch
-        ps, pl, pt = _dptr(start, "start"), _dptr(lens, "lens"), _dptr(table, "table")
-        if any(t.dtype != torch.int32 for t in (start, lens, table)):
-            raise LwError(LW_E_ARG, "start, lens and table must be int32")
+        ps, pl, pt = (_typed(t, what, _torch.int32, "int32") for t, what in ((start, "start"), (lens, "lens"), (table, "table")))
         n = lens.numel()
         if start.numel() != n + 1 or table.dim() != 3 or table.shape[0] != n:
             raise LwError(LW_E_ARG, "start must hold one entry more than lens, table [kv_heads][pages] for each")
@@ -712,11 +738,11 @@ class KvSelection:
         self.ref = C.byref(self.desc)
 
 
-def _rows(t, what, sel, cache):
-    tensor = _kv_tensor(t, what, cache)
-    if t.shape[0] != sel.n or sel.kv_heads != cache.kv_heads:
+def _selected(t, what, sel, cache):
+    tensor, shape = _vectors(t, what, cache.head_dim)
+    if shape[0] != sel.n or sel.kv_heads != cache.kv_heads:
         raise LwError(LW_E_ARG, f"the selection must have {what}'s rows and the cache's heads")
-    return tensor
+    return tensor, shape
 
 
 def lw_kv_bounds(cache: KvCache, batch: KvBatch, n_tokens: int, bounds, stream=None) -> None:
@@ -733,10 +759,9 @@ def lw_kv_select_scratch_bytes(cache: KvCache, batch: KvBatch, n_tokens: int, q_
 def lw_kv_select(cache: KvCache, batch: KvBatch, q, bounds, sel: KvSelection, first: int = 1, last: int = 1, work=None,
                  stream=None) -> None:
     """Choose sel's pages for the rows of q [n][q_heads][head_dim]."""
-    tq = _rows(q, "q", sel, cache)
-    wp, wn = _wbuf(work if work is not None and work.numel() else None)
-    st = _L.lw_kv_select(cache.ref, batch.ref, C.byref(tq), _kv_type(q), q.shape[1], _bounds(bounds, cache), first, last,
-                         sel.ref, wp, wn, _stream(stream))
+    tq, shape = _selected(q, "q", sel, cache)
+    st = _L.lw_kv_select(cache.ref, batch.ref, C.byref(tq), _kv_type(q), shape[1], _bounds(bounds, cache), first, last,
+                         sel.ref, *_work(work), _stream(stream))
     if st:
         _check(st)
 
@@ -745,9 +770,9 @@ def lw_kv_attend_selected_scratch_bytes(cache: KvCache, sel: KvSelection, q_head
     return int(_L.lw_kv_attend_selected_scratch_bytes(cache.ref, sel.ref, q_heads))
 
 
-def _lse(lse, q):
-    p = _dptr(lse, "lse")
-    if lse.shape != q.shape[:2] or (_KV_TYPES or _kv_types()).get(lse.dtype) != LW_F32:
+def _log_sums(lse, shape) -> int:
+    p = _typed(lse, "lse", _torch.float32, "fp32 [tokens][q_heads]")
+    if lse.dim() != 2 or lse.shape != shape[:2]:
         raise LwError(LW_E_ARG, "lse must be fp32 [tokens][q_heads]")
     return p
 
@@ -755,12 +780,14 @@ def _lse(lse, q):
 def lw_kv_attend_selected(cache: KvCache, sel: KvSelection, q, out, scale: float | None = None, lse=None, work=None,
                           stream=None) -> None:
     """out = attention of q [n][q_heads][head_dim] over the selected pages; scale None: head_dim ** -0.5."""
-    tq = _rows(q, "q", sel, cache)
-    to = _kv_tensor(out, "out", cache, q)
-    pl = _lse(lse, q) if lse is not None else None
-    wp, wn = _wbuf(work if work is not None and work.numel() else None)
-    st = _L.lw_kv_attend_selected(cache.ref, sel.ref, C.byref(tq), C.byref(to), _kv_type(q), q.shape[1],
-                                  cache.head_dim ** -0.5 if scale is None else scale, pl, wp, wn, _stream(stream))
+    tq, shape = _selected(q, "q", sel, cache)
+    to, got = _vectors(out, "out", cache.head_dim)
+    kind = _kv_type(q)
+    if got != shape or _kv_type(out) != kind:
+        raise LwError(LW_E_ARG, "out must have the shape and type of q")
+    st = _L.lw_kv_attend_selected(cache.ref, sel.ref, C.byref(tq), C.byref(to), kind, shape[1],
+                                  cache.head_dim ** -0.5 if scale is None else scale,
+                                  None if lse is None else _log_sums(lse, shape), *_work(work), _stream(stream))
     if st:
         _check(st)
 
@@ -768,25 +795,25 @@ def lw_kv_attend_selected(cache: KvCache, sel: KvSelection, q, out, scale: float
 # ---------------------------------------------------------------- pages given up
 
 def _weights(t, what, cache, batch):
-    p = _dptr(t, what)
-    if (t.dim() != 3 or t.shape[:2] != (batch.lens.numel(), cache.kv_heads)
-            or (_KV_TYPES or _kv_types()).get(t.dtype) != LW_F32):
+    p, shape = _typed(t, what, _torch.float32, "fp32 [sequences][kv_heads][pages]"), t.shape
+    if len(shape) != 3 or shape[0] != batch.n or shape[1] != cache.kv_heads:
         raise LwError(LW_E_ARG, f"{what} must be fp32 [sequences][kv_heads][pages]")
-    return p
+    return p, shape
 
 
 def lw_kv_weigh(cache: KvCache, batch: KvBatch, q, lse, weights, before=None, decay: float = 1.0,
                 scale: float | None = None, causal: bool = True, window: int = 0, stream=None) -> None:
     """weights [sequences][kv_heads][pages] = decay * before + what the rows of q gave to the pages' tokens."""
-    tq = _kv_tensor(q, "q", cache)
-    pw, pb = _weights(weights, "weights", cache, batch), None
+    tq, shape = _vectors(q, "q", cache.head_dim)
+    pw, pages = _weights(weights, "weights", cache, batch)
+    pb = None
     if before is not None:
-        pb = _weights(before, "before", cache, batch)
-        if before.shape != weights.shape:
+        pb, prior = _weights(before, "before", cache, batch)
+        if prior != pages:
             raise LwError(LW_E_ARG, "before must have the shape of weights")
-    st = _L.lw_kv_weigh(cache.ref, batch.ref, q.shape[0], C.byref(tq), _kv_type(q), q.shape[1],
-                        cache.head_dim ** -0.5 if scale is None else scale, causal, window, _lse(lse, q), pb, decay, pw,
-                        weights.shape[2], _stream(stream))
+    st = _L.lw_kv_weigh(cache.ref, batch.ref, shape[0], C.byref(tq), _kv_type(q), shape[1],
+                        cache.head_dim ** -0.5 if scale is None else scale, causal, window, _log_sums(lse, shape), pb, decay,
+                        pw, pages[2], _stream(stream))
     if st:
         _check(st)
 
@@ -795,13 +822,11 @@ def lw_kv_evict(cache: KvCache, batch: KvBatch, weights, keep: int, table, gone,
                 stream=None) -> None:
     """Give up each sequence's pages of least weight until keep are left: table (batch's shape; may be its own) gets
     -1 for them, gone their numbers, count how many."""
-    import torch
-    pw = _weights(weights, "weights", cache, batch)
-    ps = [_dptr(t, what) for t, what in ((table, "table"), (gone, "gone"), (count, "count"))]
-    if (any(t.dtype != torch.int32 for t in (table, gone, count)) or table.shape != batch.table.shape
-            or gone.shape != batch.table.shape or count.numel() != batch.lens.numel()):
-        raise LwError(LW_E_ARG, "table and gone must be int32 of the batch's table's shape, count int32 [sequences]")
-    st = _L.lw_kv_evict(cache.ref, batch.ref, pw, weights.shape[2], keep, first, last, *ps, _stream(stream))
+    pw, pages = _weights(weights, "weights", cache, batch)
+    pt, pg, pc = _typed(table, "table", _torch.int32, "int32"), _typed(gone, "gone", _torch.int32, "int32"), _typed(count, "count", _torch.int32, "int32")
+    if table.shape != batch.shape or gone.shape != batch.shape or count.numel() != batch.n:
+        raise LwError(LW_E_ARG, "table and gone must have the shape of the batch's table, count one number a sequence")
+    st = _L.lw_kv_evict(cache.ref, batch.ref, pw, pages[2], keep, first, last, pt, pg, pc, _stream(stream))
     if st:
         _check(st)
 
