@@ -110,7 +110,9 @@ hipError_t lw_launch_rope(const lw_rope_plan &plan, const KvGeom &g, const int32
 hipError_t lw_launch_kv_bounds(const KvGeom &g, int head_dim, uint8_t *bounds, int64_t bounds_bytes, hipStream_t s);
 // `pages`: of the longest sequence, as far as the host knows.
 hipError_t lw_launch_kv_select(const KvSelect &a, int head_dim, int dtype, int64_t pages, hipStream_t s);
-// Whether a row's scores are shared out over workgroups.
+// Whether a row's scores are shared out over workgroups: for up to that many pairs
+// of row and kv head, where their sequences are long.
+constexpr int64_t KV_SHARED_PAIRS = 512;
 bool lw_kv_select_shared(int kv_heads, int64_t n_tokens, int64_t pages);
 // a.splits and a.chunk say how rows are cut; a.g's start, lens and table are the selection's.
 hipError_t lw_launch_kv_selected(const KvAttend &a, int head_dim, int dtype, int tile, hipStream_t s);

@@ -278,13 +278,23 @@ int64_t pages_of(const lw_kv_cache *c, const lw_kv_batch *b)
 
 }  // namespace
 
+namespace {
+
+size_t select_bytes(const lw_kv_cache *c, const lw_kv_batch *b, int64_t n_tokens)
+{
+    if (!b->n_seqs || !lw_kv_select_shared(c->kv_heads, n_tokens, pages_of(c, b))) return 0;
+    return (size_t)n_tokens * c->kv_heads * b->table_stride * sizeof(uint32_t);
+}
+
+}  // namespace
+
 extern "C" size_t lw_kv_select_scratch_bytes(const lw_kv_cache *cache, const lw_kv_batch *batch, int64_t n_tokens,
                                              int q_heads)
 {
     KvGeom g;
     if (geom(cache, batch, n_tokens, g) || heads(cache, n_tokens, LW_F16, q_heads) || few_pages(batch)) return 0;
-    if (!batch->n_seqs || !lw_kv_select_shared(cache->kv_heads, n_tokens, pages_of(cache, batch))) return 0;
-    return (size_t)n_tokens * cache->kv_heads * batch->table_stride * sizeof(uint32_t);
+    // (calls of more rows than that need none)
+    return select_bytes(cache, batch, std::min<int64_t>(n_tokens, KV_SHARED_PAIRS / cache->kv_heads));
 }
 
 extern "C" lw_status lw_kv_select(const lw_kv_cache *cache, const lw_kv_batch *batch, const lw_kv_tensor *q, int dtype,
@@ -303,7 +313,7 @@ extern "C" lw_status lw_kv_select(const lw_kv_cache *cache, const lw_kv_batch *b
     if ((st = tensor(q, "q", dtype, a.q))) return st;
     if (!bounds || !aligned(bounds, 16)) return lw_fail(LW_E_ARG, "bounds must be 16-byte aligned and not null");
     if (!aligned(work, 4)) return lw_fail(LW_E_ARG, "work must be 4-byte aligned");
-    const size_t need = lw_kv_select_scratch_bytes(cache, batch, sel->n_tokens, q_heads);
+    const size_t need = select_bytes(cache, batch, sel->n_tokens);
     a.bounds = static_cast<const uint8_t *>(bounds);
     a.bounds_bytes = (int64_t)lw_kv_bounds_bytes(cache->kv_heads, cache->head_dim);
     a.group = q_heads / cache->kv_heads;
@@ -328,6 +338,18 @@ struct Chunks {
     size_t result;               // bytes of one's
 };
 
+// Chunks that a row tile is wanted in, of `tiles`: those of two workgroups a CU,
+// of 256 tokens at least (two steps of each wavefront).  Heads of 256 have
+// registers for half as many wavefronts, and take one workgroup a CU and 1024
+// tokens: 31 rows on 4 heads and 1536 tokens, with their choice, 34.0 us and not
+// 36.5.
+int64_t wanted_chunks(const lw_kv_cache *c, int64_t tiles, int64_t span)
+{
+    const int64_t groups = c->head_dim == 256 ? 256 : 512, least = c->head_dim == 256 ? 1024 : 256;
+    const int64_t base = std::max<int64_t>(tiles * c->kv_heads, 1);
+    return std::min((groups + base - 1) / base, (span + least - 1) / least);
+}
+
 Chunks chunks_of(const lw_kv_cache *c, const lw_kv_selection *sel, int q_heads, size_t room)
 {
     Chunks p;
@@ -336,14 +358,8 @@ Chunks chunks_of(const lw_kv_cache *c, const lw_kv_selection *sel, int q_heads, 
     p.tile = group <= 8 ? 8 : 16;
     p.tiles = sel->n_tokens * ((group + p.tile - 1) / p.tile);
     p.result = (size_t)c->kv_heads * p.tile * (c->head_dim + 2) * sizeof(float);
-    const int64_t base = std::max<int64_t>(p.tiles * c->kv_heads, 1);
-    // Chunks for two workgroups a CU, of 256 tokens at least (two steps of each
-    // wavefront).  Heads of 256 have registers for half as many wavefronts, and
-    // take one workgroup a CU and 1024 tokens: 31 rows on 4 heads and 1536 tokens
-    // with lw_kv_select 34.0 us and not 36.5.
-    const int64_t want = c->head_dim == 256 ? 256 : 512, least = c->head_dim == 256 ? 1024 : 256;
-    int64_t splits = std::min((want + base - 1) / base, (span + least - 1) / least);
-    splits = std::max<int64_t>(std::min<int64_t>(splits, (int64_t)(room / p.result / std::max<int64_t>(p.tiles, 1))), 1);
+    const int64_t fit = (int64_t)(room / p.result / std::max<int64_t>(p.tiles, 1));
+    const int64_t splits = std::max<int64_t>(std::min(wanted_chunks(c, p.tiles, span), fit), 1);
     p.chunk = (int)(((span + splits - 1) / splits + 127) / 128 * 128);
     p.splits = (int)((span + p.chunk - 1) / p.chunk);
     return p;
@@ -355,8 +371,16 @@ extern "C" size_t lw_kv_attend_selected_scratch_bytes(const lw_kv_cache *cache, 
 {
     KvGeom g;
     if (!cache || selection(cache, sel) || pages(cache, false, g) || heads(cache, sel->n_tokens, LW_F16, q_heads)) return 0;
-    const Chunks p = chunks_of(cache, sel, q_heads, SIZE_MAX);
-    return p.splits > 1 ? p.tiles * p.splits * p.result : 0;
+    // the most that as many rows or fewer, on as many pages or fewer, want
+    const Chunks p = chunks_of(cache, sel, q_heads, 0);
+    const int64_t per = sel->n_tokens ? p.tiles / sel->n_tokens : 1, span = sel->pages * cache->page_tokens;
+    int64_t most = 0;
+    for (int64_t n = 1; n <= sel->n_tokens; n++) {
+        const int64_t splits = wanted_chunks(cache, n * per, span);
+        if (splits <= 1) break;
+        most = std::max(most, n * per * splits);
+    }
+    return most * p.result;
 }
 
 extern "C" lw_status lw_kv_attend_selected(const lw_kv_cache *cache, const lw_kv_selection *sel, const lw_kv_tensor *q,
@@ -374,7 +398,7 @@ extern "C" lw_status lw_kv_attend_selected(const lw_kv_cache *cache, const lw_kv
     if (!aligned(lse, 4)) return lw_fail(LW_E_ARG, "lse must be 4-byte aligned");
     if (!aligned(work, 16)) return lw_fail(LW_E_ARG, "work must be 16-byte aligned");
     const Chunks p = chunks_of(cache, sel, q_heads, work ? work_bytes : 0);
-    if (p.tiles * p.splits > INT_MAX) return lw_fail(LW_E_UNSUPPORTED, "more than 2^31 tiles of query rows");
+    if (p.tiles * p.splits > (1 << 30)) return lw_fail(LW_E_UNSUPPORTED, "more than 2^30 tiles of query rows");
     a.g.start = sel->start;
     a.g.lens = sel->lens;
     a.g.table = sel->table;

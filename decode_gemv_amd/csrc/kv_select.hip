@@ -545,7 +545,10 @@ hipError_t lw_launch_kv_bounds(const KvGeom &g, int head_dim, uint8_t *bounds, i
 
 bool lw_kv_select_shared(int kv_heads, int64_t n_tokens, int64_t pages)
 {
-    return kv_heads * n_tokens <= 512 && pages >= 256;
+    // With workgroups of their own for the scores, and in the choice's: 128 pairs on
+    // 512 pages 13.1 us and 15.2 (two launches and one), 124 on 391 of heads of 256
+    // 13.2 and 17.5, 8 on 4096 14.1 and 55.  8 pairs on 80: 8.9 in one.
+    return n_tokens > 0 && kv_heads * n_tokens <= KV_SHARED_PAIRS && pages >= 256;
 }
 
 hipError_t lw_launch_kv_select(const KvSelect &a, int head_dim, int dtype, int64_t pages, hipStream_t s)

@@ -233,8 +233,8 @@ struct Rows {
     __device__ __forceinline__ void make(float scale)
     {
         raw.make(qs, qsum, scale, [&](int j, h8 y) { q[j] = y; });
-        counts = counts && fabsf(log_sum) < __builtin_inff();
         lse = log2_of(log_sum);
+        counts = counts && fabsf(lse.x) < __builtin_inff();
     }
 
     // sum over the lane's tokens of t0 .. t0 + 31
@@ -433,8 +433,8 @@ __global__ __launch_bounds__(MANY<D> * 64) void k_kv_weigh_rows(KvWeigh args)
             const RowTile t = tile_of<16>(a, q, i);
             float qs, qsum;
             raw.make(qs, qsum, a.scale, [&](int j, h8 y) { o.q[j][lane] = y; });
-            const bool counts = m < t.rows && fabsf(log_sum) < __builtin_inff();
             const float2 lse = log2_of(log_sum);
+            const bool counts = m < t.rows && fabsf(lse.x) < __builtin_inff();
             const Span seen = span_of(a, t, m), e = span_of(a, t, 0), f = span_of(a, t, t.rows - 1);
             if (quarter == 0) {
                 o.row[m] = make_float4(qs, qsum, lse.x, counts ? __builtin_amdgcn_exp2f(-lse.y) : 0.0f);

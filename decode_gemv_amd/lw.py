@@ -641,14 +641,20 @@ def lw_kv_attend(cache: KvCache, batch: KvBatch, q, out, scale: float | None = N
 # (Small calls take as long as their way to the GPU: what is checked here is checked once, and addresses are passed as
 # numbers.)
 
+def _here(t) -> bool:
+    """Whether a tensor lies on the current device, on whose stream the call goes."""
+    d = t.get_device()                                       # (-1: in host memory)
+    return d >= 0 and d == _torch._C._cuda_getDevice()
+
+
 def _addr(t, what: str) -> int:
-    """Address of a contiguous device tensor."""
+    """Address of a contiguous tensor on the current device."""
     try:
-        if t.is_cuda and t.is_contiguous():
+        if _here(t) and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         pass
-    raise LwError(LW_E_ARG, f"{what} must be a contiguous device tensor")
+    raise LwError(LW_E_ARG, f"{what} must be a contiguous tensor on the current device")
 
 
 def _typed(t, what: str, dtype, want: str) -> int:
@@ -661,12 +667,12 @@ def _typed(t, what: str, dtype, want: str) -> int:
 def _vectors(t, what: str, dim: int | None = None):
     """Descriptor of a packed device tensor [n][heads][dim] with any row and head strides, and its shape."""
     try:
-        shape, (s0, s1, s2), ok = t.shape, t.stride(), t.is_cuda
+        shape, (s0, s1, s2), ok = t.shape, t.stride(), _here(t)
     except (AttributeError, ValueError):
         ok = False
     if not ok or (s2 != 1 and shape[2] != 1) or (dim is not None and shape[2] != dim):
-        raise LwError(LW_E_ARG, f"{what} must be a device tensor [tokens][heads][{dim or 'head_dim'}] with contiguous "
-                                "head vectors")
+        raise LwError(LW_E_ARG, f"{what} must be a tensor [tokens][heads][{dim or 'head_dim'}] on the current device, "
+                                "with contiguous head vectors")
     return lw_kv_tensor(t.data_ptr(), s0, s1), shape
 
 

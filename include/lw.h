@@ -633,8 +633,9 @@ lw_status lw_kv_select(const lw_kv_cache *cache, const lw_kv_batch *batch, const
                        const void *bounds, int first, int last, const lw_kv_selection *sel, void *work,
                        size_t work_bytes, void *stream);
 
-/* Bytes of work that lw_kv_select wants for these (0 where it needs none, or
- * for arguments that it refuses). */
+/* Bytes of work that lw_kv_select wants for batches of up to that many rows,
+ * max_len and table_stride (0 where it needs none, or for arguments that it
+ * refuses). */
 size_t lw_kv_select_scratch_bytes(const lw_kv_cache *cache, const lw_kv_batch *batch, int64_t n_tokens, int q_heads);
 
 /* lw_kv_attend of sel->n_tokens rows over the pages that lw_kv_select chose:
@@ -649,6 +650,10 @@ size_t lw_kv_select_scratch_bytes(const lw_kv_cache *cache, const lw_kv_batch *b
 lw_status lw_kv_attend_selected(const lw_kv_cache *cache, const lw_kv_selection *sel, const lw_kv_tensor *q,
                                 const lw_kv_tensor *out, int dtype, int q_heads, float scale, float *lse, void *work,
                                 size_t work_bytes, void *stream);
+
+/* Bytes of work that lw_kv_attend_selected wants for selections of up to that
+ * many rows and pages (0 where it needs none, or for arguments that it
+ * refuses). */
 size_t lw_kv_attend_selected_scratch_bytes(const lw_kv_cache *cache, const lw_kv_selection *sel, int q_heads);
 
 /* ---------------------------------------------------------------- pages given up */
@@ -659,7 +664,7 @@ size_t lw_kv_attend_selected_scratch_bytes(const lw_kv_cache *cache, const lw_kv
  *   weights[s][g][j] = decay * before[s][g][j] + sum exp(scale q.k - lse)
  * over the rows of sequence s, the query heads of kv head g and the tokens of
  * page j that a row sees (causal and window as in lw_kv_attend, whose log sums
- * lse are; a row whose log sum is not finite adds nothing).
+ * lse are; a row whose log sum is not finite, or past 2^127, adds nothing).
  *   q       : [n_tokens][q_heads][D], LW_F16 or LW_BF16
  *   lse     : fp32 [n_tokens][q_heads]
  *   before  : fp32 [n_seqs][kv_heads][stride], may be weights itself, or NULL

@@ -186,6 +186,37 @@ def test_the_longest_table(torch, dg):
     give_up(torch, dg, 1, 32, table, [n * 32], rng.random((1, 1, n)).astype(np.float32), n, 10000, 1, 2)
 
 
+def test_a_long_table_in_a_graph(torch, dg):
+    """More shared memory than a kernel has without asking for it, asked for while a graph is captured."""
+    n = 20000
+    rng = np.random.default_rng(3)
+    cache = dg.KvCache(torch.empty(n * R.page_bytes(1, 64, 32), dtype=torch.uint8, device="cuda"), 1, 64, 32)
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    table, lens = rng.permutation(n).astype(np.int32)[None], np.array([n * 32], np.int32)
+    b = dg.KvBatch(torch.zeros(2, dtype=torch.int32, device="cuda"), dev(lens), dev(table))
+    weights = torch.zeros((1, 1, n), device="cuda")
+    left, gone, count = torch.empty_like(b.table), torch.empty_like(b.table), torch.empty_like(b.lens)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dg.lw_kv_evict(cache, b, weights, 12000, left, gone, count)
+    for seed in range(3):
+        w = np.random.default_rng(seed).random((1, 1, n)).astype(np.float32)
+        weights.copy_(torch.from_numpy(w))
+        graph.replay()
+        want = L.evict(table, lens, w, 32, n, 12000, 1, 1)
+        assert np.array_equal(host(left), want[0]) and np.array_equal(host(gone), want[1]) and np.array_equal(host(count), want[2])
+
+
+def test_log_sums_past_the_largest_power_of_two(torch, dg):
+    """3e38 is a number, its logarithm to base two is not one here: the row adds nothing, and no NaN."""
+    for rows in (1, 40):
+        s = Setup(torch, dg, 1, 64, 32, [rows], [100], 3).fill()
+        q, w = queries(s, 2, "bf16"), torch.zeros((1, 1, 4), device="cuda")
+        lse = torch.full((rows, 2), 3e38, device="cuda")
+        dg.lw_kv_weigh(s.cache, s.batch, q, lse, w)
+        assert not host(w).any()
+
+
 def test_refusals_of_the_binding(torch, dg):
     kv, D, P = 2, 64, 32
     s = Setup(torch, dg, kv, D, P, [3], [100], 3)

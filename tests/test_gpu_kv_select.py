@@ -179,6 +179,33 @@ def test_many_pages_chosen_alone_and_shared_out(torch, dg):
 
 
 @pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("take", [17, 12000])
+def test_the_longest_table(torch, dg, take, shared):
+    """32768 pages a sequence (a few, again and again), of which the host knows nothing: planned for one token."""
+    kv, group, D, P, n = 1, 2, 64, 32, 32768
+    rng = np.random.default_rng(7)
+    s = Setup(torch, dg, kv, D, P, [2], [n * P - 40], 4, table=rng.integers(0, 90, (1, n)), n_pages=90).fill()
+    raw = all_bounds(s)
+    bounds, q = torch.from_numpy(raw).cuda(), queries(s, group, "bf16")
+    short = dg.KvBatch(s.batch.start, s.batch.lens, s.batch.table, max_len=1)
+    b = s.batch if shared else short
+    need = dg.lw_kv_select_scratch_bytes(s.cache, b, 2, 2)
+    assert bool(need) == shared
+    sel = selection(torch, dg, 2, kv, take)
+    work = torch.empty(need, dtype=torch.uint8, device="cuda") if need else None
+    dg.lw_kv_select(s.cache, b, q, bounds, sel, 2, 3, work=work)
+    one = [L.scores(raw, kv, D, np.arange(90), 0, x) for x in host(q)]
+    for i in range(2):
+        pos = n * P - 42 + i
+        own = pos // P
+        key = np.array(one[i])[s.table[0, :own]]
+        key[:2] = key[own - 3:] = np.inf
+        mine = np.sort(np.argsort(-key, kind="stable")[:take - 1])
+        assert np.array_equal(host(sel.table)[i, 0], np.append(s.table[0, mine], s.table[0, own]))
+        assert host(sel.lens)[i] == (take - 1) * P + pos % P + 1
+
+
+@pytest.mark.parametrize("shared", [False, True])
 def test_equal_scores_take_the_first(torch, dg, shared):
     """Every page the same: the scores are equal, and the first are taken, also where as many are as a cut can have."""
     kv, D, P = 2, 64, 32

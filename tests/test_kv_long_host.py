@@ -244,3 +244,43 @@ def test_scratch():
     assert selects(a.batch, 1) == 0 and 0 < selects(long_, 1) < 1 << 20
     assert selects(long_, 1, 3) == 0 and selects(changed(long_, table_stride=-1), 1) == 0
     assert selects(changed(long_, max_len=64), 1) == 0
+
+
+@pytest.mark.parametrize("kv,heads,D,P", [(8, 32, 128, 64), (4, 16, 256, 128), (1, 20, 64, 32), (16, 16, 64, 256)])
+def test_scratch_of_the_largest_call_does_for_smaller_ones(kv, heads, D, P):
+    cache = lw.lw_kv_cache(1 << 20, 1 << 20, kv, D, P)
+    attends = lambda n, pages: dg.lib().lw_kv_attend_selected_scratch_bytes(C.byref(cache), C.byref(lw.lw_kv_selection(n, 16, 16, 16, pages)), heads)
+    selects = lambda n, stride: dg.lib().lw_kv_select_scratch_bytes(C.byref(cache), C.byref(lw.lw_kv_batch(1, 16, 16, 16, stride, 0)), n, heads)
+    for f, sizes in ((attends, (1, 2, 4, 7, 9, 16, 33, 64, 100, 129, 500)), (selects, (1, 100, 255, 256, 300, 1024, 32768))):
+        counts = (1, 2, 3, 7, 16, 31, 32, 33, 64, 65, 127, 128, 300, 513, 2000)
+        for i, n in enumerate(counts):
+            for k, size in enumerate(sizes):
+                if i:
+                    assert f(n, size) >= f(counts[i - 1], size)
+                if k:
+                    assert f(n, size) >= f(n, sizes[k - 1])
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """(Without one: what the binding asks a tensor is answered for it.)"""
+    import torch
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+
+    class There:
+        dtype, shape = torch.int32, torch.Size([3, 2, 64])
+        device = 0
+        get_device = lambda self: self.device
+        is_contiguous = lambda self: True
+        data_ptr = lambda self: 256
+        stride = lambda self: (128, 64, 1)
+
+    t = There()
+    assert lw._addr(t, "t") == 256 and lw._vectors(t, "t")[0].data == 256
+    for device in (1, -1):
+        t.device = device
+        for call in (lw._addr, lw._vectors):
+            with pytest.raises(dg.LwError, match="current device"):
+                call(t, "t")
+    for call in (lw._addr, lw._vectors):
+        with pytest.raises(dg.LwError):
+            call(None, "t")
