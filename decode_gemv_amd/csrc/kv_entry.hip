@@ -463,6 +463,8 @@ extern "C" lw_status lw_kv_evict(const lw_kv_cache *cache, const lw_kv_batch *ba
     for (const void *p : {(const void *)batch->lens, (const void *)batch->table, (const void *)weights,
                           (const void *)table, (const void *)gone, (const void *)count})
         if (!aligned(p, 4)) return lw_fail(LW_E_ARG, "the arrays must be 4-byte aligned");
+    if (batch->table_stride && (gone == table || gone == batch->table))
+        return lw_fail(LW_E_ARG, "gone must not be one of the tables");
     a.weights = weights;
     a.stride = stride;
     a.keep = keep;

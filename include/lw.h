@@ -667,8 +667,8 @@ size_t lw_kv_attend_selected_scratch_bytes(const lw_kv_cache *cache, const lw_kv
  * lse are; a row whose log sum is not finite, or past 2^127, adds nothing).
  *   q       : [n_tokens][q_heads][D], LW_F16 or LW_BF16
  *   lse     : fp32 [n_tokens][q_heads]
- *   before  : fp32 [n_seqs][kv_heads][stride], may be weights itself, or NULL
- *             (nothing before)
+ *   before  : fp32 [n_seqs][kv_heads][stride], weights itself or nowhere in
+ *             it, or NULL (nothing before)
  *   weights : the same shape; written for the sequences with new tokens, pages
  *             j < stride that hold one of their lens[s] tokens (0 where the
  *             page is absent); the others keep what they have.  n_seqs * stride
@@ -692,8 +692,9 @@ lw_status lw_kv_weigh(const lw_kv_cache *cache, const lw_kv_batch *batch, int64_
  *   weights     : fp32 [n_seqs][kv_heads][stride]
  *   table       : device int32 [n_seqs][batch->table_stride], overwritten with
  *                 batch's, -1 where a page is given up; may be batch's itself
- *   gone        : device int32 [n_seqs][batch->table_stride]: the pages given
- *                 up, in the order of their positions, then -1
+ *   gone        : device int32 [n_seqs][batch->table_stride], neither of the
+ *                 tables: the pages given up, in the order of their positions,
+ *                 then -1
  *   count       : device int32 [n_seqs]: how many
  * A sequence may have up to 32768 pages (batch->table_stride).
  * Errors: LW_E_ARG, LW_E_UNSUPPORTED (head_dim, page_tokens, table_stride),

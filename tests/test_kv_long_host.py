@@ -219,6 +219,15 @@ def test_refuses_the_rest():
     assert select(a, batch=wide) == evict(a, batch=wide) == dg.LW_E_UNSUPPORTED
 
 
+def test_refuses_pages_given_up_into_a_table():
+    a = Args()
+    q = a.p + 256
+    other = changed(a.batch, table=q)
+    for batch, table, gone in ((a.batch, a.p, a.p), (a.batch, q, a.p), (other, a.p, a.p), (other, q, q)):
+        assert evict(a, batch=batch, table=table, gone=gone) == dg.LW_E_ARG
+        assert "gone" in dg.lw_last_error()
+
+
 def test_empty_calls_do_nothing():
     a = Args()
     none = lw.lw_kv_tensor(None, 0, 0)
