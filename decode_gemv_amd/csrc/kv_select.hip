@@ -60,8 +60,9 @@ __device__ __forceinline__ void halve(float *x, bool upper)
 // lane takes one of them and D/4 of the dimensions (all of a key unit's, or of
 // two), in the units that kv_kword lays out: 1 KiB of the cache a load.  At the
 // end the 16 lanes of a unit share its channels out, and the wavefronts meet.
-// A page takes 5 us, most of it the latencies of the row's place, the table's
-// entry and the keys (8.5 with one wavefront, and every lane all channels).
+// A page takes 4.2 us, most of it the latencies of the row's place, the table's
+// entry and the keys (8.5 with one wavefront, and every lane all channels); where
+// no page is full, as for most tokens, workgroups end after the first, 1.7 to 2.2.
 template <int D>
 __global__ __launch_bounds__(BOUND_WAVES * 64) void k_kv_bounds(KvGeom g, uint8_t *bounds, int64_t bounds_bytes)
 {
@@ -351,7 +352,10 @@ __device__ __forceinline__ void score_tiles(const KvSelect &a, const Wanted &w, 
 }
 
 // Keys into the workspace: where few rows have many pages, many workgroups share
-// a row's.
+// a row's.  For 16 rows of 8 to 512 pages and 8 heads of 128 (7 MB of bounds) it
+// takes 6.5 us, for one row of 4096 (8.5 MB) 5.4, 1.6 TB/s: with one tile or two a
+// wavefront the chain of loads is what counts, from the row's place over the
+// entries to the bounds.
 template <int D, class T>
 __global__ __launch_bounds__(256) void k_kv_score(KvSelect a)
 {
@@ -368,7 +372,9 @@ __global__ __launch_bounds__(256) void k_kv_score(KvSelect a)
 }
 
 // The pages of a row and kv head.  THREADS a workgroup; the keys come from the
-// workspace where there is one.
+// workspace where there is one.  With those it takes 6.6 us for up to 512 pages and
+// 8.4 for 4096: passes over the keys in LDS, for each a barrier or two and one
+// wavefront's search for the counter; with the scores of 80 pages of its own 8.9.
 template <int D, class T, int THREADS>
 __global__ __launch_bounds__(THREADS) void k_kv_select(KvSelect a)
 {
@@ -442,6 +448,10 @@ __global__ __launch_bounds__(THREADS) void k_kv_select(KvSelect a)
 
 // ------------------------------------------------------------------ giving up
 
+// A workgroup has a sequence: its heads' weights are added in fp64 (their order is
+// the heads', and what is rounded once to fp32 is compared as whole numbers).  94
+// pages of 8 heads take 4.4 us; 64 sequences of 4 to 4096 pages 11.6: the longest's
+// 131 KB of weights through one CU, then the passes over its keys.
 template <int THREADS>
 __global__ __launch_bounds__(THREADS) void k_kv_evict(KvEvict a)
 {
@@ -573,6 +583,8 @@ hipError_t lw_launch_kv_select(const KvSelect &a, int head_dim, int dtype, int64
             hipLaunchKernelGGL(f, grid, dim3(threads), bytes, s, a);
             return hipGetLastError();
         };
+        // (4096 keys: 8.4 us and 10.9; 512 keys of 128 pairs 6.6, for which twice the
+        // wavefronts find no more to do)
         return pages > 1024 ? go(k_kv_select<D, T, 512>, 512) : go(k_kv_select<D, T, 256>, 256);
     });
 }
@@ -586,5 +598,7 @@ hipError_t lw_launch_kv_evict(const KvEvict &a, hipStream_t s)
         hipLaunchKernelGGL(f, dim3(a.g.n_seqs), dim3(threads), bytes, s, a);
         return hipGetLastError();
     };
+    // (64 tables of 4096 pages, 1024 threads, 512 and 256: 11.6 us, 13.9 and 19.0; one
+    // of 94: 6.1, 5.0 and 4.4)
     return a.g.stride > 1024 ? go(k_kv_evict<1024>, 1024) : go(k_kv_evict<256>, 256);
 }

@@ -1,10 +1,12 @@
 """One transformer layer served token by token: coded weights, a 4-bit key/value cache, attention over it.
 
-    python examples/cached_decode.py [--prompt 100] [--steps 8] [--batch 2]
+    python examples/cached_decode.py [--prompt 100] [--steps 8] [--batch 2] [--pages 4]
 
-The projections and the SwiGLU MLP are entropy-coded 4-bit matrices (lw_gemv); keys and values are quantised into a
-paged cache as they are made (lw_kv_append) and attended over (lw_kv_attend), first the prompt in pieces of at most 16
-tokens, then one new token a step.  A step is a fixed sequence of launches over buffers that stay in place, so it is
+The projections and the SwiGLU MLP are entropy-coded 4-bit matrices (lw_gemv); queries and keys are turned by their
+positions (lw_rope), keys and values quantised into a paged cache as they are made (lw_kv_append) and attended over
+(lw_kv_attend), first the prompt in pieces of at most 16 tokens, then one new token a step.  With --pages a step attends
+over that many pages of each sequence, chosen for each kv head by the bounds of their keys (lw_kv_bounds, lw_kv_select,
+lw_kv_attend_selected).  A step is a fixed sequence of launches over buffers that stay in place, so it is
 captured once and replayed; between steps the program moves the lengths on.  At the end the cache is read back
 (lw_kv_read) and the last step is compared with attention in fp64 over what it holds.
 """
@@ -34,16 +36,8 @@ def coded(rng, rows, cols):
     return dg.upload(dg.lw_bundle_build_q(dg.LW_Q4_PAIR, codes, d, m))
 
 
-def rotate(x, pos):
-    """Rotary position embedding of x [n][heads][DIM] at positions pos [n]."""
-    half = DIM // 2
-    angle = pos[:, None, None].float() * 10000.0 ** (-torch.arange(half, device=x.device) / half)
-    a, b = x[..., :half], x[..., half:]
-    return torch.cat((a * angle.cos() - b * angle.sin(), a * angle.sin() + b * angle.cos()), -1)
-
-
 class Layer:
-    def __init__(self, batch, longest, seed=1):
+    def __init__(self, batch, longest, chosen=0, seed=1):
         rng = np.random.default_rng(seed)
         self.qkv = coded(rng, (HEADS + 2 * KV) * DIM, HIDDEN)
         self.o = coded(rng, HIDDEN, HEADS * DIM)
@@ -56,27 +50,45 @@ class Layer:
         self.table = order.view(batch, per)
         self.lens = torch.zeros(batch, dtype=torch.int32, device="cuda")
         self.longest = longest
+        self.rope = dg.lw_rope_make(DIM // 2)
+        self.chosen = chosen                                 # pages that a new token attends over (0: all)
+        self.bounds = torch.empty(batch * per * dg.lw_kv_bounds_bytes(KV, DIM), dtype=torch.uint8, device="cuda")
 
     def batch(self, new):
         """Every sequence has `new` tokens, packed one sequence after the other."""
         start = torch.arange(0, (self.n_seqs + 1) * new, new, dtype=torch.int32, device="cuda")
         return dg.KvBatch(start, self.lens, self.table, max_len=self.longest)
 
-    def forward(self, x, pos, kv, keep):
-        """x [n][HIDDEN] fp16 at positions pos; lens already count these tokens.  keep: the step's buffers."""
+    def attend(self, q, out, kv, keep, get):
+        n = q.shape[0]
+        if not self.chosen or n > self.n_seqs:               # (the prompt: over all pages)
+            need = dg.lw_kv_attend_scratch_bytes(self.cache, kv, n, HEADS)
+            dg.lw_kv_attend(self.cache, kv, q, out, work=get("work", need, dtype=torch.uint8) if need else None)
+            return
+        whole = dict(dtype=torch.int32)
+        sel = keep["chosen"] = dg.KvSelection(get("sel start", n + 1, **whole), get("sel lens", n, **whole),
+                                              get("sel table", n, KV, self.chosen, **whole))
+        need = dg.lw_kv_select_scratch_bytes(self.cache, kv, n, HEADS)
+        dg.lw_kv_select(self.cache, kv, q, self.bounds, sel, first=min(1, self.chosen - 1), last=0,
+                        work=get("sel work", need, dtype=torch.uint8) if need else None)
+        need = dg.lw_kv_attend_selected_scratch_bytes(self.cache, sel, HEADS)
+        dg.lw_kv_attend_selected(self.cache, sel, q, out, work=get("work", need, dtype=torch.uint8) if need else None)
+
+    def forward(self, x, kv, keep):
+        """x [n][HIDDEN] fp16; lens already count these tokens.  keep: the step's buffers."""
         n = x.shape[0]
         get = lambda name, *shape, dtype=torch.float32: keep.setdefault(
             (name, n), torch.empty(shape, dtype=dtype, device="cuda"))
         y = get("qkv", n, (HEADS + 2 * KV) * DIM)
         dg.lw_gemv(self.qkv, x, y, n)
         y = y.view(n, HEADS + 2 * KV, DIM)
-        q, k, v = y[:, :HEADS], y[:, HEADS:HEADS + KV], y[:, HEADS + KV:]
-        q, k = rotate(q, pos).half(), rotate(k, pos)
+        q, k, v = get("q", n, HEADS, DIM, dtype=torch.float16), y[:, HEADS:HEADS + KV], y[:, HEADS + KV:]
+        dg.lw_rope(self.rope, y[:, :HEADS], q, batch=kv)
+        dg.lw_rope(self.rope, k, k, batch=kv)
         dg.lw_kv_append(self.cache, kv, k, v)
+        dg.lw_kv_bounds(self.cache, kv, n, self.bounds)
         a = get("attended", n, HEADS, DIM, dtype=torch.float16)
-        need = dg.lw_kv_attend_scratch_bytes(self.cache, kv, n, HEADS)
-        work = get("work", need, dtype=torch.uint8) if need else None
-        dg.lw_kv_attend(self.cache, kv, q, a, work=work)
+        self.attend(q, a, kv, keep, get)
         keep["q"], keep["a"] = q, a
         z = get("o", n, HIDDEN)
         dg.lw_gemv(self.o, a, z, n)
@@ -95,24 +107,24 @@ def main(argv=None):
     ap.add_argument("--prompt", type=int, default=100)
     ap.add_argument("--steps", type=int, default=8)
     ap.add_argument("--batch", type=int, default=2)
+    ap.add_argument("--pages", type=int, default=0, help="pages that a new token attends over (0: all)")
     a = ap.parse_args(argv)
-    if not 1 <= a.batch <= 16 or a.prompt < 1 or a.steps < 1:
-        ap.error("--batch must be in 1..16, --prompt and --steps at least 1")
+    if not 1 <= a.batch <= 16 or a.prompt < 1 or a.steps < 1 or not 0 <= a.pages <= 32768:
+        ap.error("--batch must be in 1..16, --prompt and --steps at least 1, --pages in 0..32768")
     torch.manual_seed(0)
-    layer, keep = Layer(a.batch, a.prompt + a.steps), {}
+    layer, keep = Layer(a.batch, a.prompt + a.steps, a.pages), {}
     prompt = torch.randn((a.batch, a.prompt, HIDDEN), device="cuda").half()
     done, piece = 0, 16 // a.batch                          # lw_gemv takes up to 16 rows
     while done < a.prompt:
         n = min(piece, a.prompt - done)
         layer.lens.add_(n)
-        pos = torch.arange(done, done + n, device="cuda").repeat(a.batch)
-        y = layer.forward(prompt[:, done:done + n].reshape(-1, HIDDEN).contiguous(), pos, layer.batch(n), keep)
+        y = layer.forward(prompt[:, done:done + n].reshape(-1, HIDDEN).contiguous(), layer.batch(n), keep)
         done += n
     x = y.view(a.batch, n, HIDDEN)[:, -1].contiguous()
     one, y = layer.batch(1), torch.empty_like(x)
 
     def step():
-        y.copy_(layer.forward(x, layer.lens - 1, one, keep))
+        y.copy_(layer.forward(x, one, keep))
 
     layer.lens.add_(1)
     step()                                                   # (its buffers, and the kernels' first use)
@@ -126,12 +138,17 @@ def main(argv=None):
         graph.replay()
     torch.cuda.synchronize()
 
-    # the last step against fp64 attention over the cache as it reads back
+    # the last step against fp64 attention over the cache as it reads back (the chosen pages of it)
     total = a.prompt + a.steps
     k, v = (torch.empty((a.batch * total, KV, DIM), device="cuda") for _ in range(2))
     dg.lw_kv_read(layer.cache, layer.batch(total), k, v)
     k, v = (t.view(a.batch, total, KV, DIM).double().repeat_interleave(HEADS // KV, 2) for t in (k, v))
-    p = torch.softmax((keep["q"].double()[:, None] * k).sum(-1) * DIM ** -0.5, 1)
+    scores = (keep["q"].double()[:, None] * k).sum(-1) * DIM ** -0.5
+    if a.pages:
+        mine = layer.table.repeat_interleave(PAGE, 1)[:, :total]             # each token's page
+        seen = (mine[:, :, None, None] == keep["chosen"].table[:, None]).any(-1)
+        scores = scores.masked_fill(~seen.repeat_interleave(HEADS // KV, 2), -torch.inf)
+    p = torch.softmax(scores, 1)
     want = (p[..., None] * v).sum(1)
     err = float((keep["a"].double() - want).norm() / want.norm())
     held = layer.cache.pages.numel()

@@ -358,6 +358,17 @@ def test_pages_past_four_gigabytes(torch, dg):
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("args", [["--pages", "2"], ["--prompt", "97", "--steps", "5", "--batch", "3", "--pages", "1"],
+                                  ["--prompt", "40", "--steps", "30", "--batch", "1", "--pages", "64"]])
+def test_example_over_chosen_pages(torch, dg, args):
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import cached_decode
+    # fp16 outputs (2^-11 of each) of fp32 scores
+    assert cached_decode.main(args) < 1e-3
+
+
 def test_bindings_refusals(torch, dg):
     kv, D, P = 2, 64, 32
     s = Setup(torch, dg, kv, D, P, [3], [100], 3)
