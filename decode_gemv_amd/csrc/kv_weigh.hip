@@ -9,7 +9,15 @@
 // Few rows a sequence (k_kv_weigh): the queries stay in registers and the keys
 // go past them, in equal parts of all sequences' pages for each wavefront.
 // Many (k_kv_weigh_rows): the keys stay in registers, unpacked once, and the
-// queries go past them, made into operands once a workgroup.
+// queries go past them, through LDS.
+//
+// Few rows are bound by HBM: one token on 131071, 64 heads on 8 of 128 (71 MB of
+// keys), 15.6 us, 4.6 TB/s; 16 sequences of 1 to 3 tokens on up to 8190, 32 heads
+// (37 MB), 12.2: four pages or five a wavefront, so that the chain of loads to the
+// first of them is half of that.  Many are bound by vector instructions: 1024 new
+// tokens of two sequences of 11 thousand, 32 heads on 8 of 128, 122 us, 0.70
+// PFLOP/s (16 by 16 products of operands in fp16 that every workgroup made took
+// 160).
 #include <algorithm>
 #include <type_traits>
 
@@ -99,9 +107,29 @@ struct Part {
         qsum = sum;
     }
 
-private:
-    template <class F>
-    static __device__ __forceinline__ void each(uint4 x, F f)
+    // The row times the power of two that makes its largest element 1 to 2 (0: of
+    // zeros, and what is below 2^-112 grows by no more); returns its inverse's
+    // exponent.
+    __device__ __forceinline__ int to_one()
+    {
+        float top = 0.0f;
+#pragma unroll
+        for (int j = 0; j < PER; j++)
+            each(w[j], [&](uint32_t x) { top = fmaxf(top, fmaxf(fabsf(low(x)), fabsf(high(x)))); });
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const int e = top > 0.0f ? max((int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127, -112) : 0;
+#pragma unroll
+        for (int j = 0; j < PER; j++)
+            each(w[j], [&](uint32_t &x) {
+                typedef T t2 __attribute__((ext_vector_type(2)));
+                x = __builtin_bit_cast(uint32_t, t2{(T)ldexpf(low(x), -e), (T)ldexpf(high(x), -e)});
+            });
+        return e;
+    }
+
+    template <class X, class F>
+    static __device__ __forceinline__ void each(X &x, F f)
     {
         f(x.x), f(x.y), f(x.z), f(x.w);
     }
@@ -346,36 +374,100 @@ __global__ __launch_bounds__(NW * 64) void k_kv_weigh(KvWeigh args)
 
 // ------------------------------------------------------------------ many rows
 
-// A workgroup, one a CU, has some blocks of 32 tokens of a sequence, and takes as
-// many row tiles at a time as it has wavefronts: each makes one of them into
-// operands in LDS for all (two buffers, one barrier a time; what comes after them
+// A workgroup, one a CU, has some blocks of 32 tokens of a sequence, and takes half
+// as many row tiles of 32 at a time as it has wavefronts: two wavefronts bring one
+// of them into LDS for all (two buffers, one barrier a time; what comes after them
 // is loaded before it is used).  A block is a wavefront's, or, where there are few,
 // several wavefronts', which take the row tiles in turn.  How many blocks a
 // workgroup has is worked out from the lengths: the fewest with which every CU has
 // as many turns as another.
+//
+// The codes are unpacked once, into the queries' own type, which holds them
+// exactly, and their pairs are multiplied by the scale, so that a row needs no more
+// than the sum of its elements and a score is two fused products: vector
+// instructions are what bounds this, and matrix ones hardly go on beside them
+// (those of 32 by 32 more than those of 16 by 16: 128 cycles of them and 32 fused
+// products, four wavefronts a SIMD, take 81 ns a wavefront with the small ones and
+// 70 with the large, 58 without the products).
 constexpr int TB = 32;
+
+typedef float f16x __attribute__((ext_vector_type(16)));
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+
+// What the types of a query have for themselves.
+template <class T> struct Kind;
+template <>
+struct Kind<_Float16> {
+    typedef h8 v8;
+    static __device__ __forceinline__ f16x product(h8 a, h8 b, f16x c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
+    static __device__ __forceinline__ float dot(uint32_t a, uint32_t b, float c)
+    {
+        return __builtin_amdgcn_fdot2(__builtin_bit_cast(h2, a), __builtin_bit_cast(h2, b), c, false);
+    }
+    static constexpr uint32_t ONES = 0x3C003C00u;
+};
+template <>
+struct Kind<__bf16> {
+    typedef bf8 v8;
+    static __device__ __forceinline__ f16x product(bf8 a, bf8 b, f16x c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
+    static __device__ __forceinline__ float dot(uint32_t a, uint32_t b, float c)
+    {
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf2, a), __builtin_bit_cast(bf2, b), c, false);
+    }
+    static constexpr uint32_t ONES = 0x3F803F80u;
+};
 
 template <int D>
 struct Made {                          // a row tile
-    h8 q[D / 32][64];
-    float4 row[16];                    // qs, qsum, log sum, 2^-what its rounding leaves (0: adds nothing)
-    int2 seen[16];
-    int4 tile;                         // tokens that some of its rows see, and that all do
+    uint4 q[D / 16][64];               // lane: row % 32, half the dimensions
+    float4 row[32];                    // sum of q, factor of the scores, log sum, 2^-what its rounding leaves (0: adds nothing)
+    int factors[2];                    // whether any of 16 rows' factors is not 1
 };
 
-// Wavefronts of a workgroup (registers, LDS).
+// The lane, found anew where this stands (as arguments()).
+__device__ __forceinline__ int lane_again()
+{
+    unsigned all = ~0u;
+    asm volatile("" : "+s"(all));
+    return (int)__builtin_amdgcn_mbcnt_hi(all, __builtin_amdgcn_mbcnt_lo(all, 0));
+}
+
+// A wavefront's priority by how much it has done of what lies between barriers, in
+// quarters: those behind go first, as the last alone would leave its SIMD idle
+// between dependent instructions (122 us, and 128 as the hardware chooses).
+__device__ __forceinline__ void give_way(int done)
+{
+    if (done == 0) __builtin_amdgcn_s_setprio(3);
+    else if (done == 1) __builtin_amdgcn_s_setprio(2);
+    else if (done == 2) __builtin_amdgcn_s_setprio(1);
+    else __builtin_amdgcn_s_setprio(0);
+}
+
+// What a row's token sees.
+__device__ __forceinline__ Span span_at(const KvAttend &a, const KvSeq &q, int token)
+{
+    RowTile t = {};
+    t.rows = 1;
+    t.n_new = q.n_new;
+    t.len = q.len;
+    t.tok0 = token;
+    return span_of(a, t, 0);
+}
+
+// Wavefronts of a workgroup (registers, LDS; with 12 for heads of 128, 129 us).
 template <int D> constexpr int MANY = D == 256 ? 8 : 16;
 
 template <int D, class T>
 __global__ __launch_bounds__(MANY<D> * 64) void k_kv_weigh_rows(KvWeigh args)
 {
-    constexpr int PER = D / 32;
-    constexpr int waves = MANY<D>;
-    __shared__ Made<D> made[2 * waves];
+    typedef typename Kind<T>::v8 v8;
+    constexpr int PER = D / 32, WORDS = D / 16, W = D >= 128 ? 4 : 2;
+    constexpr int waves = MANY<D>, side = waves / 2;         // row tiles at a time
+    __shared__ Made<D> made[2 * side];
     __shared__ float sums[waves];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), head = blockIdx.x;
-    const int m = lane % 16, quarter = lane / 16;
-    const Masks mk = masks();
+    const int col = lane % 32, half = lane / 32;             // of a product: row, and tokens 8 i + 4 half + 0 .. 3
     const int shift = args.a.g.page_shift, P = 1 << shift, each = P / TB;    // a page's blocks
     const int all = Line(args, [&](int n) { return n * each; }).all, groups = gridDim.y;
     if (all == 0) return;
@@ -389,125 +481,188 @@ __global__ __launch_bounds__(MANY<D> * 64) void k_kv_weigh_rows(KvWeigh args)
         const KvGeom &g = a.g;
         const KvSeq q = unit.q;
         // the unit's blocks, and wavefronts that share one
-        const int blocks = min(unit.pages * each - unit.at * most, most), ways = waves / blocks;
+        const int blocks = min(unit.pages * each - unit.at * most, most), ways = min(waves / blocks, side);
         const int way = wave / blocks, base = unit.at * most * TB, t0 = base + (wave - way * blocks) * TB;
+        // the scale, as a factor of the pairs and, where that could leave their range, a
+        // power of two of each row's scores
+        float times = a.scale;
+        int power = 0;
+        if (!(times >= 0x1p-40f && times <= 0x1p40f)) times = frexpf(times, &power);
+        power = __builtin_amdgcn_readfirstlane(power);
+        times *= 1.44269504088896341f;
         // the keys of t0 .. t0 + 31, as operands, and what makes scores of the lane's
-        // tokens (four of each 16)
-        h8 k[2][PER];
-        h2 dk[2][2];
-        float ck[2][4];
+        // tokens (four of each 8): score = acc dk + ck (sum of q), in log2 units
+        v8 k[WORDS];
+        float dk[16], ck[16];
         const int64_t page = t0 >> shift < unit.pages ? kv_page(g, q.seq, t0) : -1;
         {
-            Step<D, 16> x;
-            load_step<D, 16>(x, g.pages + max(page, (int64_t)0) * g.page_bytes + (int64_t)head * g.block_bytes,
-                         page < 0 ? 0 : g.block_bytes, P, t0 & (P - 1), lane);
+            // (bytes 0: zeros, and no traffic)
+            const auto from = __builtin_amdgcn_make_buffer_rsrc(
+                const_cast<uint8_t *>(g.pages + max(page, (int64_t)0) * g.page_bytes + (int64_t)head * g.block_bytes), 0,
+                page < 0 ? 0 : g.block_bytes, 0x00027000);
+            const int at = t0 & (P - 1), lane = lane_again(), col = lane % 32, half = lane / 32;
+            uint32_t w[WORDS];
 #pragma unroll
-            for (int u = 0; u < 2; u++) {
+            for (int j = 0; j < WORDS; j += W) {
+                const uint32_t off = 4 * kv_kword<D>(col, half * WORDS + j);
+                if constexpr (W == 4)
+                    *reinterpret_cast<uint4 *>(w + j) =
+                        __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(from, off, at * (D / 2), 0));
+                else
+                    *reinterpret_cast<uint2 *>(w + j) =
+                        __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(from, off, at * (D / 2), 0));
+            }
 #pragma unroll
-                for (int j = 0; j < PER; j++) k[u][j] = spread8(x.w[u][j], mk);
-                const uint32_t d[4] = {x.dm[u].x, x.dm[u].y, x.dm[u].z, x.dm[u].w};
+            for (int u = 0; u < 4; u++) {
+                const uint4 dm = __builtin_bit_cast(
+                    uint4, __builtin_amdgcn_raw_buffer_load_b128(from, 32 * u + 16 * half, P * D + at * 4, 0));
+                const uint32_t d[4] = {dm.x, dm.y, dm.z, dm.w};
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    dk[u][i / 2][i % 2] = halves(d[i])[0];
-                    ck[u][i] = fmaf(half_lo(d[i]), 8.0f, -half_hi(d[i]));
+                    dk[4 * u + i] = half_lo(d[i]) * times;
+                    ck[4 * u + i] = fmaf(half_lo(d[i]), 8.0f, -half_hi(d[i])) * times;
                 }
             }
+#pragma unroll
+            for (int j = 0; j < WORDS; j++)
+#pragma unroll
+                for (int i = 0; i < 8; i++) k[j][i] = (T)((float)(w[j] >> 4 * i & 15u) - 8.0f);
         }
-        // 16 rows, row tile i of the sequence: loaded, and made into operands
-        const int tiles = (q.n_new * a.group + 15) / 16;
-        Part<D, T> raw;
-        float log_sum = 0.0f;
-        auto load = [&](int i) {
-            if (i >= tiles) return;
-            const KvWeigh &b = arguments();
-            const KvAttend &a = b.a;
-            const RowTile t = tile_of<16>(a, q, i);
-            const int2 at = token_of(a, t, min(m, t.rows - 1));
-            const int64_t tok = t.row0 + at.x, h = (int64_t)head * a.group + at.y;
-            raw.load(a.q, tok, h, lane);
-            log_sum = b.lse[tok * ((int64_t)a.g.kv_heads * a.group) + h];
+        // rows' tokens and heads, without a division each
+        const int rows = q.n_new * a.group, tiles = (rows + 31) / 32, group = a.group;
+        struct Place {
+            int tok, head;
         };
-        auto put = [&](int i, Made<D> &o) {
-            if (i >= tiles) return;
-            const KvAttend &a = arguments().a;
-            const RowTile t = tile_of<16>(a, q, i);
-            float qs, qsum;
-            raw.make(qs, qsum, a.scale, [&](int j, h8 y) { o.q[j][lane] = y; });
-            const float2 lse = log2_of(log_sum);
-            const bool counts = m < t.rows && fabsf(lse.x) < __builtin_inff();
-            const Span seen = span_of(a, t, m), e = span_of(a, t, 0), f = span_of(a, t, t.rows - 1);
-            if (quarter == 0) {
-                o.row[m] = make_float4(qs, qsum, lse.x, counts ? __builtin_amdgcn_exp2f(-lse.y) : 0.0f);
-                o.seen[m] = make_int2(seen.lo, seen.hi);
-                // (a row past the last one adds nothing, whatever it sees)
-                if (m == 0) o.tile = make_int4(e.lo, f.hi, f.lo, e.hi);
+        auto place = [&](int row) {
+            const int tok = row / group;
+            return Place{tok, row - tok * group};
+        };
+        const Place hop = place(32 * side);
+        auto go_on = [&](Place &p) {
+            p.tok += hop.tok;
+            p.head += hop.head;
+            if (p.head >= group) {
+                p.head -= group;
+                p.tok++;
             }
         };
-        float total = 0.0f;
         // (rows before the first that sees the block's first token see none of it)
         int i0 = 0;
         if (a.causal) {
             const int64_t before = (int64_t)base - (q.len - q.n_new);
-            if (before > 0) i0 = (int)min(before * a.group / 16, (int64_t)tiles) / waves * waves;
+            if (before > 0) i0 = (int)min(before * group / 32, (int64_t)tiles) / side * side;
         }
-        int turn = 0;
-        load(i0 + wave);
-        put(i0 + wave, made[wave]);
-        load(i0 + waves + wave);
-        for (int i = i0; i < tiles; i += waves, turn ^= 1) {
-            __syncthreads();
-            put(i + waves + wave, made[(turn ^ 1) * waves + wave]);
-            load(i + 2 * waves + wave);
-            const Made<D> *o = made + turn * waves;
-            const int have = min(tiles - i, waves);
-            const int4 tile = o[min(lane, have - 1)].tile;
-            h8 y[PER];
-            float4 row;
-            auto fetch = [&](int n) {
+        // this wavefront's 16 rows of the row tile that is `coming`: loaded, and put
+        // into LDS
+        int coming = i0 + wave / 2;
+        Place mine = place(32 * coming + wave % 2 * 16 + lane_again() % 16);
+        Part<D, T> raw;
+        float log_sum = 0.0f;
+        auto load = [&] {
+            if (coming >= tiles) return;
+            const KvWeigh &b = arguments();
+            const int lane = lane_again();
+            const bool in = 32 * coming + wave % 2 * 16 + lane % 16 < rows;     // (past the last one: that one)
+            const int64_t tok = q.row0 + (in ? mine.tok : q.n_new - 1);
+            const int64_t h = (int64_t)head * group + (in ? mine.head : group - 1);
+            raw.load(b.a.q, tok, h, lane);
+            log_sum = b.lse[tok * ((int64_t)b.a.g.kv_heads * group) + h];
+        };
+        auto put = [&](Made<D> &o) {
+            if (coming >= tiles) return;
+            const int lane = lane_again(), own = wave % 2 * 16 + lane % 16, quarter = lane / 16;
+            float sum = 0.0f, squares = 0.0f;
+            auto count = [&] {
+                sum = squares = 0.0f;
 #pragma unroll
-                for (int j = 0; j < PER; j++) y[j] = o[n].q[j][lane];
-                row = o[n].row[m];
+                for (int j = 0; j < PER; j++)
+                    Part<D, T>::each(raw.w[j], [&](uint32_t x) {
+                        sum = Kind<T>::dot(x, Kind<T>::ONES, sum);
+                        squares = Kind<T>::dot(x, x, squares);
+                    });
+                sum += __shfl_xor(sum, 16);
+                squares += __shfl_xor(squares, 16);
+                sum += __shfl_xor(sum, 32);
+                squares += __shfl_xor(squares, 32);
             };
-            if (way >= ways) continue;                       // (makes tiles, and has no block)
-            fetch(min(way, have - 1));
-            for (int n = way; n < have; n += ways) {
-                f4 acc[2];
-#pragma unroll
-                for (int u = 0; u < 2; u++) {
-                    acc[u] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int j = 0; j < PER; j++) acc[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[u][j], y[j], acc[u], 0, 0, 0);
-                }
-                const float4 now = row;
-                fetch(min(n + ways, have - 1));             // the next one's, while this one's are worked on
-                const int lo = __builtin_amdgcn_readlane(tile.x, n), hi = __builtin_amdgcn_readlane(tile.y, n);
-                if (lo >= t0 + TB || hi <= t0) continue;
-                const bool every = __builtin_amdgcn_readlane(tile.z, n) <= t0 && __builtin_amdgcn_readlane(tile.w, n) >= t0 + TB;
-                float p[2][4], sum = 0.0f;
-#pragma unroll
-                for (int u = 0; u < 2; u++)
-#pragma unroll
-                    for (int x = 0; x < 4; x++)
-                        p[u][x] = __builtin_amdgcn_exp2f(fmaf(fmaf(acc[u][x], (float)dk[u][x / 2][x % 2], ck[u][x] * now.y), now.x, -now.z));
-                if (!every) {
-                    const int2 seen = o[n].seen[m];
-                    const unsigned first = t0 + 4 * quarter - seen.x, many = seen.y - seen.x;
-#pragma unroll
-                    for (int u = 0; u < 2; u++)
-#pragma unroll
-                        for (int x = 0; x < 4; x++) p[u][x] = first + 16 * u + x < many ? p[u][x] : 0.0f;
-                }
-#pragma unroll
-                for (int u = 0; u < 2; u++)
-#pragma unroll
-                    for (int x = 0; x < 4; x++) sum += p[u][x];
-                total += now.w != 0.0f ? sum * now.w : 0.0f;
+            count();
+            int by = power;
+            // rows whose products could leave fp32's range: brought to 1 by a power of two
+            if (__any(!(squares >= 0x1p-100f && squares < 0x1p100f))) {
+                by += raw.to_one();
+                count();
             }
+#pragma unroll
+            for (int j = 0; j < PER; j++) o.q[quarter % 2 * PER + j][quarter / 2 * 32 + own] = raw.w[j];
+            const float2 lse = log2_of(log_sum);
+            const bool counts = 32 * coming + own < rows && fabsf(lse.x) < __builtin_inff();
+            if (quarter == 0)
+                o.row[own] = make_float4(sum, ldexpf(1.0f, min(max(by, -126), 127)), lse.x,
+                                         counts ? __builtin_amdgcn_exp2f(-lse.y) : 0.0f);
+            const int factors = __any(by != 0);
+            if (lane == 0) o.factors[wave % 2] = factors;
+        };
+        auto next = [&] {
+            coming += side;
+            go_on(mine);
+        };
+        float total = 0.0f;
+        int turn = 0;
+        Place first = place(32 * (i0 + min(lane_again(), side)));            // of row tile `lane` of those in LDS
+        load();
+        for (int i = i0 - side; i < tiles; i += side, turn ^= 1) {
+            __syncthreads();
+            put(made[turn * side + wave / 2]);
+            next();
+            load();
+            // (nothing is there yet; or the wavefront brings tiles, and has no block)
+            if (i < i0 || way >= ways) continue;
+            const Made<D> *o = made + (turn ^ 1) * side;
+            const int have = min(tiles - i, side);
+            // of row tile `lane`: the tokens that some of its rows see, and that all do
+            const int more = min(max(rows - 32 * (i + lane), 1), 32) - 1;
+            const int last = first.tok + (int)((unsigned)(first.head + more) * a.group_inv >> 21);
+            const Span e = span_at(arguments().a, q, first.tok), f = span_at(arguments().a, q, last);
+            const int2 factor = *reinterpret_cast<const int2 *>(o[min(lane, have - 1)].factors);
+            const uint64_t some = __ballot(e.lo < t0 + TB && f.hi > t0), every = __ballot(f.lo <= t0 && e.hi >= t0 + TB);
+            const uint64_t plain = __ballot(!(factor.x | factor.y));
+            for (int n = way; n < have; n += ways) {
+                if (!(some >> n & 1)) continue;
+                give_way(n / (side / 4));
+                const float4 row = o[n].row[col];
+                f16x acc = {};
+#pragma unroll
+                for (int j = 0; j < WORDS; j++) acc = Kind<T>::product(k[j], __builtin_bit_cast(v8, o[n].q[j][lane]), acc);
+                if (plain >> n & 1) {
+#pragma unroll
+                    for (int x = 0; x < 16; x++) acc[x] = fmaf(acc[x], dk[x], fmaf(ck[x], row.x, -row.z));
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 16; x++) acc[x] = fmaf(fmaf(acc[x], dk[x], ck[x] * row.x), row.y, -row.z);
+                }
+#pragma unroll
+                for (int x = 0; x < 16; x++) acc[x] = __builtin_amdgcn_exp2f(acc[x]);
+                if (!(every >> n & 1)) {
+                    const KvAttend &a = arguments().a;
+                    const unsigned row0 = __builtin_amdgcn_readlane(first.head, n) + col;
+                    const Span seen = span_at(a, q, __builtin_amdgcn_readlane(first.tok, n) + (int)(row0 * a.group_inv >> 21));
+                    const unsigned from = t0 + 4 * half - seen.lo, many = seen.hi - seen.lo;
+#pragma unroll
+                    for (int x = 0; x < 16; x++) acc[x] = from + x / 4 * 8 + x % 4 < many ? acc[x] : 0.0f;
+                }
+#pragma unroll
+                for (int m = 8; m; m /= 2)
+#pragma unroll
+                    for (int x = 0; x < m; x++) acc[x] += acc[x + m];
+                total += row.w != 0.0f ? acc[0] * row.w : 0.0f;
+            }
+            give_way(3);
+            go_on(first);
         }
         total = all_lanes(total);
         if (lane == 0) sums[wave] = total;
         __syncthreads();
-        const int at = threadIdx.x, j = (base >> shift) + at;
+        const int at = wave * 64 + lane_again(), j = (base >> shift) + at;
         if (at * each < blocks) {
             const KvWeigh &b = arguments();
             const KvGeom &g = b.a.g;

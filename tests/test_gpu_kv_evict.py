@@ -172,6 +172,44 @@ def test_weights_that_are_special(torch, dg):
     give_up(torch, dg, 3, 32, table[:, :4], [4 * 32], w, 12, 3, 0, 1)
 
 
+@pytest.mark.parametrize("new", [[2], [50]], ids=["few", "many"])
+@pytest.mark.parametrize("D,power", [(64, 60), (128, -60), (128, 100), (256, -100), (64, 45), (256, 38)])
+def test_weights_of_queries_and_scales_far_from_one(torch, dg, new, D, power):
+    """Products that leave fp32's range unless a power of two goes from the queries to the scale or back; among them rows of
+    other sizes, whose scores are all but nothing, and rows of zeros."""
+    kv, group, P = 1, 3, 64
+    s = Setup(torch, dg, kv, D, P, new, [200], 11).fill()
+    q = queries(s, group, "bf16") * 2.0 ** power
+    q[0, 1] *= 2.0 ** -70 if power > 0 else 2.0 ** -20
+    q[new[0] // 2, 0] = 0
+    q[-1, 2] *= 2.0 ** -30
+    scale = 1.3 * D ** -0.5 * 2.0 ** -power
+    out, lse = torch.empty_like(q), torch.empty((s.rows, kv * group), device="cuda")
+    dg.lw_kv_attend(s.cache, s.batch, q, out, scale=scale, lse=lse)
+    weights = torch.full((1, kv, s.table.shape[1]), 9.0, device="cuda")
+    dg.lw_kv_weigh(s.cache, s.batch, q, lse, weights, scale=scale)
+    w, used, err = L.weigh(R.Cache(s.image, kv, D, P), s.table, s.start, s.lens, host(q), host(lse), scale, True, 0, weights.shape[2])
+    got = host(weights)
+    assert np.all(np.abs(got - w)[used[:, None]] <= err[used[:, None]] + 2.0 ** -22 * w[used[:, None]])
+    assert abs(got[0, 0][used[0]].sum() - new[0] * group) < 1e-3 * new[0] * group
+
+
+@pytest.mark.parametrize("new", [[1], [30]], ids=["few", "many"])
+def test_weights_of_half_precision_queries_under_a_small_scale(torch, dg, new):
+    """Scores of all but nothing: every token that a row sees has the same weight."""
+    s = Setup(torch, dg, 2, 128, 64, new, [180], 5).fill()
+    q = queries(s, 2, "fp16")
+    q[0, 0] = 65504
+    q[-1, 3] = 0
+    n = new[0]
+    lse = torch.log(torch.arange(180 - n + 1, 181, device="cuda").float())[:, None].expand(n, 4).contiguous()
+    weights = torch.empty((1, 2, 3), device="cuda")
+    dg.lw_kv_weigh(s.cache, s.batch, q, lse, weights, scale=2.0 ** -70)
+    seen = np.arange(180 - n + 1, 181)
+    want = [2 * (np.clip(seen - 64 * j, 0, 64) / seen).sum() for j in range(3)]
+    assert np.allclose(host(weights)[0], [want, want], rtol=2.0 ** -16, atol=0)
+
+
 def test_equal_weights_give_up_the_first(torch, dg):
     n = 3000
     table = np.random.default_rng(2).permutation(n).astype(np.int32)[None]
