@@ -17,8 +17,7 @@ namespace {
 
 constexpr int PICK_MOST = 32768;       // keys (their counts fit 16 bits)
 
-// Keys are 0 (never taken), MUST (always) or between.  They come in fours, with
-// zeros after the last one.
+// Keys are 0 (never taken), MUST (always) or between.
 constexpr uint32_t MUST = ~0u;
 
 // What a workgroup's keys are, of the last two those between.
@@ -43,12 +42,10 @@ __device__ __forceinline__ uint32_t ordered(float x)
     return u >> 31 ? ~u : u | 0x80000000u;
 }
 
-template <class F>
-__device__ __forceinline__ void each_of(uint4 x, F f)
+// The bits of lanes before this one.
+__device__ __forceinline__ int below(uint64_t x)
 {
-    const uint32_t k[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int j = 0; j < 4; j++) f(j, k[j]);
+    return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(x >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)x, 0));
 }
 
 // The largest of x over the lanes up to this one (prefix() has the steps).
@@ -108,30 +105,39 @@ struct Tally {
 // and two numbers that a wavefront leaves for the others.
 constexpr int PICK_ROW = 36, PICK_HIST = 64 * PICK_ROW, PICK_WORDS = 2 * PICK_HIST + 4;
 
+// Keys whose loads are under way at once.
+constexpr int PICK_AT_ONCE = 2;
+
 // The cut that takes all that must be and so many of the others that they are m
-// (fewer than there are).  hist: PICK_WORDS of LDS; it and the keys are 16-byte
-// aligned.  One wavefront looks for the counter (all of a large workgroup doing
-// so took longer than the barrier after it).
+// (fewer than there are).  hist: PICK_WORDS of LDS, 16-byte aligned.  One wavefront
+// looks for the counter (all of a large workgroup doing so took longer than the
+// barrier after it).
 template <int T>
-__device__ __forceinline__ Cut pick_cut(const uint32_t *key, int quads, Keys all, int m, uint32_t *hist)
+__device__ __forceinline__ Cut pick_cut(const uint32_t *key, int n, Keys all, int m, uint32_t *hist)
 {
     constexpr int BITS[3] = {11, 11, 10}, SHIFT[3] = {21, 10, 0};
-    const int lane = threadIdx.x & 63;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     Cut c = {all.least, 0, 0, 0, m - (int)all.must};
     if (c.ties <= 0) return {0, 0, ~0u, ~0u, 0};             // (none of them)
     c.up = __builtin_clz(max(all.most - all.least, 1u));
-    for (int i = threadIdx.x; i < PICK_HIST; i += T) hist[i] = 0;
+    for (int i = threadIdx.x; i < PICK_HIST / 4; i += T) reinterpret_cast<uint4 *>(hist)[i] = uint4{};
 #pragma unroll
     for (int pass = 0; pass < 3; pass++) {
         uint32_t *h = hist + pass % 2 * PICK_HIST, *next = hist + (pass + 1) % 2 * PICK_HIST;
         uint2 *found = reinterpret_cast<uint2 *>(hist + 2 * PICK_HIST);
         __syncthreads();
-#pragma unroll 2
-        for (int i = threadIdx.x; i < quads; i += T)
-            each_of(reinterpret_cast<const uint4 *>(key)[i], [&](int, uint32_t k) {
-                const uint32_t x = (k - c.least) << c.up >> SHIFT[pass] & ((1u << BITS[pass]) - 1);
-                if (k - 1 < MUST - 1 && c.place(k) == c.value) atomicAdd(&h[x / 32 * PICK_ROW + x % 32], 1u);
-            });
+        for (int i0 = wave * 64; i0 < n; i0 += PICK_AT_ONCE * T) {
+            uint32_t k[PICK_AT_ONCE];
+#pragma unroll
+            for (int i = 0; i < PICK_AT_ONCE; i++) k[i] = key[min(i0 + i * T + lane, n - 1)];
+#pragma unroll
+            for (int i = 0; i < PICK_AT_ONCE; i++) {
+                if (i0 + i * T >= n) break;
+                const uint32_t x = (k[i] - c.least) << c.up >> SHIFT[pass] & ((1u << BITS[pass]) - 1);
+                if (i0 + i * T + lane < n && k[i] - 1 < MUST - 1 && c.place(k[i]) == c.value)
+                    atomicAdd(&h[x / 32 * PICK_ROW + x % 32], 1u);
+            }
+        }
         __syncthreads();
         if (threadIdx.x < 64) {
             // rows from the last on, one a lane, then the counters of one row
@@ -146,7 +152,8 @@ __device__ __forceinline__ Cut pick_cut(const uint32_t *key, int quads, Keys all
             // what the counter has, and what is taken of it; the counter
             if (lane == i) *found = make_uint2((uint32_t)in << 16 | (uint32_t)(c.ties - (upto - in)), (63 - r) * 32 + 31 - i);
         } else {
-            for (int i = threadIdx.x - 64; i < PICK_HIST; i += T - 64) next[i] = 0;       // (last read before the barrier above)
+            for (int i = threadIdx.x - 64; i < PICK_HIST / 4; i += T - 64)         // (last read before the barrier above)
+                reinterpret_cast<uint4 *>(next)[i] = uint4{};
         }
         __syncthreads();
         const uint2 f = *found;
@@ -159,39 +166,58 @@ __device__ __forceinline__ Cut pick_cut(const uint32_t *key, int quads, Keys all
 }
 
 // put(place, rank) for each key taken (all that are there where `every`), rank by
-// rank; returns their number.  sums: T / 64 words of LDS.
+// rank; returns their number.  sums: T / 64 words of LDS.  A wavefront has its share
+// of the keys 64 at a time, whose ranks are counts of bits: what this takes is how
+// many instructions wait for the one before.
 template <int T, class F>
-__device__ __forceinline__ int pick_each(const uint32_t *key, int quads, bool every, Cut c, uint32_t *sums, F put)
+__device__ __forceinline__ int pick_each(const uint32_t *key, int n, bool every, Cut c, uint32_t *sums, F put)
 {
-    const int each = (quads + T - 1) / T, i0 = min((int)threadIdx.x * each, quads), i1 = min(i0 + each, quads);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint32_t mine = 0;                                       // taken for sure, and on the cut << 16
-    auto four = [&](int i, auto f) {
-        each_of(reinterpret_cast<const uint4 *>(key)[i], [&](int j, uint32_t k) {
-            const uint32_t y = c.place(k);
-            const bool is = k != 0 && (every || k == MUST || y > c.value);
-            f(4 * i + j, is, k != 0 && !is && y == c.value);
-        });
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int share = ((n + 63) / 64 + T / 64 - 1) / (T / 64) * 64, i0 = min(wave * share, n), i1 = min(i0 + share, n);
+    // f(key's place, whether it is taken for sure, whether it is on the cut)
+    auto each = [&](auto f) {
+        for (int i = i0; i < i1; i += PICK_AT_ONCE * 64) {
+            uint32_t k[PICK_AT_ONCE];
+#pragma unroll
+            for (int j = 0; j < PICK_AT_ONCE; j++) k[j] = key[min(i + j * 64 + lane, n - 1)];
+#pragma unroll
+            for (int j = 0; j < PICK_AT_ONCE; j++) {
+                const int at = i + j * 64 + lane;
+                if (at - lane >= i1) break;
+                const uint32_t y = c.place(k[j]);
+                const bool there = at < i1 && k[j] != 0, is = there && (every || k[j] == MUST || y > c.value);
+                f(at, is, there && !is && y == c.value);
+            }
+        }
     };
-#pragma unroll 2
-    for (int i = i0; i < i1; i++) four(i, [&](int, bool is, bool tie) { mine += is ? 1u : tie ? 0x10000u : 0u; });
-    const uint32_t upto = prefix(mine);
-    if (lane == 63) sums[wave] = upto;
+    uint32_t mine = 0;                                       // taken for sure, and on the cut << 16
+    each([&](int, bool is, bool tie) { mine += is ? 1u : tie ? 0x10000u : 0u; });
+    mine = prefix(mine);
+    if (lane == 63) sums[wave] = mine;
     __syncthreads();
-    uint32_t before = upto - mine, all = 0;
+    uint32_t before = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < T / 64; w++) {
         if (w < wave) before += sums[w];
         all += sums[w];
     }
-    if (mine) {
-        int above = before & 0xFFFFu, on = before >> 16;
-        for (int i = i0; i < i1; i++)
-            four(i, [&](int place, bool is, bool tie) {
-                if (is || (tie && on < c.ties)) put(place, above + min(on, c.ties));
-                above += is;
-                on += tie;
-            });
+    before = __builtin_amdgcn_readfirstlane(before);
+    int above = before & 0xFFFFu, on = before >> 16;
+    if ((int)(all >> 16) <= c.ties) {                        // (mostly: all on the cut are taken)
+        above += on;
+        each([&](int place, bool is, bool tie) {
+            const uint64_t taken = __ballot(is || tie);
+            if (is || tie) put(place, above + below(taken));
+            above += __popcll(taken);
+        });
+    } else {
+        each([&](int place, bool is, bool tie) {
+            const uint64_t sure = __ballot(is), ties = __ballot(tie);
+            const int rank = on + below(ties);
+            if (is || (tie && rank < c.ties)) put(place, above + below(sure) + min(rank, c.ties));
+            above += __popcll(sure);
+            on += __popcll(ties);
+        });
     }
     return (int)(all & 0xFFFFu) + min((int)(all >> 16), c.ties);
 }

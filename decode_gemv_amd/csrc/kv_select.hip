@@ -394,11 +394,10 @@ __global__ __launch_bounds__(THREADS) void k_kv_select(KvSelect a)
         a.start[row] = min(max(row, b0), b1);
         if (row + 1 == a.g.n_tokens) a.start[row + 1] = b1;
     }
-    const int n = w.q.seq < 0 ? 0 : w.n, quads = (n + 3) / 4;
+    const int n = w.q.seq < 0 ? 0 : w.n;
     int got = 0;
     if (n > 0 && a.take > 1) {
         Tally tally;
-        if (threadIdx.x < (unsigned)(4 * quads - n)) key[n + threadIdx.x] = 0;
         if (n < a.take) {                                    // all of them that are present
             for (int j = threadIdx.x; j < n; j += THREADS) {
                 key[j] = (uint32_t)w.pages[j] < a.g.n_pages;
@@ -431,15 +430,15 @@ __global__ __launch_bounds__(THREADS) void k_kv_select(KvSelect a)
         const Keys all = tally.meet<THREADS>(sums + 4 * (THREADS / 64), nothing);
         const bool every = (int)all.there < a.take;
         Cut c = {};
-        if (!every) c = pick_cut<THREADS>(key, quads, all, a.take - 1, hist);
+        if (!every) c = pick_cut<THREADS>(key, n, all, a.take - 1, hist);
         // (their places first: one load's latency then for all of them)
         uint16_t *list = reinterpret_cast<uint16_t *>(hist);
         if (a.take <= 4 * PICK_HIST) {
-            got = pick_each<THREADS>(key, quads, every, c, sums, [&](int j, int rank) { list[rank] = (uint16_t)j; });
+            got = pick_each<THREADS>(key, n, every, c, sums, [&](int j, int rank) { list[rank] = (uint16_t)j; });
             __syncthreads();
             for (int i = threadIdx.x; i < got; i += THREADS) to[i] = w.pages[list[i]];
         } else {
-            got = pick_each<THREADS>(key, quads, every, c, sums, [&](int j, int rank) { to[rank] = w.pages[j]; });
+            got = pick_each<THREADS>(key, n, every, c, sums, [&](int j, int rank) { to[rank] = w.pages[j]; });
         }
     }
     for (int i = got + threadIdx.x; i < a.take; i += THREADS) to[i] = i == got && !none ? last : -1;
@@ -465,10 +464,9 @@ __global__ __launch_bounds__(THREADS) void k_kv_evict(KvEvict a)
     const int used = (int)(((int64_t)len + (1 << a.g.page_shift) - 1) >> a.g.page_shift), n = min(used, stride);
     const float *w = a.weights + s * a.g.kv_heads * a.stride;
     const int known = (int)min((int64_t)n, a.stride);
-    const int quads = (n + 3) / 4;
     uint32_t here = 0;
     Tally tally;
-    for (int j0 = threadIdx.x; j0 < (stride + 3) / 4 * 4; j0 += 2 * THREADS) {
+    for (int j0 = threadIdx.x; j0 < stride; j0 += 2 * THREADS) {
         // (two pages and eight heads at once: their loads' latency is what this takes)
         double sum[2] = {0.0, 0.0};
         int32_t entry[2];
@@ -494,7 +492,7 @@ __global__ __launch_bounds__(THREADS) void k_kv_evict(KvEvict a)
             const float total = (float)sum[i] + 0.0f;        // (-0 counts as 0)
             // the lowest weight has the largest key; at least 1
             const uint32_t k = !spare ? 0u : j < known && total == total ? ~ordered(total) : 1u;
-            if (j < 4 * quads) {
+            if (j < n) {
                 key[j] = k;
                 tally.add(k);
             }
@@ -508,8 +506,8 @@ __global__ __launch_bounds__(THREADS) void k_kv_evict(KvEvict a)
     if (drop) {
         const bool every = drop == (int)all.there;
         Cut c = {};
-        if (!every) c = pick_cut<THREADS>(key, quads, all, drop, hist);
-        got = pick_each<THREADS>(key, quads, every, c, sums + THREADS / 64, [&](int j, int rank) {
+        if (!every) c = pick_cut<THREADS>(key, n, all, drop, hist);
+        got = pick_each<THREADS>(key, n, every, c, sums + THREADS / 64, [&](int j, int rank) {
             gone[rank] = from[j];
             to[j] = -1;
         });
