@@ -1,5 +1,6 @@
 """MI355X (gfx950) GEMV over losslessly entropy-coded LLM weights, and a 4-bit
-key/value cache with the attention that reads it.
+key/value cache with the attention that reads it, all of it or the pages of a
+long sequence that matter.
 
 The product is the C-ABI library liblw.so (include/lw.h); this package holds
 its HIP/C++ sources (csrc/), the build script and a thin ctypes binding (lw)

@@ -372,9 +372,10 @@ __global__ __launch_bounds__(256) void k_kv_score(KvSelect a)
 }
 
 // The pages of a row and kv head.  THREADS a workgroup; the keys come from the
-// workspace where there is one.  With those it takes 6.6 us for up to 512 pages and
-// 8.4 for 4096: passes over the keys in LDS, for each a barrier or two and one
-// wavefront's search for the counter; with the scores of 80 pages of its own 8.9.
+// workspace where there is one.  With those it takes 5.4 us for up to 512 pages and
+// 9.2 for 4096: passes over the keys in LDS, for each a barrier or two and one
+// wavefront's search for the counter; with the scores of 80 pages of its own 8.2,
+// a third each for the row's place, the scores and the choice.
 template <int D, class T, int THREADS>
 __global__ __launch_bounds__(THREADS) void k_kv_select(KvSelect a)
 {
@@ -449,7 +450,7 @@ __global__ __launch_bounds__(THREADS) void k_kv_select(KvSelect a)
 
 // A workgroup has a sequence: its heads' weights are added in fp64 (their order is
 // the heads', and what is rounded once to fp32 is compared as whole numbers).  94
-// pages of 8 heads take 4.4 us; 64 sequences of 4 to 4096 pages 11.6: the longest's
+// pages of 8 heads take 3.6 us; 64 sequences of 4 to 4096 pages 11.3: the longest's
 // 131 KB of weights through one CU, then the passes over its keys.
 template <int THREADS>
 __global__ __launch_bounds__(THREADS) void k_kv_evict(KvEvict a)
@@ -553,9 +554,9 @@ hipError_t lw_launch_kv_bounds(const KvGeom &g, int head_dim, uint8_t *bounds, i
 
 bool lw_kv_select_shared(int kv_heads, int64_t n_tokens, int64_t pages)
 {
-    // With workgroups of their own for the scores, and in the choice's: 128 pairs on
-    // 512 pages 13.1 us and 15.2 (two launches and one), 124 on 391 of heads of 256
-    // 13.2 and 17.5, 8 on 4096 14.1 and 55.  8 pairs on 80: 8.9 in one.
+    // Bounds, choice and attention with workgroups of their own for the scores, and
+    // with the choice's: 128 pairs on up to 512 pages 30.5 us and 33.2, 100 on 391 of
+    // heads of 256 35.4 and 38.7, 8 on 4096 27.9 and 61.3, 8 on 80 22.0 and 21.6.
     return n_tokens > 0 && kv_heads * n_tokens <= KV_SHARED_PAIRS && pages >= 256;
 }
 
@@ -581,8 +582,8 @@ hipError_t lw_launch_kv_select(const KvSelect &a, int head_dim, int dtype, int64
             hipLaunchKernelGGL(f, grid, dim3(threads), bytes, s, a);
             return hipGetLastError();
         };
-        // (4096 keys: 8.4 us and 10.9; 512 keys of 128 pairs 6.6, for which twice the
-        // wavefronts find no more to do)
+        // (with 512 and 256, bounds and attention with them: 4096 pages 27.9 us and 30.9,
+        // 80 pages 23.1 and 21.6)
         return pages > 1024 ? go(k_kv_select<D, T, 512>, 512) : go(k_kv_select<D, T, 256>, 256);
     });
 }
@@ -596,7 +597,7 @@ hipError_t lw_launch_kv_evict(const KvEvict &a, hipStream_t s)
         hipLaunchKernelGGL(f, dim3(a.g.n_seqs), dim3(threads), bytes, s, a);
         return hipGetLastError();
     };
-    // (64 tables of 4096 pages, 1024 threads, 512 and 256: 11.6 us, 13.9 and 19.0; one
-    // of 94: 6.1, 5.0 and 4.4)
+    // (64 tables of 4096 pages, 1024 threads, 512 and 256: 11.6 us, 13.0 and 18.9; one
+    // of 94: 5.6, 5.1 and 4.5)
     return a.g.stride > 1024 ? go(k_kv_evict<1024>, 1024) : go(k_kv_evict<256>, 256);
 }

@@ -15,7 +15,7 @@
 // keys), 15.6 us, 4.6 TB/s; 16 sequences of 1 to 3 tokens on up to 8190, 32 heads
 // (37 MB), 12.2: four pages or five a wavefront, so that the chain of loads to the
 // first of them is half of that.  Many are bound by vector instructions: 1024 new
-// tokens of two sequences of 11 thousand, 32 heads on 8 of 128, 122 us, 0.70
+// tokens of two sequences of 11 thousand, 32 heads on 8 of 128, 115 us, 0.74
 // PFLOP/s (16 by 16 products of operands in fp16 that every workgroup made took
 // 160).
 #include <algorithm>
@@ -435,7 +435,8 @@ __device__ __forceinline__ int lane_again()
 
 // A wavefront's priority by how much it has done of what lies between barriers, in
 // quarters: those behind go first, as the last alone would leave its SIMD idle
-// between dependent instructions (122 us, and 128 as the hardware chooses).
+// between dependent instructions (122 us, and 128 as the hardware chooses, in one
+// run).
 __device__ __forceinline__ void give_way(int done)
 {
     if (done == 0) __builtin_amdgcn_s_setprio(3);
@@ -455,7 +456,8 @@ __device__ __forceinline__ Span span_at(const KvAttend &a, const KvSeq &q, int t
     return span_of(a, t, 0);
 }
 
-// Wavefronts of a workgroup (registers, LDS; with 12 for heads of 128, 129 us).
+// Wavefronts of a workgroup (registers, LDS; heads of 128 with 16 122 us, with 12
+// 129, in one run).
 template <int D> constexpr int MANY = D == 256 ? 8 : 16;
 
 template <int D, class T>
