@@ -66,6 +66,19 @@ def test_weights(torch, dg, case):
             assert abs(got.sum() - sum(new) * kv * group) < 1e-3 * sum(new) * kv * group
 
 
+@pytest.mark.parametrize("case", [
+    # as many heads as there may be, row tiles that end inside a token, more blocks than the chip has wavefronts for, many
+    # sequences of many rows, one with few among them
+    (1, 1024, 64, 32, [1], [70], True, 0, "fp16", "dense"), (1, 70, 128, 64, [1, 2], [140, 70], True, 0, "bf16", "heads first"),
+    (1000, 1, 64, 32, [1], [40], True, 0, "bf16", "dense"), (300, 1, 64, 32, [20], [100], True, 0, "bf16", "dense"),
+    (32, 1, 64, 32, [40], [6000], True, 0, "fp16", "dense"), (16, 2, 128, 256, [33], [5000], True, 3000, "bf16", "fused"),
+    (2, 4, 64, 32, [9] * 30 + [0, 60, 1], [40] * 30 + [5, 400, 333], True, 25, "fp16", "misaligned"),
+    (8, 2, 256, 64, [40], [2500], False, 0, "bf16", "dense")],
+    ids=["group1024", "group70", "kv1000", "kv300", "kv32_long", "P256_long", "mixed", "D256_long"])
+def test_weights_at_the_ends_of_the_ranges(torch, dg, case):
+    test_weights(torch, dg, case)
+
+
 @pytest.mark.parametrize("new", [[1, 1], [30, 30]], ids=["few", "many"])
 def test_weights_of_absent_pages_and_rows_without_a_log_sum(torch, dg, new):
     kv, group, D, P = 1, 2, 64, 32

@@ -130,6 +130,14 @@ def test_selections_are_exact_and_attention_over_them(torch, dg, case):
     attend_over(torch, dg, s, sel, q, dtype, how)
 
 
+@pytest.mark.parametrize("case", [(1, 1024, 64, 32, [1], [300], 0, 1, 3, "bf16", "dense"),
+                                  (2, 70, 128, 64, [1, 2], [640, 129], 1, 0, 4, "fp16", "heads first"),
+                                  (1024, 1, 64, 32, [1], [200], 0, 0, 4, "fp16", "dense")],
+                         ids=["group1024", "group70", "kv1024"])
+def test_as_many_heads_as_there_may_be(torch, dg, case):
+    test_selections_are_exact_and_attention_over_them(torch, dg, case)
+
+
 def attend_over(torch, dg, s, sel, q, dtype, how, lse=True):
     """Attention over a selection, with work and without, against fp64; rows of no sequence keep what they have."""
     kv, D, P, heads = s.kv, s.D, s.P, q.shape[1]
