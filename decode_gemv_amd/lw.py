@@ -641,33 +641,40 @@ def lw_kv_attend(cache: KvCache, batch: KvBatch, q, out, scale: float | None = N
 # (Small calls take as long as their way to the GPU: what is checked here is checked once, and addresses are passed as
 # numbers.)
 
-def _here(t) -> bool:
-    """Whether a tensor lies on the current device, on whose stream the call goes."""
-    d = t.get_device()                                       # (-1: in host memory)
-    return d >= 0 and d == _torch._C._cuda_getDevice()
+def _device() -> int:
+    """The current device, on whose stream a call goes, as tensors number it (-1 would be host memory)."""
+    try:
+        return _torch._C._cuda_getDevice()
+    except (AttributeError, RuntimeError):                   # no GPU: no tensor is there
+        return -2
 
 
-def _addr(t, what: str) -> int:
+def _queue(stream, dev: int) -> int:
+    """Handle of the stream a call goes to, once its tensors have been found on device dev."""
+    return _torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _addr(t, what: str, dev: int | None = None) -> int:
     """Address of a contiguous tensor on the current device."""
     try:
-        if _here(t) and t.is_contiguous():
+        if t.get_device() == (_device() if dev is None else dev) and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         pass
     raise LwError(LW_E_ARG, f"{what} must be a contiguous tensor on the current device")
 
 
-def _typed(t, what: str, dtype, want: str) -> int:
-    p = _addr(t, what)
+def _typed(t, what: str, dtype, want: str, dev: int | None = None) -> int:
+    p = _addr(t, what, dev)
     if t.dtype is not dtype:
         raise LwError(LW_E_ARG, f"{what} must be {want}")
     return p
 
 
-def _vectors(t, what: str, dim: int | None = None):
+def _vectors(t, what: str, dim: int | None = None, dev: int | None = None):
     """Descriptor of a packed device tensor [n][heads][dim] with any row and head strides, and its shape."""
     try:
-        shape, (s0, s1, s2), ok = t.shape, t.stride(), _here(t)
+        shape, (s0, s1, s2), ok = t.shape, t.stride(), t.get_device() == (_device() if dev is None else dev)
     except (AttributeError, ValueError):
         ok = False
     if not ok or (s2 != 1 and shape[2] != 1) or (dim is not None and shape[2] != dim):
@@ -676,8 +683,8 @@ def _vectors(t, what: str, dim: int | None = None):
     return lw_kv_tensor(t.data_ptr(), s0, s1), shape
 
 
-def _work(work):
-    return (_addr(work, "work"), work.numel() * work.element_size()) if work is not None and work.numel() else (None, 0)
+def _work(work, dev: int):
+    return (_addr(work, "work", dev), work.nbytes) if work is not None and work.numel() else (None, 0)
 
 
 class RopePlan:
@@ -699,18 +706,19 @@ def lw_rope_make(pairs: int, layout: int = LW_ROPE_HALVES, base: float = 10000.0
 
 def lw_rope(plan: RopePlan, x, y, batch: KvBatch | None = None, pos=None, stream=None) -> None:
     """y = x [n][heads][head_dim] turned by the rows' positions: those of the batch's tokens, or pos (int32 [n])."""
-    tx, shape = _vectors(x, "x")
-    ty, out = _vectors(y, "y")
+    dev = _device()
+    tx, shape = _vectors(x, "x", None, dev)
+    ty, out = _vectors(y, "y", None, dev)
     if shape != out:
         raise LwError(LW_E_ARG, "y must have the shape of x")
     n, heads, dim = shape
     pp = None
     if pos is not None:
-        pp = _typed(pos, "pos", _torch.int32, "int32 [tokens]")
+        pp = _typed(pos, "pos", _torch.int32, "int32 [tokens]", dev)
         if pos.numel() != n:
             raise LwError(LW_E_ARG, "pos must be int32 [tokens]")
     st = _L.lw_rope(plan.ref, None if batch is None else batch.ref, pp, n, heads, dim, C.byref(tx), _kv_type(x), C.byref(ty),
-                    _kv_type(y), _stream(stream))
+                    _kv_type(y), _queue(stream, dev))
     if st:
         _check(st)
 
@@ -722,9 +730,9 @@ def lw_kv_bounds_bytes(kv_heads: int, head_dim: int) -> int:
     return int(_L.lw_kv_bounds_bytes(kv_heads, head_dim))
 
 
-def _bounds(bounds, cache) -> int:
-    p = _addr(bounds, "bounds")
-    if bounds.numel() * bounds.element_size() < cache.bounds_bytes:
+def _bounds(bounds, cache, dev: int) -> int:
+    p = _addr(bounds, "bounds", dev)
+    if bounds.nbytes < cache.bounds_bytes:
         raise LwError(LW_E_ARG, "bounds must hold lw_kv_bounds_bytes for each page of the cache")
     return p
 
@@ -744,8 +752,8 @@ class KvSelection:
         self.ref = C.byref(self.desc)
 
 
-def _selected(t, what, sel, cache):
-    tensor, shape = _vectors(t, what, cache.head_dim)
+def _selected(t, what, sel, cache, dev: int):
+    tensor, shape = _vectors(t, what, cache.head_dim, dev)
     if shape[0] != sel.n or sel.kv_heads != cache.kv_heads:
         raise LwError(LW_E_ARG, f"the selection must have {what}'s rows and the cache's heads")
     return tensor, shape
@@ -753,7 +761,8 @@ def _selected(t, what, sel, cache):
 
 def lw_kv_bounds(cache: KvCache, batch: KvBatch, n_tokens: int, bounds, stream=None) -> None:
     """Bounds of the pages that the batch's n_tokens new tokens have filled."""
-    st = _L.lw_kv_bounds(cache.ref, batch.ref, n_tokens, _bounds(bounds, cache), _stream(stream))
+    dev = _device()
+    st = _L.lw_kv_bounds(cache.ref, batch.ref, n_tokens, _bounds(bounds, cache, dev), _queue(stream, dev))
     if st:
         _check(st)
 
@@ -765,9 +774,10 @@ def lw_kv_select_scratch_bytes(cache: KvCache, batch: KvBatch, n_tokens: int, q_
 def lw_kv_select(cache: KvCache, batch: KvBatch, q, bounds, sel: KvSelection, first: int = 1, last: int = 1, work=None,
                  stream=None) -> None:
     """Choose sel's pages for the rows of q [n][q_heads][head_dim]."""
-    tq, shape = _selected(q, "q", sel, cache)
-    st = _L.lw_kv_select(cache.ref, batch.ref, C.byref(tq), _kv_type(q), shape[1], _bounds(bounds, cache), first, last,
-                         sel.ref, *_work(work), _stream(stream))
+    dev = _device()
+    tq, shape = _selected(q, "q", sel, cache, dev)
+    st = _L.lw_kv_select(cache.ref, batch.ref, C.byref(tq), _kv_type(q), shape[1], _bounds(bounds, cache, dev), first, last,
+                         sel.ref, *_work(work, dev), _queue(stream, dev))
     if st:
         _check(st)
 
@@ -776,9 +786,9 @@ def lw_kv_attend_selected_scratch_bytes(cache: KvCache, sel: KvSelection, q_head
     return int(_L.lw_kv_attend_selected_scratch_bytes(cache.ref, sel.ref, q_heads))
 
 
-def _log_sums(lse, shape) -> int:
-    p = _typed(lse, "lse", _torch.float32, "fp32 [tokens][q_heads]")
-    if lse.dim() != 2 or lse.shape != shape[:2]:
+def _log_sums(lse, shape, dev: int) -> int:
+    p = _typed(lse, "lse", _torch.float32, "fp32 [tokens][q_heads]", dev)
+    if tuple(lse.shape) != (shape[0], shape[1]):
         raise LwError(LW_E_ARG, "lse must be fp32 [tokens][q_heads]")
     return p
 
@@ -786,22 +796,23 @@ def _log_sums(lse, shape) -> int:
 def lw_kv_attend_selected(cache: KvCache, sel: KvSelection, q, out, scale: float | None = None, lse=None, work=None,
                           stream=None) -> None:
     """out = attention of q [n][q_heads][head_dim] over the selected pages; scale None: head_dim ** -0.5."""
-    tq, shape = _selected(q, "q", sel, cache)
-    to, got = _vectors(out, "out", cache.head_dim)
+    dev = _device()
+    tq, shape = _selected(q, "q", sel, cache, dev)
+    to, got = _vectors(out, "out", cache.head_dim, dev)
     kind = _kv_type(q)
     if got != shape or _kv_type(out) != kind:
         raise LwError(LW_E_ARG, "out must have the shape and type of q")
     st = _L.lw_kv_attend_selected(cache.ref, sel.ref, C.byref(tq), C.byref(to), kind, shape[1],
                                   cache.head_dim ** -0.5 if scale is None else scale,
-                                  None if lse is None else _log_sums(lse, shape), *_work(work), _stream(stream))
+                                  None if lse is None else _log_sums(lse, shape, dev), *_work(work, dev), _queue(stream, dev))
     if st:
         _check(st)
 
 
 # ---------------------------------------------------------------- pages given up
 
-def _weights(t, what, cache, batch):
-    p, shape = _typed(t, what, _torch.float32, "fp32 [sequences][kv_heads][pages]"), t.shape
+def _weights(t, what, cache, batch, dev: int):
+    p, shape = _typed(t, what, _torch.float32, "fp32 [sequences][kv_heads][pages]", dev), t.shape
     if len(shape) != 3 or shape[0] != batch.n or shape[1] != cache.kv_heads:
         raise LwError(LW_E_ARG, f"{what} must be fp32 [sequences][kv_heads][pages]")
     return p, shape
@@ -810,16 +821,17 @@ def _weights(t, what, cache, batch):
 def lw_kv_weigh(cache: KvCache, batch: KvBatch, q, lse, weights, before=None, decay: float = 1.0,
                 scale: float | None = None, causal: bool = True, window: int = 0, stream=None) -> None:
     """weights [sequences][kv_heads][pages] = decay * before + what the rows of q gave to the pages' tokens."""
-    tq, shape = _vectors(q, "q", cache.head_dim)
-    pw, pages = _weights(weights, "weights", cache, batch)
+    dev = _device()
+    tq, shape = _vectors(q, "q", cache.head_dim, dev)
+    pw, pages = _weights(weights, "weights", cache, batch, dev)
     pb = None
     if before is not None:
-        pb, prior = _weights(before, "before", cache, batch)
+        pb, prior = _weights(before, "before", cache, batch, dev)
         if prior != pages:
             raise LwError(LW_E_ARG, "before must have the shape of weights")
     st = _L.lw_kv_weigh(cache.ref, batch.ref, shape[0], C.byref(tq), _kv_type(q), shape[1],
-                        cache.head_dim ** -0.5 if scale is None else scale, causal, window, _log_sums(lse, shape), pb, decay,
-                        pw, pages[2], _stream(stream))
+                        cache.head_dim ** -0.5 if scale is None else scale, causal, window, _log_sums(lse, shape, dev), pb, decay,
+                        pw, pages[2], _queue(stream, dev))
     if st:
         _check(st)
 
@@ -828,11 +840,13 @@ def lw_kv_evict(cache: KvCache, batch: KvBatch, weights, keep: int, table, gone,
                 stream=None) -> None:
     """Give up each sequence's pages of least weight until keep are left: table (batch's shape; may be its own) gets
     -1 for them, gone their numbers, count how many."""
-    pw, pages = _weights(weights, "weights", cache, batch)
-    pt, pg, pc = _typed(table, "table", _torch.int32, "int32"), _typed(gone, "gone", _torch.int32, "int32"), _typed(count, "count", _torch.int32, "int32")
+    dev = _device()
+    pw, pages = _weights(weights, "weights", cache, batch, dev)
+    pt, pg = _typed(table, "table", _torch.int32, "int32", dev), _typed(gone, "gone", _torch.int32, "int32", dev)
+    pc = _typed(count, "count", _torch.int32, "int32", dev)
     if table.shape != batch.shape or gone.shape != batch.shape or count.numel() != batch.n:
         raise LwError(LW_E_ARG, "table and gone must have the shape of the batch's table, count one number a sequence")
-    st = _L.lw_kv_evict(cache.ref, batch.ref, pw, pages[2], keep, first, last, pt, pg, pc, _stream(stream))
+    st = _L.lw_kv_evict(cache.ref, batch.ref, pw, pages[2], keep, first, last, pt, pg, pc, _queue(stream, dev))
     if st:
         _check(st)
 
