@@ -8,9 +8,9 @@
 // at most an eighth, on which the sine and cosine are their Taylor sums (x^9
 // and x^10: 2^-29 and 2^-31 of them are left out on pi/4).
 //
-// A wavefront has one row and some of its heads: the row's place in the batch
-// is looked up once, a lane's sines and cosines serve all the heads it goes
-// through.  Where the layout allows it a lane has eight elements (of the halves
+// A wavefront has one row and some of its heads, or a few rows where they have
+// few: a row's place in the batch is looked up once, a lane's sines and cosines
+// serve all the heads it goes through.  Where the layout allows it a lane has eight elements (of the halves
 // layout twice eight: both sides of eight pairs), else one pair or element.
 //
 // HBM bounds large calls: 22 thousand rows of 40 heads of 128, fp32 to bf16, 683 MB
@@ -32,6 +32,7 @@ struct Rope {
     const int32_t *pos;          // or null
     KvTensor x, y;
     int32_t heads, per;          // and a wavefront's
+    int32_t rows;                // a wavefront's (1, or as many as have their heads side by side)
     int32_t dim;
     lw_rope_plan plan;
 };
@@ -84,34 +85,52 @@ __device__ __forceinline__ float2 unit(uint64_t turns)
 
 // N elements a lane (8 or 1).  What a head vector is made of, in the order that
 // lanes take it: `turned` units of N pairs (HALVES) or N/2 of them (PAIRS), or
-// of one pair (N = 1), then the rest in units of N elements.
-template <int N, bool HALVES, class X, class Y>
+// of one pair (N = 1), then the rest in units of N elements.  SEVERAL: a.rows rows
+// a wavefront.
+template <int N, bool HALVES, bool SEVERAL, class X, class Y>
 __global__ __launch_bounds__(WAVES * 64) void k_rope(Rope a)
 {
     const int lane = threadIdx.x & 63;
-    const int64_t row = (int64_t)blockIdx.x * WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (row >= a.g.n_tokens) return;
-    int32_t pos;
-    if (a.pos) {
-        pos = a.pos[row];
-    } else {
-        const KvSeq q = kv_find(a.g, (int)row, [](int next, int) { return next; });
-        if (q.seq < 0 || row < q.row0 || row >= q.row0 + q.n_new) return;
-        pos = q.len - (q.row0 + q.n_new - (int)row);
-    }
     constexpr int PER = N == 1 ? 1 : HALVES ? N : N / 2;     // pairs of a unit
     constexpr bool TWO = N == 1 || HALVES;                   // a unit's sides lie apart
     const int pairs = a.plan.pairs, turned = pairs / PER, units = turned + (a.dim - 2 * pairs) / N;
-    const int h0 = blockIdx.y * a.per, h1 = min(h0 + a.per, a.heads);
-    const X *px = static_cast<const X *>(a.x.data) + row * a.x.token;
-    Y *py = static_cast<Y *>(a.y.data) + row * a.y.token;
     const int hop = units < 64 ? 64 / units : 1;             // heads side by side
+    const int side = units < 64 ? lane / units : 0, sub = SEVERAL ? side / a.heads : 0;
+    const int h0 = blockIdx.y * a.per + side - sub * a.heads, h1 = min((int)blockIdx.y * a.per + a.per, a.heads);
+    const int row0 = ((int)blockIdx.x * WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * (SEVERAL ? a.rows : 1);
+    if (row0 >= a.g.n_tokens) return;
+    const int row = row0 + sub;
+    bool mine = side < hop && (!SEVERAL || (sub < a.rows && row < a.g.n_tokens));
+    auto find = [&](int row) { return kv_find(a.g, row, [](int next, int) { return next; }); };
+    auto has = [&](const KvSeq &q) { return q.seq >= 0 && row >= q.row0 && row < q.row0 + q.n_new; };
+    int32_t pos = 0;
+    if (a.pos) {
+        if (!SEVERAL || mine) pos = a.pos[row];
+    } else if constexpr (SEVERAL) {
+        // a sequence at a time, from the first row on (mostly one)
+        bool found = false;
+        for (uint64_t left = __ballot(mine); left;) {
+            const int first = __builtin_amdgcn_readlane(row, __builtin_ctzll(left));
+            const KvSeq q = find(first);
+            const bool in = mine && !found && has(q);
+            if (in) pos = q.len - (q.row0 + q.n_new - row);
+            found = found || in;
+            left &= ~__ballot(in || row == first);
+        }
+        mine = found;
+    } else {
+        const KvSeq q = find(row);
+        if (!has(q)) return;
+        pos = q.len - (q.row0 + q.n_new - row);
+    }
+    const X *px = static_cast<const X *>(a.x.data) + (int64_t)row * a.x.token;
+    Y *py = static_cast<Y *>(a.y.data) + (int64_t)row * a.y.token;
     for (int u0 = 0; u0 < units; u0 += 64) {
-        const int side = units < 64 ? lane / units : 0, u = units < 64 ? lane - side * units : u0 + lane;
-        if (side >= hop || u >= units) continue;
+        const int u = units < 64 ? lane - side * units : u0 + lane;
+        if (!mine || u >= units) continue;
         if (u >= turned) {
             const int at = 2 * pairs + (u - turned) * N;
-            for (int h = h0 + side; h < h1; h += hop) {
+            for (int h = h0; h < h1; h += hop) {
                 const Vec<X, N> x = load<N>(px + h * a.x.head + at);
                 Vec<Y, N> y;
 #pragma unroll
@@ -128,7 +147,7 @@ __global__ __launch_bounds__(WAVES * 64) void k_rope(Rope a)
             cs[i].y *= a.plan.amplitude;
         }
         const int at = HALVES ? u * PER : 2 * u * PER, other = at + (HALVES ? pairs : 1);
-        for (int h = h0 + side; h < h1; h += hop) {
+        for (int h = h0; h < h1; h += hop) {
             const Vec<X, N> x = load<N>(px + h * a.x.head + at);
             Vec<Y, N> y;
             auto turn = [&](int i, X p, X q, Y &yp, Y &yq) {
@@ -152,18 +171,19 @@ __global__ __launch_bounds__(WAVES * 64) void k_rope(Rope a)
     }
 }
 
+template <int N, bool HALVES, class X, class Y>
+hipError_t launch(const Rope &a, dim3 grid, hipStream_t s)
+{
+    if (a.rows > 1) hipLaunchKernelGGL((k_rope<N, HALVES, true, X, Y>), grid, dim3(WAVES * 64), 0, s, a);
+    else hipLaunchKernelGGL((k_rope<N, HALVES, false, X, Y>), grid, dim3(WAVES * 64), 0, s, a);
+    return hipGetLastError();
+}
+
 template <class X, class Y>
 hipError_t launch(const Rope &a, dim3 grid, bool wide, hipStream_t s)
 {
-    const dim3 block(WAVES * 64);
-    if (a.plan.layout == LW_ROPE_HALVES) {
-        if (wide) hipLaunchKernelGGL((k_rope<8, true, X, Y>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((k_rope<1, true, X, Y>), grid, block, 0, s, a);
-    } else {
-        if (wide) hipLaunchKernelGGL((k_rope<8, false, X, Y>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((k_rope<1, false, X, Y>), grid, block, 0, s, a);
-    }
-    return hipGetLastError();
+    if (a.plan.layout == LW_ROPE_HALVES) return wide ? launch<8, true, X, Y>(a, grid, s) : launch<1, true, X, Y>(a, grid, s);
+    return wide ? launch<8, false, X, Y>(a, grid, s) : launch<1, false, X, Y>(a, grid, s);
 }
 
 template <class X>
@@ -192,15 +212,19 @@ hipError_t lw_launch_rope(const lw_rope_plan &plan, const KvGeom &g, const int32
     // one off alignment 130)
     const int unit = plan.layout == LW_ROPE_HALVES ? 8 : 4;  // pairs
     const bool wide = x.wide && y.wide && head_dim % 8 == 0 && plan.pairs % unit == 0;
-    const int64_t rows = (g.n_tokens + WAVES - 1) / WAVES;
     // Heads a wavefront: as many as leave the chip 4096 wavefronts (those 20000 rows
     // with eight each: 122 us), in whole turns of those it takes side by side (one
     // row, 40 heads of 128, eight side by side: 2.9 us and 3.1 with one a wavefront;
     // 128 rows 3.3 and 5.6; off alignment one side by side: 2.5 and 3.2 with eight).
     const int64_t units = wide ? plan.pairs / unit + (head_dim - 2 * plan.pairs) / 8 : head_dim - plan.pairs;
-    const int64_t hop = std::max<int64_t>(64 / units, 1), per = rows * WAVES * heads / 4096;
+    const int64_t hop = std::max<int64_t>(64 / units, 1), per = g.n_tokens * (int64_t)heads / 4096;
     a.per = (int)std::min<int64_t>(heads, std::max<int64_t>((per + hop - 1) / hop * hop, hop));
-    const dim3 grid((unsigned)rows, (unsigned)((heads + a.per - 1) / a.per));
+    // and rows, where they have fewer heads than that (20000 rows of one head of 128,
+    // fp32 to bf16, 4.7 us and 15.0 with one a wavefront; 100000 of two of 80 17.8 and
+    // 56, the rate of a copy)
+    a.rows = (int)std::max<int64_t>(hop / heads, 1);
+    const int64_t some = (int64_t)WAVES * a.rows;
+    const dim3 grid((unsigned)((g.n_tokens + some - 1) / some), (unsigned)((heads + a.per - 1) / a.per));
     if (x_dtype == LW_F16) return launch_x<_Float16>(a, y_dtype, grid, wide, s);
     if (x_dtype == LW_BF16) return launch_x<__bf16>(a, y_dtype, grid, wide, s);
     return launch_x<float>(a, y_dtype, grid, wide, s);

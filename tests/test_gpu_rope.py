@@ -132,6 +132,32 @@ def test_positions_of_a_batch(torch, dg, dim, pairs):
 
 
 @pytest.mark.parametrize("halves", [True, False], ids=["halves", "pairs"])
+@pytest.mark.parametrize("heads,dim,pairs", [(1, 128, 64), (2, 80, 40), (3, 64, 32), (1, 16, 8), (1, 2, 1), (5, 34, 3), (7, 64, 20)])
+def test_rows_of_few_heads(torch, dg, heads, dim, pairs, halves):
+    """Rows that share a wavefront: of one sequence, of several, of none, before the first sequence and behind the last."""
+    rng = np.random.default_rng(heads * dim)
+    news = [3, 0, 1, 1, 1, 0, 70, 2, 129, 1]
+    start = (5 + np.concatenate(([0], np.cumsum(news)))).tolist()
+    lens = [int(n + rng.integers(0, 5000)) for n in news]
+    rows = start[-1] + 9
+    pos = np.zeros(rows, np.int32)
+    for s, n in enumerate(news):
+        pos[start[s]:start[s + 1]] = lens[s] - n + np.arange(n)
+    plan = dg.lw_rope_make(pairs, layout=dg.LW_ROPE_HALVES if halves else dg.LW_ROPE_PAIRS)
+    x = tensor(torch, rows, heads, dim, "fp32", "dense", rng.standard_normal((rows, heads, dim)).astype(np.float32))
+    for given in (False, True):
+        y = tensor(torch, rows, heads, dim, "fp16", "fused")
+        if given:
+            dg.lw_rope(plan, x, y, pos=torch.from_numpy(pos).cuda())
+        else:
+            dg.lw_rope(plan, x, y, batch=batch(torch, dg, start, lens))
+        got, mine = host(y), slice(0, rows) if given else slice(start[0], start[-1])
+        check(got[mine], host(x)[mine], pos[mine], L.turns(pairs, 10000.0), halves, 1.0, "fp16")
+        if not given:
+            assert np.all(got[:start[0]] == 7) and np.all(got[start[-1]:] == 7)
+
+
+@pytest.mark.parametrize("halves", [True, False], ids=["halves", "pairs"])
 @pytest.mark.parametrize("dim,pairs", [(128, 64), (128, 24), (70, 33)])
 def test_in_place_and_back(torch, dg, dim, pairs, halves):
     rng = np.random.default_rng(9)
