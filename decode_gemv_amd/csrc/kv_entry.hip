@@ -338,16 +338,18 @@ struct Chunks {
     size_t result;               // bytes of one's
 };
 
-// Chunks that a row tile is wanted in, of `tiles`: those of two workgroups a CU,
-// of 256 tokens at least (two steps of each wavefront).  Heads of 256 have
-// registers for half as many wavefronts, and take one workgroup a CU and 1024
-// tokens: 31 rows on 4 heads and 1536 tokens, with their choice, 34.0 us and not
-// 36.5.
+// Chunks that a row tile is wanted in, of `tiles`: as many as two workgroups a CU
+// hold (heads of 256 have registers for one), of 256 tokens at least, two steps of
+// each wavefront.  One more than that, which leaves some CUs more workgroups than
+// others, where chunks of 2048 tokens outweigh it.  With the bounds and the choice,
+// rounded up, down and so: heads of 128, 480 workgroups of 1024 tokens 45.0, 40.2
+// and 40.2 us, 288 of 4096 65.8, 71.3 and 65.8; heads of 256, 26 of 2368 (with
+// chunks of 1024 at least) 37.6, 32.1 and 32.1, 144 of 4096 74.0, 77.7 and 74.0.
 int64_t wanted_chunks(const lw_kv_cache *c, int64_t tiles, int64_t span)
 {
-    const int64_t groups = c->head_dim == 256 ? 256 : 512, least = c->head_dim == 256 ? 1024 : 256;
-    const int64_t base = std::max<int64_t>(tiles * c->kv_heads, 1);
-    return std::min((groups + base - 1) / base, (span + least - 1) / least);
+    const int64_t groups = c->head_dim == 256 ? 256 : 512, base = std::max<int64_t>(tiles * c->kv_heads, 1);
+    return std::max(std::min(std::max<int64_t>(groups / base, 1), (span + 255) / 256),
+                    std::min((groups + base - 1) / base, span / 2048));
 }
 
 Chunks chunks_of(const lw_kv_cache *c, const lw_kv_selection *sel, int q_heads, size_t room)
