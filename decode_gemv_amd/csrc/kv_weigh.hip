@@ -34,12 +34,25 @@ __device__ __forceinline__ const KvWeigh &arguments()
     return *(const KvWeigh *)p;
 }
 
-// A row's log sum, as log2 and what its rounding leaves.
-__device__ __forceinline__ float2 log2_of(float l)
+// A row's log sum as log2, x, and what its rounding leaves of it, y: as a factor
+// 2^-y of the row's sums, or, from 2^16 on (FAR_SUM), as a number that each score
+// loses before the exponential.  y grows with x, by 2^-24 of it: far out the factor
+// leaves fp32's range (from 2^31 on) while what it belongs to is nothing or
+// infinite already, and their product would not be a number.  Scores that near such
+// a log sum are products with the fp32 logarithm of e, too, so that its own rest
+// (REST) is not for them: a score of l then weighs 1.
+constexpr float FAR_SUM = 0x1p16f;
+
+struct LogSum {
+    float x, rest, factor;       // rest 0, or factor 1
+};
+
+__device__ __forceinline__ LogSum log2_of(float l)
 {
     constexpr float L = 1.44269504088896341f, REST = (float)(1.44269504088896340736 - (double)L);
-    const float x = l * L;
-    return make_float2(x, fmaf(l, L, -x) + l * REST);
+    const float x = l * L, y = fmaf(l, L, -x);
+    const bool far = fabsf(x) >= FAR_SUM;
+    return {x, far ? y : 0.0f, far ? 1.0f : __builtin_amdgcn_exp2f(-(y + l * REST))};
 }
 
 // A lane's part of its row's query (PER words of eight elements), for matrix
@@ -242,7 +255,7 @@ struct Rows {
     Part<D, T> raw;
     h8 q[D / 32];
     float qs, qsum, log_sum;
-    float2 lse;
+    float most, left, factor;    // the log sum: what goes from raw scores, and from scores, and a factor of sums
     bool counts;
     Span seen;
 
@@ -261,8 +274,16 @@ struct Rows {
     __device__ __forceinline__ void make(float scale)
     {
         raw.make(qs, qsum, scale, [&](int j, h8 y) { q[j] = y; });
-        lse = log2_of(log_sum);
+        const LogSum lse = log2_of(log_sum);
         counts = counts && fabsf(lse.x) < __builtin_inff();
+        // (a far log sum goes from the raw scores, where a fused product takes it for
+        // nothing, but for what is left of it; raw scores lie within 2^44, and one that
+        // is past all of them goes as it is)
+        most = lse.x * __builtin_amdgcn_rcpf(qs);
+        const bool far = fabsf(lse.x) >= FAR_SUM && fabsf(most) < 0x1p60f;
+        left = far ? fmaf(-most, qs, lse.x) + lse.rest : lse.x;
+        most = far ? most : 0.0f;
+        factor = lse.factor;
     }
 
     // sum over the lane's tokens of t0 .. t0 + 31
@@ -284,8 +305,8 @@ struct Rows {
 #pragma unroll
             for (int i = 0; i < 4; i++) {
                 const float x = ROWS == 8 && second ? acc[1][i] : acc[u][i];
-                const float s = fmaf(x, half_lo(dm[i]), fmaf(half_lo(dm[i]), 8.0f, -half_hi(dm[i])) * qsum);
-                p[u][i] = __builtin_amdgcn_exp2f(fmaf(s, qs, -lse.x));
+                const float s = fmaf(x, half_lo(dm[i]), fmaf(fmaf(half_lo(dm[i]), 8.0f, -half_hi(dm[i])), qsum, -most));
+                p[u][i] = __builtin_amdgcn_exp2f(fmaf(s, qs, -left));
             }
         }
         if (!all) {
@@ -358,7 +379,7 @@ __global__ __launch_bounds__(NW * 64) void k_kv_weigh(KvWeigh args)
                     if (t0 < t.hi && t0 + 32 > t.lo) sum += r.sum(k[x], t0, t0 >= f.lo && t0 + 32 <= e.hi, mk, lane);
                     load(k[x], step + 2);
                     if (step + 1 & (1 << hops) - 1) continue;
-                    const float total = all_lanes(r.counts ? sum * __builtin_amdgcn_exp2f(-r.lse.y) : 0.0f);
+                    const float total = all_lanes(r.counts ? sum * r.factor : 0.0f);
                     mine = lane == step >> hops ? total : mine;
                     sum = 0.0f;
                 }
@@ -421,8 +442,9 @@ struct Kind<__bf16> {
 template <int D>
 struct Made {                          // a row tile
     uint4 q[D / 16][64];               // lane: row % 32, half the dimensions
-    float4 row[32];                    // sum of q, factor of the scores, log sum, 2^-what its rounding leaves (0: adds nothing)
-    int factors[2];                    // whether any of 16 rows' factors is not 1
+    float4 row[32];                    // sum of q, factor of the scores, log sum and its factor (0: adds nothing)
+    float rest[32];                    // and what the scores lose with it
+    int factors[2];                    // whether any of 16 rows' scores have a factor or lose something
 };
 
 // The lane, found anew where this stands (as arguments()).
@@ -596,12 +618,13 @@ __global__ __launch_bounds__(MANY<D> * 64) void k_kv_weigh_rows(KvWeigh args)
             }
 #pragma unroll
             for (int j = 0; j < PER; j++) o.q[quarter % 2 * PER + j][quarter / 2 * 32 + own] = raw.w[j];
-            const float2 lse = log2_of(log_sum);
+            const LogSum lse = log2_of(log_sum);
             const bool counts = 32 * coming + own < rows && fabsf(lse.x) < __builtin_inff();
-            if (quarter == 0)
-                o.row[own] = make_float4(sum, ldexpf(1.0f, min(max(by, -126), 127)), lse.x,
-                                         counts ? __builtin_amdgcn_exp2f(-lse.y) : 0.0f);
-            const int factors = __any(by != 0);
+            if (quarter == 0) {
+                o.row[own] = make_float4(sum, ldexpf(1.0f, min(max(by, -126), 127)), lse.x, counts ? lse.factor : 0.0f);
+                o.rest[own] = lse.rest;
+            }
+            const int factors = __any(by != 0 || (counts && fabsf(lse.x) >= FAR_SUM));
             if (lane == 0) o.factors[wave % 2] = factors;
         };
         auto next = [&] {
@@ -641,6 +664,9 @@ __global__ __launch_bounds__(MANY<D> * 64) void k_kv_weigh_rows(KvWeigh args)
                 } else {
 #pragma unroll
                     for (int x = 0; x < 16; x++) acc[x] = fmaf(fmaf(acc[x], dk[x], ck[x] * row.x), row.y, -row.z);
+                    const float rest = o[n].rest[lane_again() % 32];
+#pragma unroll
+                    for (int x = 0; x < 16; x++) acc[x] -= rest;
                 }
 #pragma unroll
                 for (int x = 0; x < 16; x++) acc[x] = __builtin_amdgcn_exp2f(acc[x]);

@@ -268,6 +268,63 @@ def test_log_sums_past_the_largest_power_of_two(torch, dg):
         assert not host(w).any()
 
 
+def rounded_logs(far):
+    """Eight log sums from `far` on, and what fp32 rounds off their products with the logarithm of e, of either sign."""
+    l = [np.float32(far)]
+    while len(l) < 8:
+        l.append(np.nextafter(l[-1], np.float32(np.inf)))
+    l, e = np.array(l), np.float32(1.44269504088896341)
+    rest = l.astype(np.float64) * float(e) - (l * e).astype(np.float64)
+    assert (rest > 0).any() and (rest < 0).any()
+    return l
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rows", [1, 40], ids=["few", "many"])
+@pytest.mark.parametrize("far", [7e4, 3e9, 1e10, 1e12, 1e20, 1e30])
+def test_log_sums_far_above_and_below_the_scores(torch, dg, rows, far, D):
+    """Ordinary scores are nothing beside the one, and past fp32 beside the other: 0 and infinity, no NaN; rows beside such
+    a one keep what they give."""
+    kv, group, P = 1, 8, 32
+    s = Setup(torch, dg, kv, D, P, [rows], [100], 3).fill()
+    q, w = queries(s, group, "bf16"), torch.zeros((1, kv, 4), device="cuda")
+    logs = torch.from_numpy(rounded_logs(far)).cuda().expand(rows, group).contiguous()
+    dg.lw_kv_weigh(s.cache, s.batch, q, logs, w)
+    assert np.array_equal(host(w), np.zeros((1, kv, 4)))
+    dg.lw_kv_weigh(s.cache, s.batch, q, -logs, w)
+    assert np.all(np.isposinf(host(w)[0, 0]))
+    out, lse = torch.empty_like(q), torch.empty((rows, group), device="cuda")
+    dg.lw_kv_attend(s.cache, s.batch, q, out, lse=lse)
+    lse[0, ::2] = logs[0, ::2]
+    dg.lw_kv_weigh(s.cache, s.batch, q, lse, w)
+    want, used, err = L.weigh(R.Cache(s.image, kv, D, P), s.table, s.start, s.lens, host(q), host(lse), D ** -0.5, True, 0, 4)
+    assert used.all() and np.all(np.abs(host(w) - want) <= err)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rows", [1, 40], ids=["few", "many"])
+@pytest.mark.parametrize("power", [17, 20, 24, 28])
+def test_log_sums_beside_scores_as_large(torch, dg, rows, power, D):
+    """Scores of 2^power, exactly, under log sums a step above and below: exp of the difference.  Off by an exponential's
+    last place, by 2^-25 of the difference (up to 2^5) for the logarithm of e in fp32, and by the additions (kv_long_ref.weigh)."""
+    kv, group, P = 1, 4, 32
+    s = Setup(torch, dg, kv, D, P, [rows], [100], 3).fill()
+    image = s.image.reshape(s.n_pages, kv, -1)
+    image[:, :, P * D:P * (D + 4)] = np.tile(np.array([0.0, -1.0], np.float16).view(np.uint8), P)          # keys of ones
+    s.pages.copy_(torch.from_numpy(s.image))
+    q = torch.zeros((rows, group, D), dtype=torch.bfloat16, device="cuda")
+    q[:, :, 5] = 2.0 ** power
+    one = np.float32(2.0 ** power)
+    logs = np.array([one, np.nextafter(one, np.float32(np.inf)), np.nextafter(one, np.float32(0)), one], np.float32)
+    w = torch.zeros((1, kv, 4), device="cuda")
+    dg.lw_kv_weigh(s.cache, s.batch, q, torch.from_numpy(logs).cuda().expand(rows, group).contiguous(), w, scale=1.0)
+    seen = np.arange(100 - rows + 1, 101)
+    tokens = np.array([np.clip(seen - P * j, 0, P).sum() for j in range(4)])
+    want = tokens * np.exp(2.0 ** power - logs.astype(np.float64)).sum()
+    chain = (rows * group + 16) * (P // 16 + 1) // 4 + 64
+    assert np.all(np.abs(host(w)[0, 0] - want) <= want * (chain * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -22))
+
+
 def test_refusals_of_the_binding(torch, dg):
     kv, D, P = 2, 64, 32
     s = Setup(torch, dg, kv, D, P, [3], [100], 3)
