@@ -47,6 +47,9 @@ struct LogSum {
     float x, rest, factor;       // rest 0, or factor 1
 };
 
+// Those of log sums up to 2^127 (the next number's is another); false for NaN.
+__device__ __forceinline__ bool counted(float x) { return fabsf(x) <= 1.44269504088896341f * 0x1p127f; }
+
 __device__ __forceinline__ LogSum log2_of(float l)
 {
     constexpr float L = 1.44269504088896341f, REST = (float)(1.44269504088896340736 - (double)L);
@@ -275,7 +278,7 @@ struct Rows {
     {
         raw.make(qs, qsum, scale, [&](int j, h8 y) { q[j] = y; });
         const LogSum lse = log2_of(log_sum);
-        counts = counts && fabsf(lse.x) < __builtin_inff();
+        counts = counts && counted(lse.x);
         // (a far log sum goes from the raw scores, where a fused product takes it for
         // nothing, but for what is left of it; raw scores lie within 2^44, and one that
         // is past all of them goes as it is)
@@ -619,7 +622,7 @@ __global__ __launch_bounds__(MANY<D> * 64) void k_kv_weigh_rows(KvWeigh args)
 #pragma unroll
             for (int j = 0; j < PER; j++) o.q[quarter % 2 * PER + j][quarter / 2 * 32 + own] = raw.w[j];
             const LogSum lse = log2_of(log_sum);
-            const bool counts = 32 * coming + own < rows && fabsf(lse.x) < __builtin_inff();
+            const bool counts = 32 * coming + own < rows && counted(lse.x);
             if (quarter == 0) {
                 o.row[own] = make_float4(sum, ldexpf(1.0f, min(max(by, -126), 127)), lse.x, counts ? lse.factor : 0.0f);
                 o.rest[own] = lse.rest;

@@ -325,6 +325,18 @@ def test_log_sums_beside_scores_as_large(torch, dg, rows, power, D):
     assert np.all(np.abs(host(w)[0, 0] - want) <= want * (chain * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -22))
 
 
+def test_log_sums_up_to_the_largest_power_of_two_count(torch, dg):
+    """2^127 is the last that does, on either side of zero; what lies past it adds nothing, also where its product with the
+    logarithm of e is still a number."""
+    past = float(np.nextafter(np.float32(2.0 ** 127), np.float32(np.inf)))
+    for rows in (1, 40):
+        s = Setup(torch, dg, 1, 64, 32, [rows], [100], 3).fill()
+        q, w = queries(s, 2, "bf16"), torch.zeros((1, 1, 4), device="cuda")
+        for value, want in ((2.0 ** 127, 0.0), (-2.0 ** 127, np.inf), (-past, 0.0), (past, 0.0), (-2.3e38, 0.0), (-3e38, 0.0)):
+            dg.lw_kv_weigh(s.cache, s.batch, q, torch.full((rows, 2), value, device="cuda"), w)
+            assert np.array_equal(host(w), np.full((1, 1, 4), want)), (rows, value)
+
+
 def test_refusals_of_the_binding(torch, dg):
     kv, D, P = 2, 64, 32
     s = Setup(torch, dg, kv, D, P, [3], [100], 3)
