@@ -43,6 +43,7 @@ extern "C" lw_status lw_rope_make(const lw_rope_opts *o, lw_rope_plan *plan)
             return n * std::log(o->original / (turns * (2 * 3.14159265358979323846))) / std::log(o->base);
         };
         lo = std::max(std::floor(at(o->high)), 0.0);
+        if (!std::isfinite(lo)) return lw_fail(LW_E_ARG, "original / (2 pi high) is past what 64 bits hold");
         hi = std::min(std::ceil(at(o->low)), 2.0 * n - 1);
         if (hi == lo) hi = lo + 0.001L;
     }

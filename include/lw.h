@@ -541,7 +541,8 @@ typedef struct {
     double base;               /* 1..2^64 (INDEX: above 1) */
     double factor;             /* 2^-64..2^64 (PLAIN: not looked at) */
     double original;           /* INDEX, TURNS: positive, at most 2^64 */
-    double low, high;          /* INDEX: positive; TURNS: low < high, low not negative; both at most 2^64 */
+    double low, high;          /* INDEX: positive, original / (2 pi high) a finite number; TURNS: low < high, low not
+                                  negative; both at most 2^64 */
 } lw_rope_opts;
 
 /* What lw_rope needs to know: plain data, to be kept and copied as one likes.

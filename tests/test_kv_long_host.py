@@ -52,6 +52,19 @@ def test_refuses_plans(kw):
     assert dg.lib().lw_rope_make(None, None) == dg.LW_E_ARG
 
 
+def test_refuses_plans_whose_turns_leave_64_bits():
+    """original / (2 pi high) overflows: there is no pair that turns `high` times.  An overflow with low only keeps every
+    pair on the ramp, which its last one ends."""
+    kw = dict(scaling=3, factor=4.0, original=2.0 ** 64)
+    for high in (1e-300, 5e-324):
+        for low in (1.0, 1e-300):
+            with pytest.raises(dg.LwError) as e:
+                dg.lw_rope_make(32, low=low, high=high, **kw)
+            assert e.value.status == dg.LW_E_ARG
+    fine = dg.lw_rope_make(32, low=1e-300, high=32.0, **kw).desc
+    assert list(fine.step) == list(dg.lw_rope_make(32, low=1e-200, high=32.0, **kw).desc.step)
+
+
 def test_sizes():
     assert dg.lw_kv_bounds_bytes(8, 128) == 8 * 260 and dg.lw_kv_bounds_bytes(1, 64) == 144
     for bad in ((0, 128), (1025, 128), (8, 96)):
