@@ -38,7 +38,8 @@ extern "C" lw_status lw_rope_make(const lw_rope_opts *o, lw_rope_plan *plan)
     if (o->scaling == LW_ROPE_BASE) base *= powl(factor, (R)n / (n - 1));
     if (o->scaling == LW_ROPE_INDEX) {
         // (at's arithmetic in 64 bits, as models' own programs have it: floor
-        // and ceil are to fall the same way)
+        // and ceil are to fall the same way; so are the ends, each kept on one
+        // side, also where that leaves hi below lo)
         auto at = [&](double turns) {
             return n * std::log(o->original / (turns * (2 * 3.14159265358979323846))) / std::log(o->base);
         };

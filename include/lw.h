@@ -524,10 +524,13 @@ typedef enum {
     LW_ROPE_PLAIN = 0,         /* f */
     LW_ROPE_LINEAR = 1,        /* f / factor */
     LW_ROPE_BASE = 2,          /* base factor^(pairs / (pairs - 1)) in the base's place (pairs >= 2) */
-    LW_ROPE_INDEX = 3,         /* f (1 - r + r / factor), r = (i - lo) / (hi - lo) within 0..1, lo = floor(at(high)) and
-                                  hi = ceil(at(low)) within 0..2 pairs - 1 (hi 0.001 more where they are equal), at(t) =
+    LW_ROPE_INDEX = 3,         /* f (1 - r + r / factor), r = (i - lo) / (hi - lo) within 0..1, lo = max(floor(at(high)), 0)
+                                  and hi = min(ceil(at(low)), 2 pairs - 1) (hi 0.001 more where they are equal), at(t) =
                                   pairs ln(original / (2 pi t)) / ln(base): the pairs that turn `high` times over the
-                                  original context keep their pace, those that turn `low` times take factor's */
+                                  original context keep their pace, those that turn `low` times take factor's.  (Each
+                                  end is kept on one side, as trained models have it: where all pairs turn more than
+                                  `high` times, or fewer than `low`, hi may lie below lo, and the ramp runs the other
+                                  way: with lo past 2 pairs - 1 all take factor's, with hi below 0 none does) */
     LW_ROPE_TURNS = 4          /* f (s + (1 - s) / factor), s = (original f / (2 pi) - low) / (high - low) within 0..1 */
 } lw_rope_scaling;
 

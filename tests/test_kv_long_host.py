@@ -65,6 +65,21 @@ def test_refuses_plans_whose_turns_leave_64_bits():
     assert list(fine.step) == list(dg.lw_rope_make(32, low=1e-200, high=32.0, **kw).desc.step)
 
 
+@pytest.mark.parametrize("pairs,kw,takes", [
+    # all pairs turn more than `high` times over the original context: lo = 10, hi = 13 kept to 7
+    (4, dict(base=10.0, factor=4.0, original=8192.0, low=1.0, high=4.0), 4.0),
+    (8, dict(base=10.0, factor=4.0, original=32768.0, low=1.0, high=32.0), 4.0),
+    # all turn fewer than `low` times: hi = -2, lo kept to 0
+    (32, dict(base=500000.0, factor=4.0, original=100.0, low=50.0, high=60.0), 1.0)])
+def test_plans_whose_ramp_runs_the_other_way(pairs, kw, takes):
+    """The ends that lw.h states, each kept on one side.  A step is a whole number of 2^-64 turns, off by half of one; `want`
+    is in 64 bits, off by a few 2^-53 of itself, the power by its exponent of up to 13 times that."""
+    got = dg.lw_rope_make(pairs, scaling=SCALINGS["index"], **kw).desc
+    for i in range(pairs):
+        want = kw["base"] ** (-i / pairs) / takes / (2 * np.pi)
+        assert abs(got.step[i] * 2.0 ** -64 - want) <= 2.0 ** -48 * want + 2.0 ** -65
+
+
 def test_sizes():
     assert dg.lw_kv_bounds_bytes(8, 128) == 8 * 260 and dg.lw_kv_bounds_bytes(1, 64) == 144
     for bad in ((0, 128), (1025, 128), (8, 96)):
