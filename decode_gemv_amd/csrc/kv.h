@@ -12,6 +12,28 @@
 // few steps past them fit 32 bits, chunks and pages divide it.
 constexpr int32_t KV_MOST_TOKENS = 0x7FFF0000;
 
+// A launch has fewer than 2^32 threads along a dimension of its grid.  Workgroups
+// that are numbered in one row, and may be more than that holds, go on in another
+// dimension after each 2^KV_FOLD (their number is b << KV_FOLD | a).
+constexpr int KV_FOLD = 20;
+
+struct KvFold {
+    unsigned a, b;
+};
+
+constexpr KvFold kv_fold(int64_t groups)
+{
+    const int64_t row = (int64_t)1 << KV_FOLD;
+    return groups <= row ? KvFold{(unsigned)groups, 1} : KvFold{(unsigned)row, (unsigned)((groups + row - 1) / row)};
+}
+
+// Whether that many workgroups of so many threads can be launched.
+constexpr bool kv_fold_fits(int64_t groups, int64_t threads)
+{
+    const KvFold f = kv_fold(groups);
+    return f.a * threads < (int64_t)1 << 32 && f.b < 1 << 16 && (int64_t)f.a * f.b >= groups;
+}
+
 // A cache and a batch as the kernels see them: passed by value, so every
 // field is uniform.
 struct KvGeom {

@@ -97,7 +97,8 @@ __global__ __launch_bounds__(WAVES * 64) void k_rope(Rope a)
     const int hop = units < 64 ? 64 / units : 1;             // heads side by side
     const int side = units < 64 ? lane / units : 0, sub = SEVERAL ? side / a.heads : 0;
     const int h0 = blockIdx.y * a.per + side - sub * a.heads, h1 = min((int)blockIdx.y * a.per + a.per, a.heads);
-    const int row0 = ((int)blockIdx.x * WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * (SEVERAL ? a.rows : 1);
+    const int group = (int)(blockIdx.z << KV_FOLD | blockIdx.x);
+    const int row0 = (group * WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * (SEVERAL ? a.rows : 1);
     if (row0 >= a.g.n_tokens) return;
     const int row = row0 + sub;
     bool mine = side < hop && (!SEVERAL || (sub < a.rows && row < a.g.n_tokens));
@@ -224,7 +225,9 @@ hipError_t lw_launch_rope(const lw_rope_plan &plan, const KvGeom &g, const int32
     // 56, the rate of a copy)
     a.rows = (int)std::max<int64_t>(hop / heads, 1);
     const int64_t some = (int64_t)WAVES * a.rows;
-    const dim3 grid((unsigned)((g.n_tokens + some - 1) / some), (unsigned)((heads + a.per - 1) / a.per));
+    static_assert(kv_fold_fits(((int64_t)1 << 26) / WAVES, WAVES * 64), "as many rows as lw_rope takes");
+    const KvFold f = kv_fold((g.n_tokens + some - 1) / some);
+    const dim3 grid(f.a, (unsigned)((heads + a.per - 1) / a.per), f.b);
     if (x_dtype == LW_F16) return launch_x<_Float16>(a, y_dtype, grid, wide, s);
     if (x_dtype == LW_BF16) return launch_x<__bf16>(a, y_dtype, grid, wide, s);
     return launch_x<float>(a, y_dtype, grid, wide, s);

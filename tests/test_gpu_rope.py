@@ -218,3 +218,20 @@ def test_refusals_of_the_binding(torch, dg):
     for kw in (dict(), dict(pos=pos[:2]), dict(pos=pos.long()), dict(pos=pos, batch=b)):
         with pytest.raises(dg.LwError):
             dg.lw_rope(plan, x, x.clone(), **kw)
+
+
+def test_as_many_rows_as_there_may_be(torch, dg):
+    """2^26 rows, a wavefront each: more threads than a launch takes along one dimension.  Every row is turned, once."""
+    n, dim = 1 << 26, 34
+    x = torch.empty((n, 1, dim), dtype=torch.float16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(1))
+    y, pos = x.clone(), torch.arange(n, dtype=torch.int32, device="cuda")
+    dg.lw_rope(dg.lw_rope_make(1), y, y, pos=pos)
+    assert torch.equal(y[:, :, 2:], x[:, :, 2:])
+    for i in range(0, n, 1 << 22):
+        a, b = (x[i:i + (1 << 22), 0, j].double() for j in (0, 1))
+        angle = pos[i:i + (1 << 22)].double()                # (the plan is off by 2^-65 turns a position: 2^-36 in all)
+        c, s = angle.cos(), angle.sin()
+        err = (a.abs() + b.abs()) * (2.0 ** -22 + 2.0 ** -23)
+        for j, want in ((0, a * c - b * s), (1, a * s + b * c)):
+            off = (y[i:i + (1 << 22), 0, j].double() - want).abs()
+            assert bool((off <= err + (want.abs() + err) * HALF["fp16"] + TINY["fp16"]).all()), (i, j)
