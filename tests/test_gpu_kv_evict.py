@@ -237,6 +237,25 @@ def test_the_longest_table(torch, dg):
     give_up(torch, dg, 1, 32, table, [n * 32], rng.random((1, 1, n)).astype(np.float32), n, 10000, 1, 2)
 
 
+def test_as_many_sequences_as_there_may_be(torch, dg):
+    """2^22 sequences of tables past 1024 pages: more threads than a launch takes along one dimension.  Pages without a
+    weight are equal: the first go."""
+    n, wide, keep = 1 << 22, 1025, 600
+    cache = dg.KvCache(torch.empty(wide * R.page_bytes(1, 64, 32), dtype=torch.uint8, device="cuda"), 1, 64, 32)
+    table = torch.arange(wide, dtype=torch.int32, device="cuda").repeat(n, 1)
+    used = torch.arange(n, dtype=torch.int32, device="cuda") % 1000 + 2
+    b = dg.KvBatch(torch.zeros(n + 1, dtype=torch.int32, device="cuda"), used * 32 - 5, table)
+    gone, count = torch.full_like(table, -9), torch.full((n,), -9, dtype=torch.int32, device="cuda")
+    dg.lw_kv_evict(cache, b, torch.empty((n, 1, 0), device="cuda"), keep, table, gone, count)
+    drop = (used - keep).clamp(min=0).minimum(used - 2)
+    assert torch.equal(count, drop)
+    j = torch.arange(wide, dtype=torch.int32, device="cuda")
+    for i in range(0, n, 1 << 18):
+        d = drop[i:i + (1 << 18), None]
+        assert torch.equal(table[i:i + (1 << 18)], torch.where((j >= 1) & (j <= d), -1, j))
+        assert torch.equal(gone[i:i + (1 << 18)], torch.where(j < d, j + 1, -1))
+
+
 def test_a_long_table_in_a_graph(torch, dg):
     """More shared memory than a kernel has without asking for it, asked for while a graph is captured."""
     n = 20000
