@@ -59,9 +59,9 @@ class Layer:
         start = torch.arange(0, (self.n_seqs + 1) * new, new, dtype=torch.int32, device="cuda")
         return dg.KvBatch(start, self.lens, self.table, max_len=self.longest)
 
-    def attend(self, q, out, kv, keep, get):
+    def attend(self, q, out, kv, keep, get, chosen):
         n = q.shape[0]
-        if not self.chosen or n > self.n_seqs:               # (the prompt: over all pages)
+        if not chosen:
             need = dg.lw_kv_attend_scratch_bytes(self.cache, kv, n, HEADS)
             dg.lw_kv_attend(self.cache, kv, q, out, work=get("work", need, dtype=torch.uint8) if need else None)
             return
@@ -74,11 +74,12 @@ class Layer:
         need = dg.lw_kv_attend_selected_scratch_bytes(self.cache, sel, HEADS)
         dg.lw_kv_attend_selected(self.cache, sel, q, out, work=get("work", need, dtype=torch.uint8) if need else None)
 
-    def forward(self, x, kv, keep):
-        """x [n][HIDDEN] fp16; lens already count these tokens.  keep: the step's buffers."""
-        n = x.shape[0]
+    def forward(self, x, kv, keep, step=False):
+        """x [n][HIDDEN] fp16; lens already count these tokens.  keep: the buffers.  step: new tokens, which attend over the
+        chosen pages; a piece of the prompt, also of one token a sequence, does over all."""
+        n, chosen = x.shape[0], step and self.chosen > 0
         get = lambda name, *shape, dtype=torch.float32: keep.setdefault(
-            (name, n), torch.empty(shape, dtype=dtype, device="cuda"))
+            (name, n, chosen), torch.empty(shape, dtype=dtype, device="cuda"))
         y = get("qkv", n, (HEADS + 2 * KV) * DIM)
         dg.lw_gemv(self.qkv, x, y, n)
         y = y.view(n, HEADS + 2 * KV, DIM)
@@ -88,7 +89,7 @@ class Layer:
         dg.lw_kv_append(self.cache, kv, k, v)
         dg.lw_kv_bounds(self.cache, kv, n, self.bounds)
         a = get("attended", n, HEADS, DIM, dtype=torch.float16)
-        self.attend(q, a, kv, keep, get)
+        self.attend(q, a, kv, keep, get, chosen)
         keep["q"], keep["a"] = q, a
         z = get("o", n, HIDDEN)
         dg.lw_gemv(self.o, a, z, n)
@@ -124,7 +125,7 @@ def main(argv=None):
     one, y = layer.batch(1), torch.empty_like(x)
 
     def step():
-        y.copy_(layer.forward(x, one, keep))
+        y.copy_(layer.forward(x, one, keep, step=True))
 
     layer.lens.add_(1)
     step()                                                   # (its buffers, and the kernels' first use)

@@ -377,6 +377,21 @@ def test_example_over_chosen_pages(torch, dg, args):
     assert cached_decode.main(args) < 1e-3
 
 
+@pytest.mark.parametrize("args", [["--prompt", "5", "--steps", "3", "--batch", "9", "--pages", "1"],
+                                  ["--prompt", "97", "--steps", "3", "--pages", "2"]], ids=["pieces", "the last piece"])
+def test_example_attends_over_all_pages_for_pieces_of_one_token(torch, dg, monkeypatch, args):
+    """Pieces of the prompt have as many rows as a step there, and are none: pages are chosen in the step alone, once as it
+    is and once as it is captured."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import cached_decode
+    calls, select = [], dg.lw_kv_select
+    monkeypatch.setattr(dg, "lw_kv_select", lambda *a, **kw: (calls.append(1), select(*a, **kw)))
+    assert cached_decode.main(args) < 1e-3
+    assert len(calls) == 2
+
+
 def test_bindings_refusals(torch, dg):
     kv, D, P = 2, 64, 32
     s = Setup(torch, dg, kv, D, P, [3], [100], 3)
