@@ -87,7 +87,8 @@ class Layer:
         dg.lw_rope(self.rope, y[:, :HEADS], q, batch=kv)
         dg.lw_rope(self.rope, k, k, batch=kv)
         dg.lw_kv_append(self.cache, kv, k, v)
-        dg.lw_kv_bounds(self.cache, kv, n, self.bounds)
+        if self.chosen:
+            dg.lw_kv_bounds(self.cache, kv, n, self.bounds)
         a = get("attended", n, HEADS, DIM, dtype=torch.float16)
         self.attend(q, a, kv, keep, get, chosen)
         keep["q"], keep["a"] = q, a

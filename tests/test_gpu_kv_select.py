@@ -392,6 +392,19 @@ def test_example_attends_over_all_pages_for_pieces_of_one_token(torch, dg, monke
     assert len(calls) == 2
 
 
+def test_example_makes_no_bounds_that_nothing_reads(torch, dg, monkeypatch):
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import cached_decode
+    calls, bounds = [], dg.lw_kv_bounds
+    monkeypatch.setattr(dg, "lw_kv_bounds", lambda *a, **kw: (calls.append(1), bounds(*a, **kw)))
+    assert cached_decode.main(["--prompt", "33", "--steps", "2"]) < 1e-3
+    assert not calls
+    assert cached_decode.main(["--prompt", "33", "--steps", "2", "--pages", "1"]) < 1e-3
+    assert len(calls) == 5 + 2                               # (pieces of 8 tokens, the step and its capture)
+
+
 def test_bindings_refusals(torch, dg):
     kv, D, P = 2, 64, 32
     s = Setup(torch, dg, kv, D, P, [3], [100], 3)
