@@ -536,11 +536,17 @@ class KvCache:
         n = pages.numel() * pages.element_size()
         if n % size:
             raise LwError(LW_E_ARG, f"pages must hold whole pages of {size} bytes")
-        self.pages, self.n_pages = pages, n // size
+        self.pages, self.n_pages, self.device = pages, n // size, pages.get_device()
         self.kv_heads, self.head_dim, self.page_tokens = kv_heads, head_dim, page_tokens
         self.bounds_bytes = self.n_pages * int(_L.lw_kv_bounds_bytes(kv_heads, head_dim))
         self.desc = lw_kv_cache(p, n // size, kv_heads, head_dim, page_tokens)
         self.ref = C.byref(self.desc)
+
+
+def _common(*tensors) -> int:
+    """The device of all of them, -1 if there is none."""
+    on = {t.get_device() for t in tensors}
+    return on.pop() if len(on) == 1 else -1
 
 
 class KvBatch:
@@ -556,7 +562,7 @@ class KvBatch:
         if start.numel() != n + 1 or table.dim() != 2 or table.shape[0] != n:
             raise LwError(LW_E_ARG, "start must hold one entry more than lens, table one row for each")
         self.start, self.lens, self.table = start, lens, table
-        self.n, self.shape = n, table.shape
+        self.n, self.shape, self.device = n, table.shape, _common(start, lens, table)
         self.desc = lw_kv_batch(n, ps, pl, pt, table.shape[1], max_len)
         self.ref = C.byref(self.desc)
 
@@ -683,6 +689,10 @@ def _vectors(t, what: str, dim: int | None = None, dev: int | None = None):
     return lw_kv_tensor(t.data_ptr(), s0, s1), shape
 
 
+def _elsewhere():
+    raise LwError(LW_E_ARG, "the cache, the batch and the selection must lie on the current device")
+
+
 def _work(work, dev: int):
     return (_addr(work, "work", dev), work.nbytes) if work is not None and work.numel() else (None, 0)
 
@@ -712,6 +722,8 @@ def lw_rope(plan: RopePlan, x, y, batch: KvBatch | None = None, pos=None, stream
     if shape != out:
         raise LwError(LW_E_ARG, "y must have the shape of x")
     n, heads, dim = shape
+    if batch is not None and batch.device != dev:
+        _elsewhere()
     pp = None
     if pos is not None:
         pp = _typed(pos, "pos", _torch.int32, "int32 [tokens]", dev)
@@ -747,7 +759,7 @@ class KvSelection:
         if start.numel() != n + 1 or table.dim() != 3 or table.shape[0] != n:
             raise LwError(LW_E_ARG, "start must hold one entry more than lens, table [kv_heads][pages] for each")
         self.start, self.lens, self.table = start, lens, table
-        self.n, self.kv_heads = n, table.shape[1]
+        self.n, self.kv_heads, self.device = n, table.shape[1], _device()
         self.desc = lw_kv_selection(n, ps, pl, pt, table.shape[2])
         self.ref = C.byref(self.desc)
 
@@ -762,6 +774,8 @@ def _selected(t, what, sel, cache, dev: int):
 def lw_kv_bounds(cache: KvCache, batch: KvBatch, n_tokens: int, bounds, stream=None) -> None:
     """Bounds of the pages that the batch's n_tokens new tokens have filled."""
     dev = _device()
+    if cache.device != dev or batch.device != dev:
+        _elsewhere()
     st = _L.lw_kv_bounds(cache.ref, batch.ref, n_tokens, _bounds(bounds, cache, dev), _queue(stream, dev))
     if st:
         _check(st)
@@ -775,6 +789,8 @@ def lw_kv_select(cache: KvCache, batch: KvBatch, q, bounds, sel: KvSelection, fi
                  stream=None) -> None:
     """Choose sel's pages for the rows of q [n][q_heads][head_dim]."""
     dev = _device()
+    if cache.device != dev or batch.device != dev or sel.device != dev:
+        _elsewhere()
     tq, shape = _selected(q, "q", sel, cache, dev)
     st = _L.lw_kv_select(cache.ref, batch.ref, C.byref(tq), _kv_type(q), shape[1], _bounds(bounds, cache, dev), first, last,
                          sel.ref, *_work(work, dev), _queue(stream, dev))
@@ -797,6 +813,8 @@ def lw_kv_attend_selected(cache: KvCache, sel: KvSelection, q, out, scale: float
                           stream=None) -> None:
     """out = attention of q [n][q_heads][head_dim] over the selected pages; scale None: head_dim ** -0.5."""
     dev = _device()
+    if cache.device != dev or sel.device != dev:
+        _elsewhere()
     tq, shape = _selected(q, "q", sel, cache, dev)
     to, got = _vectors(out, "out", cache.head_dim, dev)
     kind = _kv_type(q)
@@ -822,6 +840,8 @@ def lw_kv_weigh(cache: KvCache, batch: KvBatch, q, lse, weights, before=None, de
                 scale: float | None = None, causal: bool = True, window: int = 0, stream=None) -> None:
     """weights [sequences][kv_heads][pages] = decay * before + what the rows of q gave to the pages' tokens."""
     dev = _device()
+    if cache.device != dev or batch.device != dev:
+        _elsewhere()
     tq, shape = _vectors(q, "q", cache.head_dim, dev)
     pw, pages = _weights(weights, "weights", cache, batch, dev)
     pb = None
@@ -841,6 +861,8 @@ def lw_kv_evict(cache: KvCache, batch: KvBatch, weights, keep: int, table, gone,
     """Give up each sequence's pages of least weight until keep are left: table (batch's shape; may be its own) gets
     -1 for them, gone their numbers, count how many."""
     dev = _device()
+    if cache.device != dev or batch.device != dev:
+        _elsewhere()
     pw, pages = _weights(weights, "weights", cache, batch, dev)
     pt, pg = _typed(table, "table", _torch.int32, "int32", dev), _typed(gone, "gone", _torch.int32, "int32", dev)
     pc = _typed(count, "count", _torch.int32, "int32", dev)

@@ -321,3 +321,52 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
     for call in (lw._addr, lw._vectors):
         with pytest.raises(dg.LwError):
             call(None, "t")
+
+
+def test_caches_batches_and_selections_of_another_device_are_refused(monkeypatch):
+    """The tensors of a call may lie on the current device, and what they are used with on another: as above, without one."""
+    import torch
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0, raising=False)
+    mem = np.zeros(1 << 16, np.uint8)
+
+    class There:
+        is_cuda = True
+
+        def __init__(self, *shape, dtype=torch.float32, device=0):
+            self.shape, self.dtype, self.device = torch.Size(shape), dtype, device
+            self.nbytes = self.numel() * dtype.itemsize
+
+        numel = lambda self: int(np.prod(self.shape))
+        element_size = lambda self: self.dtype.itemsize
+        dim = lambda self: len(self.shape)
+        get_device = lambda self: self.device
+        is_contiguous = lambda self: True
+        data_ptr = lambda self: (mem.ctypes.data + 255) & ~255
+        stride = lambda self: tuple(int(np.prod(self.shape[i + 1:])) for i in range(len(self.shape)))
+
+    monkeypatch.setattr(lw, "_dptr", lambda t, what: C.c_void_p(t.data_ptr()))
+    i32 = lambda *shape, device=0: There(*shape, dtype=torch.int32, device=device)
+    cache = lambda device: dg.KvCache(There(4 * dg.lw_kv_page_bytes(2, 64, 32), dtype=torch.uint8, device=device), 2, 64, 32)
+    batch = lambda *on: dg.KvBatch(*(i32(*shape, device=d) for shape, d in zip(((2,), (1,), (1, 3)), on)))
+    here, sel = (cache(0), batch(0, 0, 0)), dg.KvSelection(i32(4), i32(3), i32(3, 2, 5))
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+    far = dg.KvSelection(i32(4, device=1), i32(3, device=1), i32(3, 2, 5, device=1))
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    q, lse, weights = There(3, 4, 64, dtype=torch.float16), There(3, 4), There(1, 2, 3)
+    bounds = There(4 * dg.lw_kv_bounds_bytes(2, 64), dtype=torch.uint8)
+    plan = dg.lw_rope_make(32)
+    for c, b, s in ((cache(1), here[1], sel), (here[0], batch(1, 1, 1), sel), (here[0], batch(0, 0, 1), sel),
+                    (here[0], batch(1, 0, 0), sel), (*here, far)):
+        calls = []
+        if s is sel:
+            calls += [lambda: dg.lw_kv_bounds(c, b, 3, bounds), lambda: dg.lw_kv_weigh(c, b, q, lse, weights),
+                      lambda: dg.lw_kv_evict(c, b, weights, 2, i32(1, 3), i32(1, 3), i32(1))]
+        if b is not here[1]:
+            calls.append(lambda: dg.lw_rope(plan, q, There(3, 4, 64, dtype=torch.float16), batch=b))
+        else:
+            calls.append(lambda: dg.lw_kv_attend_selected(c, s, q, There(3, 4, 64, dtype=torch.float16)))
+        for call in calls + [lambda: dg.lw_kv_select(c, b, q, bounds, s)]:
+            with pytest.raises(dg.LwError, match="the cache, the batch and the selection") as e:
+                call()
+            assert e.value.status == dg.LW_E_ARG
