@@ -1,7 +1,7 @@
 // kv_entry.hip -- the entry points of the 4-bit key/value cache and of the
-// rotary positions of what goes into it: argument checks and launches.  Everything the kernels assume of the host's numbers
-// is checked here; what lies in device memory (start, lens, table) the
-// kernels check themselves.
+// rotary positions of what goes into it: argument checks and launches.
+// Everything the kernels assume of the host's numbers is checked here; what lies
+// in device memory (start, lens, table) the kernels check themselves.
 #include <algorithm>
 #include <climits>
 #include <cmath>

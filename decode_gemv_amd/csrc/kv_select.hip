@@ -60,9 +60,12 @@ __device__ __forceinline__ void halve(float *x, bool upper)
 // lane takes one of them and D/4 of the dimensions (all of a key unit's, or of
 // two), in the units that kv_kword lays out: 1 KiB of the cache a load.  At the
 // end the 16 lanes of a unit share its channels out, and the wavefronts meet.
-// A page takes 4.2 us, most of it the latencies of the row's place, the table's
-// entry and the keys (8.5 with one wavefront, and every lane all channels); where
-// no page is full, as for most tokens, workgroups end after the first, 1.7 to 2.2.
+// A page takes 4.2 us (kernel trace), most of it the latencies of the row's place,
+// the table's entry and the keys (8.5 with one wavefront, and every lane all
+// channels); where no page is full, as for most tokens, workgroups end after the
+// first, 2.0 to 2.3.  Many pages at once are bound by those chains, too: 5 prompts
+// of 8192 tokens (640 pages of 64, 8 heads of 128, 24 MB) 24 us, 16 of them 70,
+// 1.1 TB/s (replays of a graph).
 template <int D>
 __global__ __launch_bounds__(BOUND_WAVES * 64) void k_kv_bounds(KvGeom g, uint8_t *bounds, int64_t bounds_bytes)
 {
@@ -353,9 +356,9 @@ __device__ __forceinline__ void score_tiles(const KvSelect &a, const Wanted &w, 
 
 // Keys into the workspace: where few rows have many pages, many workgroups share
 // a row's.  For 16 rows of 8 to 512 pages and 8 heads of 128 (7 MB of bounds) it
-// takes 6.5 us, for one row of 4096 (8.5 MB) 5.4, 1.6 TB/s: with one tile or two a
-// wavefront the chain of loads is what counts, from the row's place over the
-// entries to the bounds.
+// takes 6.6 us (kernel trace), for one row of 4096 (8.5 MB) 5.9, 1.4 TB/s: with one
+// tile or two a wavefront the chain of loads is what counts, from the row's place
+// over the entries to the bounds.
 template <int D, class T>
 __global__ __launch_bounds__(256) void k_kv_score(KvSelect a)
 {
@@ -372,10 +375,10 @@ __global__ __launch_bounds__(256) void k_kv_score(KvSelect a)
 }
 
 // The pages of a row and kv head.  THREADS a workgroup; the keys come from the
-// workspace where there is one.  With those it takes 5.4 us for up to 512 pages and
-// 9.2 for 4096: passes over the keys in LDS, for each a barrier or two and one
-// wavefront's search for the counter; with the scores of 80 pages of its own 8.2,
-// a third each for the row's place, the scores and the choice.
+// workspace where there is one.  With those it takes 6.0 us (kernel trace) for up to
+// 512 pages and 9.2 for 4096: passes over the keys in LDS, for each a barrier or two
+// and one wavefront's search for the counter; with the scores of 80 pages of its own
+// 8.3, a third each for the row's place, the scores and the choice.
 template <int D, class T, int THREADS>
 __global__ __launch_bounds__(THREADS) void k_kv_select(KvSelect a)
 {
@@ -450,8 +453,8 @@ __global__ __launch_bounds__(THREADS) void k_kv_select(KvSelect a)
 
 // A workgroup has a sequence: its heads' weights are added in fp64 (their order is
 // the heads', and what is rounded once to fp32 is compared as whole numbers).  94
-// pages of 8 heads take 3.6 us; 64 sequences of 4 to 4096 pages 11.3: the longest's
-// 131 KB of weights through one CU, then the passes over its keys.
+// pages of 8 heads take 3.8 us (kernel trace); 64 sequences of 4 to 4096 pages 11.4:
+// the longest's 131 KB of weights through one CU, then the passes over its keys.
 template <int THREADS>
 __global__ __launch_bounds__(THREADS) void k_kv_evict(KvEvict a)
 {
@@ -527,7 +530,10 @@ hipError_t with_types(int head_dim, int dtype, F f)
     return hipErrorInvalidValue;
 }
 
-// LDS of a workgroup that picks from n keys.
+// LDS of a workgroup that picks from n keys, which are as many as the table is wide:
+// what a row has is known on the device only.  A wide table of few pages costs
+// places on a CU: 128 rows of 80 pages take 20.5 us up to 4096 entries, 32.5 with
+// 32768; one row 8.1 either way (replays of a graph).
 size_t pick_bytes(int64_t n, int threads) { return (PICK_WORDS + 8 * (threads / 64) + (n + 3) / 4 * 4) * sizeof(uint32_t); }
 
 // A kernel's LDS beyond 64 KiB has to be asked for.

@@ -4,8 +4,8 @@
 // order of their positions and the row's own is the last, so that what a row
 // sees is one run of tokens from 0 on, without a mask.
 //
-// 16 rows of up to 2048 tokens, 32 heads on 8 of 128 (36 MB): 13.4 us, 2.7 TB/s, and
-// 4.0 to join the chunks.  A wavefront has only four steps of 32 tokens: the chain
+// 16 rows of up to 2048 tokens, 32 heads on 8 of 128 (36 MB): 13.7 us (kernel trace),
+// 2.6 TB/s, and 3.9 to join the chunks.  A wavefront has only four steps of 32 tokens: the chain
 // of loads before the first key (the selection, then its pages) takes 1.8 us, the
 // meeting of the wavefronts is another wait, and in between a step's unpacking
 // takes as long as its memory.  Sixteen wavefronts a workgroup, chunks half and

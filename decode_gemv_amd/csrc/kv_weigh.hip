@@ -11,13 +11,17 @@
 // Many (k_kv_weigh_rows): the keys stay in registers, unpacked once, and the
 // queries go past them, through LDS.
 //
-// Few rows are bound by HBM: one token on 131071, 64 heads on 8 of 128 (71 MB of
-// keys), 15.6 us, 4.6 TB/s; 16 sequences of 1 to 3 tokens on up to 8190, 32 heads
-// (37 MB), 12.2: four pages or five a wavefront, so that the chain of loads to the
-// first of them is half of that.  Many are bound by vector instructions: 1024 new
-// tokens of two sequences of 11 thousand, 32 heads on 8 of 128, 115 us, 0.74
-// PFLOP/s (16 by 16 products of operands in fp16 that every workgroup made took
-// 160).
+// (Times here and below are replays of a graph, one call after the other.)  Few
+// rows are bound by HBM: one token on 131071, 64 heads on 8 of 128 (71 MB of keys),
+// 17.5 us, 4.1 TB/s; 16 sequences of 1 to 3 tokens on up to 8190, 32 heads (37 MB),
+// 13.8: four pages or five a wavefront, so that the chain of loads to the first of
+// them is half of that.  Many are bound by vector instructions and matrix ones
+// after one another: 1024 new tokens of each of two sequences, 11 thousand tokens
+// in all, 32 heads on 8 of 128, 115 us, 0.74 PFLOP/s (16 by 16 products of operands
+// in fp16 that every workgroup made took 160).  Of the cycles in which a CU has
+// work there its SIMDs are at vector instructions for 77 % and at products for 38,
+// which do little beside each other; and a CU has work for four fifths of the time,
+// as units are 240 for 256 CUs and end apart.
 #include <algorithm>
 #include <type_traits>
 
@@ -409,10 +413,12 @@ __global__ __launch_bounds__(NW * 64) void k_kv_weigh(KvWeigh args)
 // The codes are unpacked once, into the queries' own type, which holds them
 // exactly, and their pairs are multiplied by the scale, so that a row needs no more
 // than the sum of its elements and a score is two fused products: vector
-// instructions are what bounds this, and matrix ones hardly go on beside them
+// instructions are most of the time, and matrix ones hardly go on beside them
 // (those of 32 by 32 more than those of 16 by 16: 128 cycles of them and 32 fused
 // products, four wavefronts a SIMD, take 81 ns a wavefront with the small ones and
-// 70 with the large, 58 without the products).
+// 70 with the large, 58 without the products).  Row tiles that see none of a unit's
+// tokens are left out where they lie before it (causal), and not where it is behind
+// their window: 1024 new tokens on 8192 take 90 us, in a window of 64 still 48.
 constexpr int TB = 32;
 
 typedef float f16x __attribute__((ext_vector_type(16)));
@@ -460,8 +466,7 @@ __device__ __forceinline__ int lane_again()
 
 // A wavefront's priority by how much it has done of what lies between barriers, in
 // quarters: those behind go first, as the last alone would leave its SIMD idle
-// between dependent instructions (122 us, and 128 as the hardware chooses, in one
-// run).
+// between dependent instructions (115 us, and 118 as the hardware chooses).
 __device__ __forceinline__ void give_way(int done)
 {
     if (done == 0) __builtin_amdgcn_s_setprio(3);
@@ -481,8 +486,8 @@ __device__ __forceinline__ Span span_at(const KvAttend &a, const KvSeq &q, int t
     return span_of(a, t, 0);
 }
 
-// Wavefronts of a workgroup (registers, LDS; heads of 128 with 16 122 us, with 12
-// 129, in one run).
+// Wavefronts of a workgroup (registers, LDS; heads of 128 with 16 115 us, with 12
+// 118.5).
 template <int D> constexpr int MANY = D == 256 ? 8 : 16;
 
 template <int D, class T>
@@ -715,13 +720,18 @@ hipError_t launch(const KvWeigh &b, hipStream_t s)
 {
     const KvGeom &g = b.a.g;
     const int64_t rows = (int64_t)g.n_tokens * b.a.group;
+    // By the average, which is all that the host knows.  It is dear for a batch of both
+    // kinds: 63 sequences with one token on 2000, 32 heads on 8 of 128, 16.7 us, one
+    // with 190 17.8 and with 500 30.5, alone; together the first are 254 us (the
+    // prompt's keys are read once for each 16 rows), with the second 112 (the tokens'
+    // rows fill an eighth of a tile of 32).
     if (rows <= 16 * (int64_t)g.n_seqs) {
-        // Four wavefronts a SIMD: one token on 131071, 64 heads on 8, 16.4 us, with two
-        // 17.3 and with eight 18.8; 16 sequences of up to 8190 14.2, 15.6 and 14.4.
+        // Four wavefronts a SIMD: one token on 131071, 64 heads on 8, 17.5 us, with two
+        // 18.6 and with eight 20.0; 16 sequences of up to 8190 13.8, 14.6 and 14.6.
         const dim3 grid(g.kv_heads, std::max(4096 / g.kv_heads / NW, 1));
         // Eight rows where no sequence has more, as far as the host can tell (the first
-        // of those calls with 16: 17.4 us; the second has sequences of 4 to 12 rows, of
-        // which 8 would read the keys twice: 13.3 us with 16).
+        // of those calls with 16: 18.6 us; the second has sequences of 4 to 12 rows, of
+        // which 8 read the keys twice: 14.7 us, and 13.8 with 16).
         if (rows <= 8 || (b.a.group <= 8 && g.n_tokens <= g.n_seqs))
             hipLaunchKernelGGL((k_kv_weigh<D, 8, T>), grid, dim3(NW * 64), 0, s, b);
         else

@@ -10,12 +10,13 @@
 //
 // A wavefront has one row and some of its heads, or a few rows where they have
 // few: a row's place in the batch is looked up once, a lane's sines and cosines
-// serve all the heads it goes through.  Where the layout allows it a lane has eight elements (of the halves
-// layout twice eight: both sides of eight pairs), else one pair or element.
+// serve all the heads it goes through.  Where the layout allows it a lane has
+// eight elements (of the halves layout twice eight: both sides of eight pairs),
+// else one pair or element.
 //
 // HBM bounds large calls: 22 thousand rows of 40 heads of 128, fp32 to bf16, 683 MB
-// in 130 us, 5.3 TB/s, as fast as a copy.  Small ones take 4.0 us, the latencies
-// of the row's place and its elements.
+// in 130 us, 5.3 TB/s, as fast as a copy.  Small ones take 4.0 us (kernel trace),
+// the latencies of the row's place and its elements.
 #include <algorithm>
 #include <string>
 
@@ -210,7 +211,9 @@ hipError_t lw_launch_rope(const lw_rope_plan &plan, const KvGeom &g, const int32
     a.plan = plan;
     // Eight elements a lane where every unit of eight is 16-byte aligned and lies
     // on one side of a pair (20000 rows of 40 heads of 128, fp32 to bf16, 116 us;
-    // one off alignment 130)
+    // one off alignment 130).  One is dearer in 16 bits, by the instructions: fp16 to
+    // fp16, 20000 rows of 40 heads of 128 with eight 82 us, 5.0 TB/s; of 66 with 33
+    // pairs 53, 4.0; of 80 with 20 94, 2.7; of 96 with 12 179, 1.7.
     const int unit = plan.layout == LW_ROPE_HALVES ? 8 : 4;  // pairs
     const bool wide = x.wide && y.wide && head_dim % 8 == 0 && plan.pairs % unit == 0;
     // Heads a wavefront: as many as leave the chip 4096 wavefronts (those 20000 rows

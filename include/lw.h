@@ -622,9 +622,10 @@ typedef struct {
 
 /* Choose the pages of sel->n_tokens new tokens (rows of q, [n][q_heads][D],
  * LW_F16 or LW_BF16).  A row at position p takes the page of p (last, absent
- * or not), and of its sequence's pages before that which are present: the
- * first `first`, the last `last`, and of the others those of the highest
- * scores, of equal ones that of the lowest position, until it has sel->pages.
+ * or not), and of its sequence's pages before that which are present: those
+ * of the first `first` places, those of the last `last`, and of the others
+ * those of the highest scores, of equal ones that of the lowest position,
+ * until it has sel->pages.
  * Pages before p's count as full: their bounds have to be there.
  *   first, last : not negative, first + last < sel->pages
  *   work        : device, 4-byte aligned, lw_kv_select_scratch_bytes bytes
@@ -686,9 +687,9 @@ lw_status lw_kv_weigh(const lw_kv_cache *cache, const lw_kv_batch *batch, int64_
                       const float *before, float decay, float *weights, int64_t stride, void *stream);
 
 /* Give up pages of every sequence (start is not looked at) until `keep` are
- * left: of those present that hold one of its lens[s] tokens, without the
- * first `first` and the last `last`, the ones of the lowest weight, of equal
- * ones that of the lowest position.  A page's weight is the sum of its heads',
+ * left: of those present that hold one of its lens[s] tokens, without those of
+ * the first `first` places and the last `last` (present or not), the ones of
+ * the lowest weight, of equal ones that of the lowest position.  A page's weight is the sum of its heads',
  * in 64 bits and in order, rounded to 32; NaN counts as the largest, and pages
  * j >= stride as the largest, too.  What cannot be spared stays, so that more
  * than keep may be left.
